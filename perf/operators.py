@@ -176,7 +176,7 @@ def prepare(case, seed):
         import mlp_step_gb300 as M
         need = {"ln_train": lambda: M.mlp_layernorm_workspace_bytes(T, case["d"]),
                 "lin_fwd": lambda: M.mlp_linear_workspace_bytes(T, case["k"], case["n"], dt),
-                "lin_bwd": lambda: M.mlp_linear_bwd_workspace_bytes(T, case["k"], case["n"], dt),
+                "lin_bwd": lambda: M.mlp_linear_bwd_workspace_bytes(T, case["n"], case["k"], dt),
                 "act_bwd": lambda: M.mlp_act_bwd_workspace_bytes(T, case["n"])}
         s["ws"] = torch.empty(need[op]() if op in need else 0, dtype=torch.uint8, device="cuda")
         s["act"] = {"none": M.MLP_ACT_NONE, "relu": M.MLP_ACT_RELU,
