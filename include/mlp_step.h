@@ -64,6 +64,11 @@ typedef int mlp_status;
 #define MLP_ACT_NONE 0
 #define MLP_ACT_RELU 1               /* [cap] "The minimum model"                    */
 #define MLP_ACT_LEAKY_RELU_SQ 2      /* [mk] "What Worked": (leaky_relu(u))^2        */
+#define MLP_ACT_GELU 3               /* u Phi(u), Phi the normal distribution; the
+                                        linear layers' activations (mlp_gemm and
+                                        mlp_create take NONE and RELU)               */
+#define MLP_ACT_GELU_TANH 4          /* u (1 + tanh(sqrt(2/pi)(u + 0.044715 u^3)))/2  */
+#define MLP_ACT_SILU 5               /* u / (1 + exp(-u))                            */
 
 #define MLP_PREC_FP32 0              /* fp32 operands, fp32 SIMT kernels             */
 #define MLP_PREC_BF16 1              /* bf16 operands, fp32 accumulation in tensor
@@ -392,6 +397,110 @@ mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float ep
                                 float* velocity, float* grads, void* params_bf16, float lr,
                                 float momentum, float* loss_out, void* workspace,
                                 size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- 8-bit checkpoints
+ * Saved activations in 33/32 byte per value.  32 consecutive values of a row
+ * (the last group of a row may be shorter) share one scale byte b; the stored
+ * int8 q stands for q 2^(b - 133).  With E = floor(log2(largest magnitude of
+ * the group)): b = E + 127, at least 7, and q = x 2^(133 - b) rounded to the
+ * nearest whole number (halves to even) and held to [-127, 127].  So a value
+ * is off by at most 2^(E - 7) (half a step; one step, 2^(E - 6), where it was
+ * held), under 1/64 of the group's largest magnitude.  A group that holds an
+ * infinity or NaN gets b = 255 and reads back as NaN.  The encoding is exact
+ * arithmetic, the same on every machine.
+ * x, out: [rows][ld] of dtype F32, BF16 or F16; q: int8 [rows][ldq];
+ * scale: bytes [rows][lds], mlp_ckpt8_scale_cols(cols) of them per row.  Any
+ * pitches >= the widths; rows that start on 16 bytes (q: 8) are fastest.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE (beyond 2^31 blocks of
+ * 1024 16-byte pieces). */
+#define MLP_CKPT8_GROUP 32
+int mlp_ckpt8_scale_cols(int cols);
+mlp_status mlp_ckpt8_encode(const void* x, int x_dtype, int rows, int cols, int ldx, int8_t* q,
+                            int ldq, uint8_t* scale, int lds, void* stream);
+mlp_status mlp_ckpt8_decode(const int8_t* q, int ldq, const uint8_t* scale, int lds, int rows,
+                            int cols, void* out, int out_dtype, int ldo, void* stream);
+
+/* ---------------------------------------------------------------- layer norm
+ * Per row of x [T][d]:  mu = mean_i x_i,  rho = 1 / sqrt(mean_i (x_i - mu)^2 + eps),
+ *   xh = (x - mu) rho,  y = xh gain + shift.
+ * x and y have the type dtype (F32, BF16 or F16), gain and shift are fp32 [d]
+ * (nullable: 1 and 0), mean_out and rstd_out fp32 [T] (nullable) receive mu
+ * and rho for the backward pass.  x_q and x_scale (both or neither) receive x
+ * as an 8-bit checkpoint, written in the same pass.  Statistics and
+ * arithmetic are fp32, the variance is taken about the mean.  1 <= d <= 65536.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
+mlp_status mlp_layernorm_fwd(const void* x, int dtype, int ldx, const float* gain,
+                             const float* shift, int T, int d, float eps, void* y, int ldy,
+                             float* mean_out, float* rstd_out, int8_t* x_q, int ldq,
+                             uint8_t* x_scale, int lds, void* stream);
+
+/* Backward: with g = dy gain,
+ *   dx = rho (g - mean_i(g_i) - xh mean_i(g_i xh_i)) + dres,
+ *   dgain = sum_t dy xh,  dshift = sum_t dy   (fp32 [d], overwritten).
+ * The forward's input is given either as it was (x) or as its 8-bit
+ * checkpoint (x_q, x_scale; x NULL), with the forward's mean and rstd either
+ * way.  dres (nullable, [T][ldr]) is the gradient that reaches x past the
+ * norm (the residual branch); dx may be dres itself.  Column sums run in a
+ * fixed order without atomics: results are the same in every run.  T == 0
+ * sets dgain and dshift to zero.  workspace: mlp_layernorm_workspace_bytes,
+ * written before it is read; calls that may overlap on the GPU (other
+ * streams, graphs in flight together) need workspaces of their own. */
+size_t mlp_layernorm_workspace_bytes(int T, int d);
+mlp_status mlp_layernorm_bwd(const void* dy, int dtype, int lddy, const void* x, int ldx,
+                             const int8_t* x_q, int ldq, const uint8_t* x_scale, int lds,
+                             const float* mean, const float* rstd, const float* gain,
+                             const void* dres, int ldr, int T, int d, void* dx, int lddx,
+                             float* dgain, float* dshift, void* workspace, size_t ws_bytes,
+                             void* stream);
+
+/* ---------------------------------------------------------------- linear layer
+ * u = x W + bias;  y = f(u) + residual, in one product whose epilogue keeps
+ * everything fp32 up to the one rounding of each output.
+ * x [T][d_in], W [d_in][d_out] of the operand type dtype (BF16 or F16: tcgen05
+ * kernels, fp32 accumulation; F32: fp32 FMA); bias fp32 [d_out] (nullable);
+ * act any MLP_ACT_* (slope: of LEAKY_RELU_SQ); residual (nullable) and y
+ * [T][d_out] of y_dtype, the operand type or F32; y may be residual itself.
+ * For the backward pass the pre-activations may be kept: u_out (nullable, the
+ * operand type) and / or u_q and u_scale (both or neither: an 8-bit
+ * checkpoint of the unrounded u).
+ * Pitches of x and W in 16-bit types are multiples of 8.  d_in >= 1.
+ * workspace: mlp_linear_workspace_bytes(...) bytes (0 for most shapes; NULL is
+ * then fine), with the same rule on overlapping calls as above.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
+size_t mlp_linear_workspace_bytes(int T, int d_in, int d_out, int dtype);
+mlp_status mlp_linear_fwd(const void* x, int ldx, const void* w, int ldw, int T, int d_in,
+                          int d_out, int dtype, const float* bias, int act, float slope,
+                          const void* residual, int ldr, void* y, int ldy, int y_dtype,
+                          void* u_out, int ldu, int8_t* u_q, int ldq, uint8_t* u_scale, int lds,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* Backward through a linear layer and the activation in front of it: with
+ * dy [T][d_out] the gradient of the layer's output, W [d_in][d_out] its weight
+ * and u [T][d_in] the pre-activations whose f(u) was its input,
+ *   du = (dy W^T) f'(u)  [T][d_in] of du_dtype (the operand type or F32),
+ *   dbias = sum_t du     (fp32 [d_in], nullable; from the unrounded du, in a
+ *                         fixed order: the bias gradient of the layer that
+ *                         made u),
+ *   a_out = f(u)         (nullable, the operand type: the left operand of this
+ *                         layer's weight gradient, dW = a^T dy, mlp_gemm).
+ * u is given in the operand type (u) or as an 8-bit checkpoint (u_q, u_scale;
+ * u NULL); with act NONE and no a_out it may be missing.  T == 0 sets dbias to
+ * zero.  Pitches of dy and W in 16-bit types are multiples of 8. */
+size_t mlp_linear_bwd_workspace_bytes(int T, int d_in, int d_out, int dtype);
+mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int T, int d_in,
+                          int d_out, int dtype, int act, float slope, const void* u, int ldu,
+                          const int8_t* u_q, int ldq, const uint8_t* u_scale, int lds, void* du,
+                          int lddu, int du_dtype, float* dbias, void* a_out, int lda,
+                          void* workspace, size_t ws_bytes, void* stream);
+
+/* The same without a product, for a layer whose own output has the
+ * activation: du = dy f'(u), dbias = sum_t du, a_out = f(u), all [T][n] of
+ * dtype F32, BF16 or F16. */
+size_t mlp_act_bwd_workspace_bytes(int T, int n);
+mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int act, float slope,
+                       const void* u, int ldu, const int8_t* u_q, int ldq,
+                       const uint8_t* u_scale, int lds, void* du, int lddu, float* dbias,
+                       void* a_out, int lda, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -16,7 +16,8 @@ import os
 
 __all__ = [
     "MlpError", "load", "lib_path",
-    "MLP_ACT_NONE", "MLP_ACT_RELU", "MLP_ACT_LEAKY_RELU_SQ",
+    "MLP_ACT_NONE", "MLP_ACT_RELU", "MLP_ACT_LEAKY_RELU_SQ", "MLP_ACT_GELU",
+    "MLP_ACT_GELU_TANH", "MLP_ACT_SILU", "MLP_CKPT8_GROUP",
     "MLP_PREC_FP32", "MLP_PREC_BF16", "MLP_PREC_FP16", "MLP_DTYPE_F32", "MLP_DTYPE_BF16",
     "MLP_DTYPE_U8", "MLP_DTYPE_F16", "MLP_ORDER_FAST", "MLP_ORDER_LINEAR",
 ]
@@ -32,6 +33,9 @@ MLP_ERR_NUMERIC = 6
 MLP_ACT_NONE = 0
 MLP_ACT_RELU = 1
 MLP_ACT_LEAKY_RELU_SQ = 2
+MLP_ACT_GELU = 3
+MLP_ACT_GELU_TANH = 4
+MLP_ACT_SILU = 5
 MLP_PREC_FP32 = 0
 MLP_PREC_BF16 = 1
 MLP_PREC_FP16 = 2
@@ -41,6 +45,7 @@ MLP_DTYPE_U8 = 2
 MLP_DTYPE_F16 = 3
 MLP_ORDER_FAST = 0
 MLP_ORDER_LINEAR = 1
+MLP_CKPT8_GROUP = 32
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmlp_step.so")
@@ -96,6 +101,23 @@ SIGNATURES = {
     "mlp_stack_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "mlp_stack_train_step": (_i, [_i, _i, _i, _i, _f, _f, _vp, _vp, _vp, _vp, _vp, _vp, _f, _f,
                                   _vp, _vp, _sz, _vp]),
+    "mlp_ckpt8_scale_cols": (_i, [_i]),
+    "mlp_ckpt8_encode": (_i, [_vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp]),
+    "mlp_ckpt8_decode": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _i, _i, _vp]),
+    "mlp_layernorm_fwd": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _f, _vp, _i, _vp, _vp, _vp, _i,
+                               _vp, _i, _vp]),
+    "mlp_layernorm_workspace_bytes": (_sz, [_i, _i]),
+    "mlp_layernorm_bwd": (_i, [_vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i,
+                               _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "mlp_linear_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "mlp_linear_fwd": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _i, _f, _vp, _i, _vp, _i, _i,
+                            _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _vp]),
+    "mlp_linear_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "mlp_linear_bwd": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i,
+                            _vp, _i, _i, _vp, _vp, _i, _vp, _sz, _vp]),
+    "mlp_act_bwd_workspace_bytes": (_sz, [_i, _i]),
+    "mlp_act_bwd": (_i, [_vp, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp,
+                         _vp, _i, _vp, _sz, _vp]),
 }
 
 
@@ -422,3 +444,211 @@ def mlp_stack_train_step(n_blocks, T, d, hidden, x0, target, params, velocity, g
                                        _ptr(params_bf16), lr, momentum, _ptr(loss_out),
                                        _ptr(workspace), wsb, _stream(stream)),
            "mlp_stack_train_step")
+
+
+# ------------------------------------------------------------------ feed-forward operators
+#
+# Matrices are 2-D CUDA tensors on the current device with unit stride along a
+# row; their row pitch is taken from stride(0), so column slices of wider
+# tensors are fine.  Outputs are given by the caller.  `ckpt` is an 8-bit
+# checkpoint: a pair (q, scale) of an int8 [rows, cols] and a uint8
+# [rows, mlp_ckpt8_scale_cols(cols)] matrix.
+
+def _on_device(t, what):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current CUDA device (got %s)" % (what, t.device))
+
+
+def _mat(t, what, rows, cols, dtype=None):
+    """(address, row pitch) of a [rows, cols] matrix; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must be [%d, %d] (got %s)" % (what, rows, cols, tuple(t.shape)))
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError("%s must be %s (got %s)" % (what, dtype, t.dtype))
+    _on_device(t, what)
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("%s: the values of a row must be adjacent (strides %s)"
+                         % (what, tuple(t.stride())))
+    # the pitch of a single row is never used; a whole number of 16-byte
+    # pieces keeps it acceptable for any width
+    return t.data_ptr(), t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+
+
+def _vec(t, what, n):
+    """Address of a contiguous fp32 vector of n values; None for None."""
+    import torch
+    if t is None:
+        return None
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be %d contiguous values (got %s)" % (what, n, tuple(t.shape)))
+    if t.dtype != torch.float32:
+        raise TypeError("%s must be float32 (got %s)" % (what, t.dtype))
+    _on_device(t, what)
+    return t.data_ptr()
+
+
+def _ckpt(ckpt, what, rows, cols):
+    """(q address, pitch, scale address, pitch) of an 8-bit checkpoint."""
+    import torch
+    if ckpt is None:
+        return None, 0, None, 0
+    q, scale = ckpt
+    groups = (cols + MLP_CKPT8_GROUP - 1) // MLP_CKPT8_GROUP
+    return (*_mat(q, what + " values", rows, cols, torch.int8),
+            *_mat(scale, what + " scales", rows, groups, torch.uint8))
+
+
+def _ws(t):
+    if t is None:
+        return None, 0
+    _on_device(t, "workspace")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _float_code(t):
+    code = _dtype_code(t)
+    if code == MLP_DTYPE_U8:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return code
+
+
+def _code_of(dtype):
+    import torch
+    code = {torch.float32: MLP_DTYPE_F32, torch.bfloat16: MLP_DTYPE_BF16,
+            torch.float16: MLP_DTYPE_F16}.get(dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % dtype)
+    return code
+
+
+def mlp_ckpt8_scale_cols(cols: int) -> int:
+    """Scale bytes per row of an 8-bit checkpoint of `cols` columns."""
+    return load().mlp_ckpt8_scale_cols(cols)
+
+
+def mlp_ckpt8_encode(x, q, scale, stream=None):
+    """x [rows, cols] (fp32, bf16 or fp16) into the 8-bit checkpoint (q, scale)."""
+    T, d = x.shape
+    xp, ldx = _mat(x, "x", T, d)
+    qp, ldq, sp, lds = _ckpt((q, scale), "checkpoint", T, d)
+    _check(load().mlp_ckpt8_encode(xp, _float_code(x), T, d, ldx, qp, ldq, sp, lds,
+                                   _stream(stream)), "mlp_ckpt8_encode")
+
+
+def mlp_ckpt8_decode(q, scale, out, stream=None):
+    """The values of the 8-bit checkpoint (q, scale) into out (fp32, bf16 or fp16)."""
+    T, d = out.shape
+    op, ldo = _mat(out, "out", T, d)
+    qp, ldq, sp, lds = _ckpt((q, scale), "checkpoint", T, d)
+    _check(load().mlp_ckpt8_decode(qp, ldq, sp, lds, T, d, op, _float_code(out), ldo,
+                                   _stream(stream)), "mlp_ckpt8_decode")
+
+
+def mlp_layernorm_fwd(x, y, gain=None, shift=None, mean=None, rstd=None, ckpt=None, eps=1e-5,
+                      stream=None):
+    """Layer norm of the rows of x into y (same dtype); mean, rstd: fp32 [T]
+    kept for the backward; ckpt: receives x in 8 bits."""
+    T, d = x.shape
+    xp, ldx = _mat(x, "x", T, d)
+    yp, ldy = _mat(y, "y", T, d, x.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, d)
+    _check(load().mlp_layernorm_fwd(xp, _float_code(x), ldx, _vec(gain, "gain", d),
+                                    _vec(shift, "shift", d), T, d, eps, yp, ldy,
+                                    _vec(mean, "mean", T), _vec(rstd, "rstd", T), qp, ldq, sp,
+                                    lds, _stream(stream)), "mlp_layernorm_fwd")
+
+
+def mlp_layernorm_workspace_bytes(T: int, d: int) -> int:
+    return load().mlp_layernorm_workspace_bytes(T, d)
+
+
+def mlp_layernorm_bwd(dy, mean, rstd, dx, dgain, dshift, workspace, x=None, ckpt=None, gain=None,
+                      dres=None, stream=None):
+    """Backward of mlp_layernorm_fwd from its input x or the 8-bit checkpoint
+    of it; dx (+ dres, the gradient past the norm), dgain and dshift fp32."""
+    T, d = dy.shape
+    dyp, lddy = _mat(dy, "dy", T, d)
+    xp, ldx = _mat(x, "x", T, d, dy.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, d)
+    rp, ldr = _mat(dres, "dres", T, d, dy.dtype)
+    dxp, lddx = _mat(dx, "dx", T, d, dy.dtype)
+    wp, wsb = _ws(workspace)
+    _check(load().mlp_layernorm_bwd(dyp, _float_code(dy), lddy, xp, ldx, qp, ldq, sp, lds,
+                                    _vec(mean, "mean", T), _vec(rstd, "rstd", T),
+                                    _vec(gain, "gain", d), rp, ldr, T, d, dxp, lddx,
+                                    _vec(dgain, "dgain", d), _vec(dshift, "dshift", d), wp, wsb,
+                                    _stream(stream)), "mlp_layernorm_bwd")
+
+
+def mlp_linear_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
+    """Workspace of mlp_linear_fwd (0 for most shapes); dtype: the operands' torch dtype."""
+    return load().mlp_linear_workspace_bytes(T, d_in, d_out, _code_of(dtype))
+
+
+def mlp_linear_fwd(x, w, y, bias=None, act=MLP_ACT_NONE, slope=0.5, residual=None, u=None,
+                   ckpt=None, workspace=None, stream=None):
+    """y = f(x w + bias) + residual; x [T, d_in], w [d_in, d_out]; y (and
+    residual) of x's dtype or fp32; u: receives the pre-activations, ckpt:
+    receives them in 8 bits."""
+    T, k = x.shape
+    n = w.shape[1]
+    xp, ldx = _mat(x, "x", T, k)
+    wp, ldw = _mat(w, "w", k, n, x.dtype)
+    yp, ldy = _mat(y, "y", T, n)
+    rp, ldr = _mat(residual, "residual", T, n, y.dtype)
+    up, ldu = _mat(u, "u", T, n, x.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n)
+    ws, wsb = _ws(workspace)
+    _check(load().mlp_linear_fwd(xp, ldx, wp, ldw, T, k, n, _float_code(x), _vec(bias, "bias", n),
+                                 act, slope, rp, ldr, yp, ldy, _float_code(y), up, ldu, qp, ldq,
+                                 sp, lds, ws, wsb, _stream(stream)), "mlp_linear_fwd")
+
+
+def mlp_linear_bwd_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
+    """Workspace of mlp_linear_bwd for w [d_in, d_out] and dy [T, d_out]."""
+    return load().mlp_linear_bwd_workspace_bytes(T, d_in, d_out, _code_of(dtype))
+
+
+def mlp_linear_bwd(dy, w, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, dbias=None, a=None,
+                   workspace=None, stream=None):
+    """du = (dy w^T) f'(u); dy [T, d_out], w [d_in, d_out], u [T, d_in] given
+    as it is or as an 8-bit checkpoint; dbias fp32 [d_in] receives the column
+    sums of du, a (dy's dtype) the activations f(u)."""
+    T, k = dy.shape
+    n = w.shape[0]
+    dyp, lddy = _mat(dy, "dy", T, k)
+    wp, ldw = _mat(w, "w", n, k, dy.dtype)
+    dup, lddu = _mat(du, "du", T, n)
+    up, ldu = _mat(u, "u", T, n, dy.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n)
+    ap, lda = _mat(a, "a", T, n, dy.dtype)
+    ws, wsb = _ws(workspace)
+    _check(load().mlp_linear_bwd(dyp, lddy, wp, ldw, T, n, k, _float_code(dy), act, slope, up, ldu,
+                                 qp, ldq, sp, lds, dup, lddu, _float_code(du),
+                                 _vec(dbias, "dbias", n), ap, lda, ws, wsb, _stream(stream)),
+           "mlp_linear_bwd")
+
+
+def mlp_act_bwd_workspace_bytes(T: int, n: int) -> int:
+    return load().mlp_act_bwd_workspace_bytes(T, n)
+
+
+def mlp_act_bwd(dy, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, dbias=None, a=None,
+                workspace=None, stream=None):
+    """du = dy f'(u) with the column sums and activations of mlp_linear_bwd,
+    without a product (a layer whose own output has the activation)."""
+    T, n = dy.shape
+    dyp, lddy = _mat(dy, "dy", T, n)
+    dup, lddu = _mat(du, "du", T, n, dy.dtype)
+    up, ldu = _mat(u, "u", T, n, dy.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n)
+    ap, lda = _mat(a, "a", T, n, dy.dtype)
+    ws, wsb = _ws(workspace)
+    _check(load().mlp_act_bwd(dyp, lddy, T, n, _float_code(dy), act, slope, up, ldu, qp, ldq, sp,
+                              lds, dup, lddu, _vec(dbias, "dbias", n), ap, lda, ws, wsb,
+                              _stream(stream)), "mlp_act_bwd")

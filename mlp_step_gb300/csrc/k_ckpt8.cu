@@ -1,0 +1,185 @@
+// 8-bit activation checkpoints (format: ckpt8.cuh): encode and decode of a
+// matrix.  Both are one pass over the data and bound by HBM: 2 + 33/32 bytes
+// per bf16 value either way.
+//
+// Work item = one 16-byte piece of a row (8 16-bit or 4 fp32 values), so a
+// group of 32 is 4 or 8 neighbouring lanes, every load and store of a warp is
+// one contiguous run, and the group's largest magnitude is two or three
+// shuffles.  A thread takes four items a block-width apart, all loads first:
+// with 64 bytes in flight per thread and full occupancy the loads cover the
+// latency without a staging pipeline.
+#include "ckpt8.cuh"
+#include "kernels.cuh"
+#include "rowvec.cuh"
+#include "trace.cuh"
+
+namespace mlp {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kItems = 4;  // per thread
+
+// Pieces of a row, padded to whole groups so that a group's lanes never
+// straddle two rows.
+template <typename T>
+__host__ __device__ constexpr int pieces_per_row(int cols) {
+  return (cols + kCkptGroup - 1) / kCkptGroup * (kCkptGroup / RowVec<T>::N);
+}
+
+// First row and piece of a block's items: one 64-bit division per block, the
+// items then divide a small offset.
+struct Span {
+  long long row0;
+  unsigned off0;
+};
+__device__ __forceinline__ Span block_span(int per_row) {
+  const long long base = (long long)blockIdx.x * (kThreads * kItems);
+  const long long r = base / per_row;
+  return {r, (unsigned)(base - r * per_row)};
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_encode_kernel(const T* __restrict__ x, long long rows, int cols, long long ldx,
+                        int8_t* __restrict__ q, long long ldq, uint8_t* __restrict__ scale,
+                        long long lds, int x_vec, int q_vec) {
+  constexpr int N = RowVec<T>::N;
+  constexpr int LANES = kCkptGroup / N;  // lanes of a group
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per_row = pieces_per_row<T>(cols);
+  const Span sp = block_span(per_row);
+  long long row[kItems];
+  int col[kItems];
+  uint4 raw[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const unsigned o = sp.off0 + k * kThreads + threadIdx.x;
+    const unsigned r = o / (unsigned)per_row;
+    row[k] = sp.row0 + r;
+    col[k] = (int)(o - r * per_row) * N;
+    raw[k] = load_piece(x + row[k] * ldx + col[k], row[k] < rows ? cols - col[k] : 0, x_vec);
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    float v[N];
+    unpack_piece<T>(raw[k], v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) amax = max(amax, abs_bits(v[j]));
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1)
+      amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const uint32_t b = ckpt8_byte(amax);
+    const float inv = ckpt8_inv_step(b);
+    uint32_t w[N / 4];
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j)
+      w[j] = b == kCkptNanByte
+                 ? 0u
+                 : ckpt8_pack4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv);
+    if (row[k] < rows && col[k] < cols) {
+      store_q<N>(q + row[k] * ldq + col[k], cols - col[k], q_vec, w);
+      if ((threadIdx.x & (LANES - 1)) == 0) scale[row[k] * lds + col[k] / kCkptGroup] = (uint8_t)b;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_decode_kernel(const int8_t* __restrict__ q, long long ldq,
+                        const uint8_t* __restrict__ scale, long long lds, long long rows, int cols,
+                        T* __restrict__ out, long long ldo, int q_vec, int o_vec) {
+  constexpr int N = RowVec<T>::N;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int per_row = pieces_per_row<T>(cols);
+  const Span sp = block_span(per_row);
+  long long row[kItems];
+  int col[kItems];
+  uint32_t w[kItems][N / 4], b[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const unsigned o = sp.off0 + k * kThreads + threadIdx.x;
+    const unsigned r = o / (unsigned)per_row;
+    row[k] = sp.row0 + r;
+    col[k] = (int)(o - r * per_row) * N;
+    const int n = row[k] < rows ? cols - col[k] : 0;
+    load_q<N>(q + row[k] * ldq + col[k], n, q_vec, w[k]);
+    b[k] = n > 0 ? scale[row[k] * lds + col[k] / kCkptGroup] : 0u;
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const float step = ckpt8_step(b[k]);
+    float v[N];
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) {
+      const uint32_t f = ckpt8_flip(w[k][j]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[4 * j + e] = ckpt8_value(f, e, step);
+    }
+    if (row[k] < rows) store_piece(out + row[k] * ldo + col[k], v, cols - col[k], o_vec);
+  }
+}
+
+// Rows of pitch ld (elements of size esz) keep pieces of `bytes` aligned?
+bool rows_aligned(const void* p, long long ld, int esz, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * esz % bytes == 0;
+}
+
+template <typename T>
+mlp_status encode_t(const T* x, long long rows, int cols, long long ldx, int8_t* q, long long ldq,
+                    uint8_t* scale, long long lds, cudaStream_t st) {
+  const long long items = rows * pieces_per_row<T>(cols);
+  const long long blocks = (items + kThreads * kItems - 1) / (kThreads * kItems);
+  if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
+  LaunchScope ls("ckpt8_encode", st, rows, cols, sizeof(T));
+  launch_k(ckpt8_encode_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, x, rows, cols,
+           ldx, q, ldq, scale, lds, (int)rows_aligned(x, ldx, sizeof(T), 16),
+           (int)rows_aligned(q, ldq, 1, RowVec<T>::N));
+  return launch_status();
+}
+
+template <typename T>
+mlp_status decode_t(const int8_t* q, long long ldq, const uint8_t* scale, long long lds,
+                    long long rows, int cols, T* out, long long ldo, cudaStream_t st) {
+  const long long items = rows * pieces_per_row<T>(cols);
+  const long long blocks = (items + kThreads * kItems - 1) / (kThreads * kItems);
+  if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
+  LaunchScope ls("ckpt8_decode", st, rows, cols, sizeof(T));
+  launch_k(ckpt8_decode_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, q, ldq, scale,
+           lds, rows, cols, out, ldo, (int)rows_aligned(q, ldq, 1, RowVec<T>::N),
+           (int)rows_aligned(out, ldo, sizeof(T), 16));
+  return launch_status();
+}
+
+}  // namespace
+
+mlp_status launch_ckpt8_encode(const void* x, int dtype, long long rows, int cols, long long ldx,
+                               int8_t* q, long long ldq, uint8_t* scale, long long lds,
+                               cudaStream_t st) {
+  switch (dtype) {
+    case MLP_DTYPE_BF16:
+      return encode_t(static_cast<const __nv_bfloat16*>(x), rows, cols, ldx, q, ldq, scale, lds, st);
+    case MLP_DTYPE_F16:
+      return encode_t(static_cast<const __half*>(x), rows, cols, ldx, q, ldq, scale, lds, st);
+    default:
+      return encode_t(static_cast<const float*>(x), rows, cols, ldx, q, ldq, scale, lds, st);
+  }
+}
+
+mlp_status launch_ckpt8_decode(const int8_t* q, long long ldq, const uint8_t* scale, long long lds,
+                               long long rows, int cols, void* out, int dtype, long long ldo,
+                               cudaStream_t st) {
+  switch (dtype) {
+    case MLP_DTYPE_BF16:
+      return decode_t(q, ldq, scale, lds, rows, cols, static_cast<__nv_bfloat16*>(out), ldo, st);
+    case MLP_DTYPE_F16:
+      return decode_t(q, ldq, scale, lds, rows, cols, static_cast<__half*>(out), ldo, st);
+    default:
+      return decode_t(q, ldq, scale, lds, rows, cols, static_cast<float*>(out), ldo, st);
+  }
+}
+
+}  // namespace mlp

@@ -1,0 +1,616 @@
+// Layer norm over the rows of a matrix, forward and backward.
+//   mu = mean_i x_i,  rho = 1 / sqrt(mean_i (x_i - mu)^2 + eps)
+//   xh = (x - mu) rho,  y = xh gain + shift
+//   g = dy gain,  dx = rho (g - mean(g) - xh mean(g xh)) + dres
+//   dgain = sum_t dy xh,  dshift = sum_t dy
+// All of it is bound by HBM (forward 4, backward 6 to 8 bytes per bf16 value),
+// so a row is read once and stays in registers between its reductions: the
+// variance is taken about the mean that was just found (two passes over
+// registers), not as a difference of moments, which would cancel for rows
+// whose mean is large against their spread.  Everything between load and
+// store is fp32.
+//
+// A row is held by WPR warps, 16 values per thread (two 16-byte pieces in 16
+// bits, four in fp32), piece i at column (i * 32 WPR + thread) * N: every load
+// of a warp is one contiguous run and a group of 32 values for the 8-bit form
+// is 4 (8) neighbouring lanes.  Blocks walk over rows with a grid stride; the
+// next row's loads are issued before this row's reductions.
+#include "ckpt8.cuh"
+#include "kernels.cuh"
+#include "rowvec.cuh"
+#include "trace.cuh"
+
+namespace mlp {
+
+namespace {
+
+constexpr int kPerThread = 16;        // values of a row per thread
+constexpr int kHeldWidth = 16 * 512;  // widest row held by one block's registers
+constexpr int kLoopThreads = 512;
+
+// Threads of the blocks that hold rows with WPR warps each.
+template <int WPR>
+struct HeldBlock {
+  static constexpr int ROWS = WPR >= 8 ? 1 : 8 / WPR;  // rows at a time
+  static constexpr int THREADS = 32 * WPR * ROWS;
+};
+
+// Waits for the warps that share a row (the whole block where it holds one).
+template <int WPR>
+__device__ __forceinline__ void row_barrier(int slot) {
+  if constexpr (WPR == 1) __syncwarp();
+  else if constexpr (WPR >= 8) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(slot + 1), "r"(32 * WPR) : "memory");
+}
+
+// Sums of NV values over the row's threads, the same in each and in a fixed
+// order.  `part`: NV * WPR floats of the row's slot, of which callers use two
+// in turn so that one barrier a call is enough.
+template <int WPR, int NV>
+__device__ __forceinline__ void row_sums(float (&v)[NV], float* part, int slot, int warp_in_row) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) part[i * WPR + warp_in_row] = v[i];
+    row_barrier<WPR>(slot);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float s = part[i * WPR];
+#pragma unroll
+      for (int w = 1; w < WPR; ++w) s += part[i * WPR + w];
+      v[i] = s;
+    }
+  }
+}
+
+// N parameter values (fp32) from column c, `fill` past n values or without a vector.
+template <int N>
+__device__ __forceinline__ void load_param(const float* p, int c, int n, bool vec, float fill,
+                                           float (&v)[N]) {
+  if (p && vec && n >= N) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(p + c + j));
+      v[j] = f.x;
+      v[j + 1] = f.y;
+      v[j + 2] = f.z;
+      v[j + 3] = f.w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = p && j < n ? __ldg(p + c + j) : fill;
+}
+
+// The 8-bit form of a piece at column c of a row (its group's lanes together).
+template <typename T>
+__device__ __forceinline__ void store_ckpt(const float (&v)[RowVec<T>::N], int8_t* qrow,
+                                           uint8_t* srow, int c, int n, bool vec) {
+  constexpr int N = RowVec<T>::N, LANES = kCkptGroup / N;
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) amax = max(amax, abs_bits(v[j]));
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1)
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const uint32_t b = ckpt8_byte(amax);
+  const float inv = ckpt8_inv_step(b);
+  uint32_t w[N / 4];
+#pragma unroll
+  for (int j = 0; j < N / 4; ++j)
+    w[j] = b == kCkptNanByte
+               ? 0u
+               : ckpt8_pack4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv);
+  if (n > 0) {
+    store_q<N>(qrow + c, n, vec, w);
+    if ((threadIdx.x & (LANES - 1)) == 0) srow[c / kCkptGroup] = (uint8_t)b;
+  }
+}
+
+// ------------------------------------------------------------ forward
+
+template <typename T, int WPR>
+__global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_fwd_kernel(const LayerNormFwd p) {
+  constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
+  __shared__ float part[2][ROWS][WPR];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int slot = threadIdx.x / (32 * WPR), t = threadIdx.x % (32 * WPR);
+  const long long stride = (long long)gridDim.x * ROWS;
+  long long row = (long long)blockIdx.x * ROWS + slot;
+  const float inv_d = 1.f / (float)p.d;
+  const T* x = static_cast<const T*>(p.x);
+  uint4 raw[NV];
+  auto load = [&](long long r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + t) * N;
+      raw[i] = load_piece(x + r * p.ldx + c, r < p.T ? p.d - c : 0, p.x_vec);
+    }
+  };
+  load(row);
+  for (; row < p.T; row += stride) {  // uniform over the warps that share a row
+    float v[NV][N];
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      unpack_piece<T>(raw[i], v[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[0] += v[i][j];
+    }
+    load(row + stride);
+    row_sums<WPR>(s, part[0][slot], slot, t >> 5);
+    const float mu = s[0] * inv_d;
+    s[0] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int n = p.d - (i * 32 * WPR + t) * N;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float c = j < n ? v[i][j] - mu : 0.f;
+        s[0] = fmaf(c, c, s[0]);
+      }
+    }
+    row_sums<WPR>(s, part[1][slot], slot, t >> 5);
+    const float rho = 1.f / sqrtf(s[0] * inv_d + p.eps);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = rho;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + t) * N;
+      const int n = p.d - c;
+      if (p.q)
+        store_ckpt<T>(v[i], p.q + row * p.ldq, p.scale + row * p.lds, c, n, p.q_vec);
+      float a[N], b[N];
+      load_param<N>(p.gain, c, n, p.p_vec, 1.f, a);
+      load_param<N>(p.shift, c, n, p.p_vec, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i][j] = fmaf((v[i][j] - mu) * rho, a[j], b[j]);
+      store_piece(static_cast<T*>(p.y) + row * p.ldy + c, v[i], n, p.y_vec);
+    }
+  }
+}
+
+// Rows wider than the registers of a block: one block per row, which reads the
+// row three times (the second and third mostly from L1 and L2).
+template <typename T>
+__global__ void __launch_bounds__(kLoopThreads) ln_fwd_wide_kernel(const LayerNormFwd p) {
+  constexpr int N = RowVec<T>::N, WPR = kLoopThreads / 32;
+  __shared__ float part[2][WPR];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t = threadIdx.x;
+  const float inv_d = 1.f / (float)p.d;
+  // whole warps walk together past the row's end, so that group shuffles are full
+  const int end = (p.d + 32 * N - 1) / (32 * N) * (32 * N);
+  for (long long row = blockIdx.x; row < p.T; row += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + row * p.ldx;
+    float s[1] = {0.f};
+    for (int c = t * N; c < p.d; c += kLoopThreads * N) {
+      float v[N];
+      unpack_piece<T>(load_piece(x + c, p.d - c, p.x_vec), v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[0] += v[j];
+    }
+    row_sums<WPR>(s, part[0], 0, t >> 5);
+    const float mu = s[0] * inv_d;
+    s[0] = 0.f;
+    for (int c = t * N; c < p.d; c += kLoopThreads * N) {
+      float v[N];
+      unpack_piece<T>(load_piece(x + c, p.d - c, p.x_vec), v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const float e = c + j < p.d ? v[j] - mu : 0.f;
+        s[0] = fmaf(e, e, s[0]);
+      }
+    }
+    row_sums<WPR>(s, part[1], 0, t >> 5);
+    const float rho = 1.f / sqrtf(s[0] * inv_d + p.eps);
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mu;
+      if (p.rstd) p.rstd[row] = rho;
+    }
+    for (int c = t * N; c < end; c += kLoopThreads * N) {
+      const int n = p.d - c;
+      float v[N], a[N], b[N];
+      unpack_piece<T>(load_piece(x + c, n, p.x_vec), v);
+      if (p.q) store_ckpt<T>(v, p.q + row * p.ldq, p.scale + row * p.lds, c, n, p.q_vec);
+      load_param<N>(p.gain, c, n, p.p_vec, 1.f, a);
+      load_param<N>(p.shift, c, n, p.p_vec, 0.f, b);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = fmaf((v[j] - mu) * rho, a[j], b[j]);
+      store_piece(static_cast<T*>(p.y) + row * p.ldy + c, v, n, p.y_vec);
+    }
+  }
+}
+
+// ------------------------------------------------------------ backward
+
+// A piece of the forward's input: its raw 16 bytes, or the 8-bit words and the
+// group's scale byte.
+template <typename T, bool CK>
+struct XPiece {
+  static constexpr int N = RowVec<T>::N;
+  uint4 raw;
+  uint32_t w[N / 4], b;
+  __device__ __forceinline__ void load(const LayerNormBwd& p, long long row, int c, int n) {
+    if constexpr (CK) {
+      load_q<N>(p.q + row * p.ldq + c, n, p.q_vec, w);
+      b = n > 0 ? p.scale[row * p.lds + c / kCkptGroup] : 0u;
+    } else {
+      raw = load_piece(static_cast<const T*>(p.x) + row * p.ldx + c, n, p.x_vec);
+    }
+  }
+  __device__ __forceinline__ void values(float (&v)[N]) const {
+    if constexpr (CK) {
+      const float step = ckpt8_step(b);
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const uint32_t f = ckpt8_flip(w[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * k + e] = ckpt8_value(f, e, step);
+      }
+    } else {
+      unpack_piece<T>(raw, v);
+    }
+  }
+};
+
+// Per row: s1 = sum g, s2 = sum g xh, then dx; the sums of dy xh and dy over
+// the block's rows stay in registers (each thread always has the same
+// columns), are added over the block's row slots in order at the end, and
+// leave as one row of partial sums per block: no atomics, so the gradients
+// are the same in every run.
+template <typename T, int WPR, bool CK>
+__global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_bwd_kernel(const LayerNormBwd p) {
+  constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
+  __shared__ float part[2][ROWS][2 * WPR];
+  extern __shared__ float sums[];  // ROWS > 1: one slot's values at a time
+  pdl_wait();
+  pdl_launch_dependents();
+  const int slot = threadIdx.x / (32 * WPR), t = threadIdx.x % (32 * WPR);
+  const long long stride = (long long)gridDim.x * ROWS;
+  long long row = (long long)blockIdx.x * ROWS + slot;
+  const float inv_d = 1.f / (float)p.d;
+  const T* dy = static_cast<const T*>(p.dy);
+  float gain[NV][N], dg[NV][N], ds[NV][N];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * 32 * WPR + t) * N;
+    load_param<N>(p.gain, c, p.d - c, p.p_vec, 1.f, gain[i]);
+#pragma unroll
+    for (int j = 0; j < N; ++j) dg[i][j] = ds[i][j] = 0.f;
+  }
+  uint4 rdy[NV];
+  XPiece<T, CK> rx[NV];
+  float mu_n = 0.f, rho_n = 0.f;
+  auto load = [&](long long r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + t) * N;
+      const int n = r < p.T ? p.d - c : 0;
+      rdy[i] = load_piece(dy + r * p.lddy + c, n, p.dy_vec);
+      rx[i].load(p, r, c, n);
+    }
+    if (r < p.T) {
+      mu_n = p.mean[r];
+      rho_n = p.rstd[r];
+    }
+  };
+  load(row);
+  int turn = 0;
+  for (; row < p.T; row += stride, turn ^= 1) {
+    const float mu = mu_n, rho = rho_n;
+    float g[NV][N], xh[NV][N];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int n = p.d - (i * 32 * WPR + t) * N;
+      unpack_piece<T>(rdy[i], g[i]);
+      rx[i].values(xh[i]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        // past the row's end xh is set to 0 (dy reads as 0 there, but 0 times
+        // a mean or scale that is not finite would not be)
+        xh[i][j] = j < n ? (xh[i][j] - mu) * rho : 0.f;
+        dg[i][j] = fmaf(g[i][j], xh[i][j], dg[i][j]);
+        ds[i][j] += g[i][j];
+        g[i][j] *= gain[i][j];
+        s[0] += g[i][j];
+        s[1] = fmaf(g[i][j], xh[i][j], s[1]);
+      }
+    }
+    load(row + stride);
+    row_sums<WPR>(s, part[turn][slot], slot, t >> 5);
+    const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * 32 * WPR + t) * N;
+#pragma unroll
+      for (int j = 0; j < N; ++j) g[i][j] = rho * (g[i][j] - fmaf(xh[i][j], m2, m1));
+      if (p.dres) {
+        float r[N];
+        unpack_piece<T>(load_piece(static_cast<const T*>(p.dres) + row * p.ldr + c, p.d - c,
+                                   p.r_vec),
+                        r);
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[i][j] += r[j];
+      }
+      store_piece(static_cast<T*>(p.dx) + row * p.lddx + c, g[i], p.d - c, p.dx_vec);
+    }
+  }
+  // this block's partial sums, row slots added in order
+  float* out = p.part + (long long)blockIdx.x * 2 * p.d;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float(&a)[NV][N] = which ? ds : dg;
+    if constexpr (ROWS > 1) {
+      for (int k = 1; k < ROWS; ++k) {
+        __syncthreads();
+        if (slot == k)
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) sums[(i * N + j) * 32 * WPR + t] = a[i][j];
+        __syncthreads();
+        if (slot == 0)
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < N; ++j) a[i][j] += sums[(i * N + j) * 32 * WPR + t];
+      }
+    }
+    if (slot == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 * WPR + t) * N;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+          if (c + j < p.d) out[(long long)which * p.d + c + j] = a[i][j];
+      }
+  }
+}
+
+// Wide rows, dx: one block per row, dy and x read twice.
+template <typename T, bool CK>
+__global__ void __launch_bounds__(kLoopThreads) ln_bwd_wide_kernel(const LayerNormBwd p) {
+  constexpr int N = RowVec<T>::N, WPR = kLoopThreads / 32;
+  __shared__ float part[2][2 * WPR];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t = threadIdx.x;
+  const float inv_d = 1.f / (float)p.d;
+  int turn = 0;
+  for (long long row = blockIdx.x; row < p.T; row += gridDim.x, turn ^= 1) {
+    const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
+    const float mu = p.mean[row], rho = p.rstd[row];
+    float s[2] = {0.f, 0.f};
+    auto piece = [&](int c, float(&g)[N], float(&xh)[N]) {
+      XPiece<T, CK> x;
+      float gain[N];
+      x.load(p, row, c, p.d - c);
+      x.values(xh);
+      unpack_piece<T>(load_piece(dy + c, p.d - c, p.dy_vec), g);
+      load_param<N>(p.gain, c, p.d - c, p.p_vec, 1.f, gain);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        xh[j] = c + j < p.d ? (xh[j] - mu) * rho : 0.f;
+        g[j] *= gain[j];
+      }
+    };
+    for (int c = t * N; c < p.d; c += kLoopThreads * N) {
+      float g[N], xh[N];
+      piece(c, g, xh);
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        s[0] += g[j];
+        s[1] = fmaf(g[j], xh[j], s[1]);
+      }
+    }
+    row_sums<WPR>(s, part[turn], 0, t >> 5);
+    const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+    for (int c = t * N; c < p.d; c += kLoopThreads * N) {
+      float g[N], xh[N];
+      piece(c, g, xh);
+#pragma unroll
+      for (int j = 0; j < N; ++j) g[j] = rho * (g[j] - fmaf(xh[j], m2, m1));
+      if (p.dres) {
+        float r[N];
+        unpack_piece<T>(
+            load_piece(static_cast<const T*>(p.dres) + row * p.ldr + c, p.d - c, p.r_vec), r);
+#pragma unroll
+        for (int j = 0; j < N; ++j) g[j] += r[j];
+      }
+      store_piece(static_cast<T*>(p.dx) + row * p.lddx + c, g, p.d - c, p.dx_vec);
+    }
+  }
+}
+
+// Wide rows, partial sums of dy xh and dy: block (x, y) adds rows y, y + chunks,
+// ... of its 256-piece stripe of columns.
+template <typename T, bool CK>
+__global__ void __launch_bounds__(256) ln_bwd_wide_sums_kernel(const LayerNormBwd p) {
+  constexpr int N = RowVec<T>::N;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int c = (blockIdx.x * 256 + threadIdx.x) * N;
+  if (c >= p.d) return;
+  float dg[N], ds[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) dg[j] = ds[j] = 0.f;
+#pragma unroll 2
+  for (long long row = blockIdx.y; row < p.T; row += gridDim.y) {
+    XPiece<T, CK> x;
+    float g[N], xh[N];
+    x.load(p, row, c, p.d - c);
+    x.values(xh);
+    unpack_piece<T>(
+        load_piece(static_cast<const T*>(p.dy) + row * p.lddy + c, p.d - c, p.dy_vec), g);
+    const float mu = p.mean[row], rho = p.rstd[row];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      dg[j] = fmaf(g[j], (xh[j] - mu) * rho, dg[j]);
+      ds[j] += g[j];
+    }
+  }
+  float* out = p.part + (long long)blockIdx.y * 2 * p.d;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (c + j < p.d) {
+      out[c + j] = dg[j];
+      out[p.d + c + j] = ds[j];
+    }
+}
+
+// dgain and dshift from the partial rows, in a fixed order: 32 columns per
+// block, one per lane (coalesced rows of 128 bytes), the rows dealt over 32
+// warps whose sums are added in warp order.
+__global__ void __launch_bounds__(1024) ln_bwd_sums_kernel(const float* __restrict__ part,
+                                                           int blocks, int d,
+                                                           float* __restrict__ dgain,
+                                                           float* __restrict__ dshift) {
+  __shared__ float s[32][33];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long c = (long long)blockIdx.x * 32 + lane;
+  float a = 0.f;
+  if (c < 2ll * d) {
+#pragma unroll 4
+    for (int r = w; r < blocks; r += 32) a += part[(long long)r * 2 * d + c];
+  }
+  s[w][lane] = a;
+  __syncthreads();
+  if (w != 0 || c >= 2ll * d) return;
+#pragma unroll
+  for (int r = 1; r < 32; ++r) a += s[r][lane];
+  if (c < d) dgain[c] = a;
+  else dshift[c - d] = a;
+}
+
+// ------------------------------------------------------------ launches
+
+bool row_vec(const void* p, long long ld, int esz, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * esz % bytes == 0;
+}
+
+// Blocks of a row-walking launch: enough for every SM to be full, at most one
+// per row set.
+int walk_blocks(long long T, int rows_per_block, int per_sm) {
+  const long long need = (T + rows_per_block - 1) / rows_per_block;
+  const long long most = (long long)num_sms() * per_sm;
+  return (int)(need < most ? need : most);
+}
+
+template <typename T, int WPR>
+mlp_status fwd_held(const LayerNormFwd& p, cudaStream_t st) {
+  using B = HeldBlock<WPR>;
+  const int per_sm = 2048 / B::THREADS;
+  launch_k(ln_fwd_kernel<T, WPR>, dim3(walk_blocks(p.T, B::ROWS, per_sm)), dim3(B::THREADS), 0, st,
+           p);
+  return launch_status();
+}
+
+template <typename T>
+mlp_status fwd_t(LayerNormFwd p, cudaStream_t st) {
+  p.x_vec = row_vec(p.x, p.ldx, sizeof(T), 16);
+  p.y_vec = row_vec(p.y, p.ldy, sizeof(T), 16);
+  p.q_vec = p.q && row_vec(p.q, p.ldq, 1, RowVec<T>::N);
+  p.p_vec = row_vec(p.gain, 0, 4, 16) && row_vec(p.shift, 0, 4, 16);
+  LaunchScope ls("layernorm_fwd", st, p.T, p.d, sizeof(T));
+  if (p.d <= 512) return fwd_held<T, 1>(p, st);
+  if (p.d <= 1024) return fwd_held<T, 2>(p, st);
+  if (p.d <= 2048) return fwd_held<T, 4>(p, st);
+  if (p.d <= 4096) return fwd_held<T, 8>(p, st);
+  if (p.d <= kHeldWidth) return fwd_held<T, 16>(p, st);
+  launch_k(ln_fwd_wide_kernel<T>, dim3(walk_blocks(p.T, 1, 2048 / kLoopThreads)),
+           dim3(kLoopThreads), 0, st, p);
+  return launch_status();
+}
+
+template <typename T, int WPR, bool CK>
+mlp_status bwd_held(const LayerNormBwd& p, int blocks, cudaStream_t st) {
+  using B = HeldBlock<WPR>;
+  const size_t smem = B::ROWS > 1 ? (size_t)32 * WPR * kPerThread * 4 : 0;
+  LaunchScope ls("layernorm_bwd", st, p.T, p.d, sizeof(T));
+  launch_k(ln_bwd_kernel<T, WPR, CK>, dim3(blocks), dim3(B::THREADS), smem, st, p);
+  return launch_status();
+}
+
+// Partial rows of a backward launch (also sizes its workspace, so it depends
+// on the sizes alone): 304 blocks of 8 row slots (or of one wide row) are two
+// per SM; more would read and write more partial sums than they save.
+constexpr int kBwdBlocks = 304;
+int bwd_blocks(long long T, int d) {
+  const int rows = d <= 512 ? 8 : d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
+  const long long need = (T + rows - 1) / rows;
+  return (int)(need < kBwdBlocks ? need : kBwdBlocks);
+}
+
+template <typename T, bool CK>
+mlp_status bwd_t(LayerNormBwd p, cudaStream_t st) {
+  p.dy_vec = row_vec(p.dy, p.lddy, sizeof(T), 16);
+  p.x_vec = CK ? 0 : row_vec(p.x, p.ldx, sizeof(T), 16);
+  p.q_vec = CK ? row_vec(p.q, p.ldq, 1, RowVec<T>::N) : 0;
+  p.r_vec = row_vec(p.dres, p.ldr, sizeof(T), 16);
+  p.dx_vec = row_vec(p.dx, p.lddx, sizeof(T), 16);
+  p.p_vec = row_vec(p.gain, 0, 4, 16);
+  const int blocks = bwd_blocks(p.T, p.d);
+  if (p.d <= 512) MLP_CHECK((bwd_held<T, 1, CK>(p, blocks, st)));
+  else if (p.d <= 1024) MLP_CHECK((bwd_held<T, 2, CK>(p, blocks, st)));
+  else if (p.d <= 2048) MLP_CHECK((bwd_held<T, 4, CK>(p, blocks, st)));
+  else if (p.d <= 4096) MLP_CHECK((bwd_held<T, 8, CK>(p, blocks, st)));
+  else if (p.d <= kHeldWidth) MLP_CHECK((bwd_held<T, 16, CK>(p, blocks, st)));
+  else {
+    {
+      LaunchScope ls("layernorm_bwd_wide", st, p.T, p.d, sizeof(T));
+      launch_k(ln_bwd_wide_kernel<T, CK>, dim3(walk_blocks(p.T, 1, 2048 / kLoopThreads)),
+               dim3(kLoopThreads), 0, st, p);
+      MLP_CHECK(launch_status());
+    }
+    LaunchScope ls("layernorm_bwd_wide_sums", st, p.T, p.d, sizeof(T));
+    const int stripe = 256 * RowVec<T>::N;
+    launch_k(ln_bwd_wide_sums_kernel<T, CK>, dim3((p.d + stripe - 1) / stripe, blocks), dim3(256),
+             0, st, p);
+    MLP_CHECK(launch_status());
+  }
+  LaunchScope ls("layernorm_bwd_sums", st, blocks, p.d);
+  launch_k(ln_bwd_sums_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st,
+           static_cast<const float*>(p.part), blocks, p.d, p.dgain, p.dshift);
+  return launch_status();
+}
+
+template <typename T>
+mlp_status bwd_ck(const LayerNormBwd& p, cudaStream_t st) {
+  return p.q ? bwd_t<T, true>(p, st) : bwd_t<T, false>(p, st);
+}
+
+}  // namespace
+
+size_t layernorm_ws_bytes(long long T, int d) {
+  return (size_t)bwd_blocks(T, d) * 2 * d * sizeof(float);
+}
+
+mlp_status launch_layernorm_fwd(const LayerNormFwd& a, cudaStream_t st) {
+  switch (a.dtype) {
+    case MLP_DTYPE_BF16: return fwd_t<__nv_bfloat16>(a, st);
+    case MLP_DTYPE_F16: return fwd_t<__half>(a, st);
+    default: return fwd_t<float>(a, st);
+  }
+}
+
+mlp_status launch_layernorm_bwd(const LayerNormBwd& a, cudaStream_t st) {
+  switch (a.dtype) {
+    case MLP_DTYPE_BF16: return bwd_ck<__nv_bfloat16>(a, st);
+    case MLP_DTYPE_F16: return bwd_ck<__half>(a, st);
+    default: return bwd_ck<float>(a, st);
+  }
+}
+
+}  // namespace mlp

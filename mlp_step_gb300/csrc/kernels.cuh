@@ -154,6 +154,112 @@ mlp_status launch_block_bwd_act(const void* x, const void* wg, const void* wd, c
 mlp_status launch_rmsnorm_bwd(const void* dnp, const void* x, const void* dy, const float* rstd,
                               int T, void* dx, cudaStream_t st);
 
+// k_ckpt8.cu: 8-bit checkpoints of a matrix (dtype of x / out: F32, BF16, F16).
+mlp_status launch_ckpt8_encode(const void* x, int dtype, long long rows, int cols, long long ldx,
+                               int8_t* q, long long ldq, uint8_t* scale, long long lds,
+                               cudaStream_t st);
+mlp_status launch_ckpt8_decode(const int8_t* q, long long ldq, const uint8_t* scale, long long lds,
+                               long long rows, int cols, void* out, int dtype, long long ldo,
+                               cudaStream_t st);
+
+// k_layernorm.cu.  The *_vec flags (16-byte pieces of each matrix's rows are
+// aligned) are the launchers' own.
+struct LayerNormFwd {
+  int dtype;
+  const void* x;
+  long long ldx;
+  const float* gain;   // nullable: 1
+  const float* shift;  // nullable: 0
+  long long T;
+  int d;
+  float eps;
+  void* y;
+  long long ldy;
+  float* mean;  // nullable
+  float* rstd;  // nullable
+  int8_t* q;    // nullable: x in 8 bits
+  long long ldq;
+  uint8_t* scale;
+  long long lds;
+  int x_vec, y_vec, q_vec, p_vec;
+};
+struct LayerNormBwd {
+  int dtype;
+  const void* dy;
+  long long lddy;
+  const void* x;  // or q and scale
+  long long ldx;
+  const int8_t* q;
+  long long ldq;
+  const uint8_t* scale;
+  long long lds;
+  const float* mean;
+  const float* rstd;
+  const float* gain;  // nullable
+  const void* dres;   // nullable
+  long long ldr;
+  long long T;
+  int d;
+  void* dx;
+  long long lddx;
+  float* dgain;
+  float* dshift;
+  float* part;  // workspace: layernorm_ws_bytes
+  int dy_vec, x_vec, q_vec, r_vec, dx_vec, p_vec;
+};
+size_t layernorm_ws_bytes(long long T, int d);
+mlp_status launch_layernorm_fwd(const LayerNormFwd& a, cudaStream_t st);
+mlp_status launch_layernorm_bwd(const LayerNormBwd& a, cudaStream_t st);
+
+// Linear layers: u = x W + bias, y = f(u) + residual (forward), or
+// du = (dy W^T) f'(u), a = f(u) and the column sums of du (backward).
+// Matrices of the operand type `dtype`, except y / residual / du which are
+// fp32 where out_f32 is set.
+struct LinearArgs {
+  int dtype;
+  long long T;
+  int K, N;  // contracted and output widths
+  const void* x;  // [T][K] (backward: dy)
+  long long ldx;
+  const void* w;  // forward [K][N], backward [N][K]
+  long long ldw;
+  int act;
+  float slope;
+  const float* bias;
+  const void* res;
+  long long ldr;
+  void* y;  // forward y, backward du
+  long long ldy;
+  int out_f32;
+  void* u_out;  // forward: pre-activations; backward: activations
+  long long ldu_out;
+  const void* u_in;  // backward: saved pre-activations, or q / scale
+  long long ldu_in;
+  int8_t* q;  // forward: pre-activations in 8 bits (out); backward: (in)
+  long long ldq;
+  uint8_t* scale;
+  long long lds;
+  float* colpart;    // backward: fp32 [linear_part_rows(T)][ldcp] partial column sums (nullable)
+  long long ldcp;
+  float* partial;    // fp32 [splits][T][ldp] raw sums
+  long long ldp;
+  int splits;
+};
+// Rows of colpart: one per 32 rows of du.
+inline long long linear_part_rows(long long T) { return (T + 31) / 32; }
+// k_linear.cu: tcgen05 kernel of 16-bit operands.  splits > 1: raw partial
+// sums into a.partial, to be finished by launch_linear_finish.
+mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st);
+// Split count of that kernel (from the shape alone).
+int linear_tc_splits(long long T, int K, int N);
+// k_linear_small.cu: up to kLinearFewRows rows, all types, one launch; in the
+// backward it writes the column sums to `dbias` itself.
+constexpr int kLinearFewRows = 8;
+mlp_status launch_linear_few(const LinearArgs& a, bool bwd, float* dbias, cudaStream_t st);
+// k_linear_small.cu: the epilogue over a.splits planes of raw sums
+// (a.partial), or, with elementwise set, over dy itself (a.x).
+mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, bool elementwise, cudaStream_t st);
+
 // Host helpers (api.cu)
 unsigned long long wait_limit_ns();
 // MLP_ORDER_LINEAR in effect (mlp_set_reduction_order)?
