@@ -5,108 +5,210 @@
 //   MLP_ACT_GELU_TANH       u (1 + tanh z) / 2 = u / (1 + e^(-2z)),
 //                           z = sqrt(2 / pi) (u + 0.044715 u^3)
 //   MLP_ACT_SILU            u / (1 + e^(-u))
-// ACC = true uses the CUDA library functions (fp32 operands); ACC = false the
-// hardware exponential and reciprocal (a few 2^-23 relative) and, for Phi,
-// the rational approximation 7.1.26 of Abramowitz and Stegun, "Handbook of
-// Mathematical Functions" (absolute error 1.5e-7 of erfc): below the rounding
-// of 16-bit outputs, and about half the instructions, which bound the
-// epilogue of short-K products.
+// ACC = true (fp32 layers) uses the CUDA library functions.  ACC = false
+// (16-bit layers, where the activation's instructions bound the epilogue of
+// short-K products) works on two values at a time with the packed fp32
+// instructions, the hardware exponential and reciprocal (a few 2^-23
+// relative) and, for Phi, the rational approximation 7.1.26 of Abramowitz and
+// Stegun, "Handbook of Mathematical Functions" (absolute error 1.5e-7 of
+// erfc): all below the rounding of 16-bit outputs.
 #pragma once
 
 #include "common.cuh"
 
 namespace mlp {
 
-// 2^x by the hardware instruction
-__device__ __forceinline__ float exp2f_fast(float x) {
+// ------------------------------------------------------------ packed fp32
+
+struct alignas(8) F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 f2(float a, float b) { return {a, b}; }
+__device__ __forceinline__ F2 f2(float a) { return {a, a}; }
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  const float2 r = __fmul2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y));
+  return {r.x, r.y};
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  const float2 r = __fadd2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y));
+  return {r.x, r.y};
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  const float2 r =
+      __ffma2_rn(make_float2(a.x, a.y), make_float2(b.x, b.y), make_float2(c.x, c.y));
+  return {r.x, r.y};
+}
+
+// 2^x and 1 / x by the hardware instructions
+__device__ __forceinline__ float ex2_fast(float x) {
   float r;
-  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// min(|x|, limit); a NaN stays one
+__device__ __forceinline__ float abs_upto(float x, float limit) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(x)), "f"(limit));
   return r;
 }
 
-template <bool ACC>
-__device__ __forceinline__ float act_sigmoid(float z) {
-  if constexpr (ACC) return 1.f / (1.f + expf(-z));
-  else return __fdividef(1.f, 1.f + __expf(-z));
+// Logistic function of z.
+__device__ __forceinline__ F2 sigmoid2(F2 z) {
+  const F2 t = mul2(z, f2(-1.4426950408889634f));
+  const F2 d = add2(f2(ex2_fast(t.x), ex2_fast(t.y)), f2(1.f));
+  return f2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
-// Phi(u), and e^(-u^2 / 2) on the way
-template <bool ACC>
-__device__ __forceinline__ float act_phi(float u, float& gauss) {
-  if constexpr (ACC) {
-    gauss = expf(-0.5f * u * u);
-    return 0.5f * erfcf(-0.70710678118654752f * u);
+// Of c = min(|u|, 14): Phi(-c) and the Gaussian e^(-c^2 / 2).
+__device__ __forceinline__ F2 normal_tail2(F2 c, F2& gauss) {
+  const F2 e = mul2(mul2(c, c), f2(-0.72134752044448170f));  // log2(e) / 2
+  gauss = f2(ex2_fast(e.x), ex2_fast(e.y));
+  const F2 d = fma2(c, f2(0.23164188827f), f2(1.f));  // 0.3275911 / sqrt 2
+  const F2 t = f2(rcp_fast(d.x), rcp_fast(d.y));
+  // half of a5 .. a1
+  F2 p = fma2(f2(0.5307027145f), t, f2(-0.7265760135f));
+  p = fma2(p, t, f2(0.7107068705f));
+  p = fma2(p, t, f2(-0.142248368f));
+  p = fma2(p, t, f2(0.127414796f));
+  return mul2(mul2(p, t), gauss);
+}
+
+constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhCubic = 0.044715f;
+// Arguments beyond which the bell-shaped parts are below the smallest fp32:
+// they are evaluated there instead, so that an infinite u gives the limits 0
+// and 1 rather than 0 times infinity.
+constexpr float kGaussEnd = 14.f, kLogisticEnd = 104.f;
+
+// f(u) of activation ACT for two values.
+template <int ACT>
+__device__ __forceinline__ F2 act_value2(F2 u, float slope) {
+  if constexpr (ACT == MLP_ACT_RELU) {
+    return f2(u.x <= 0.f ? 0.f : u.x, u.y <= 0.f ? 0.f : u.y);  // a NaN stays one
+  } else if constexpr (ACT == MLP_ACT_LEAKY_RELU_SQ) {
+    const F2 s = mul2(u, f2(slope));
+    const F2 t = f2(u.x > 0.f ? u.x : s.x, u.y > 0.f ? u.y : s.y);
+    return mul2(t, t);
+  } else if constexpr (ACT == MLP_ACT_GELU) {
+    // u Phi(u) = max(u, 0) - |u| Phi(-|u|)
+    const F2 c = f2(abs_upto(u.x, kGaussEnd), abs_upto(u.y, kGaussEnd));
+    F2 g;
+    const F2 tail = normal_tail2(c, g);
+    return f2(fmaf(-c.x, tail.x, fmaxf(u.x, 0.f)), fmaf(-c.y, tail.y, fmaxf(u.y, 0.f)));
+  } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
+    const F2 k = fma2(mul2(u, u), f2(kTanhScale * kTanhCubic), f2(kTanhScale));
+    return mul2(u, sigmoid2(mul2(u, k)));
+  } else if constexpr (ACT == MLP_ACT_SILU) {
+    return mul2(u, sigmoid2(u));
   } else {
-    gauss = exp2f_fast(-0.72134752044448170f * u * u);  // log2(e) / 2
-    const float t = __fdividef(1.f, fmaf(0.23164188612f, fabsf(u), 1.f));  // 0.3275911 / sqrt 2
-    // half of a1 .. a5
-    float p = fmaf(0.5307027145f, t, -0.7265760135f);
-    p = fmaf(p, t, 0.7107068705f);
-    p = fmaf(p, t, -0.142248368f);
-    p = fmaf(p, t, 0.127414796f);
-    const float tail = p * t * gauss;  // Phi(-|u|)
-    return u < 0.f ? tail : 1.f - tail;
+    return u;
   }
 }
 
-template <bool ACC>
-__device__ __forceinline__ float act_value(float u, int act, float slope) {
-  switch (act) {
-    case MLP_ACT_RELU: return u <= 0.f ? 0.f : u;  // a NaN stays one
-    case MLP_ACT_LEAKY_RELU_SQ: {
-      const float t = u > 0.f ? u : slope * u;
-      return t * t;
-    }
-    case MLP_ACT_GELU: {
-      float g;
-      return u * act_phi<ACC>(u, g);
-    }
-    case MLP_ACT_GELU_TANH:
-      return u * act_sigmoid<ACC>(1.5957691216057308f * fmaf(0.044715f * u * u, u, u));
-    case MLP_ACT_SILU: return u * act_sigmoid<ACC>(u);
-    default: return u;
+// f'(u) of two values; f(u) into `value`.
+template <int ACT>
+__device__ __forceinline__ F2 act_grad2(F2 u, float slope, F2& value) {
+  if constexpr (ACT == MLP_ACT_RELU) {
+    value = f2(u.x <= 0.f ? 0.f : u.x, u.y <= 0.f ? 0.f : u.y);
+    return f2(u.x <= 0.f ? 0.f : 1.f, u.y <= 0.f ? 0.f : 1.f);
+  } else if constexpr (ACT == MLP_ACT_LEAKY_RELU_SQ) {
+    const F2 s = f2(u.x > 0.f ? 1.f : slope, u.y > 0.f ? 1.f : slope);
+    const F2 t = mul2(s, u);
+    value = mul2(t, t);
+    return mul2(s, add2(t, t));
+  } else if constexpr (ACT == MLP_ACT_GELU) {
+    const F2 c = f2(abs_upto(u.x, kGaussEnd), abs_upto(u.y, kGaussEnd));
+    F2 g;
+    const F2 tail = normal_tail2(c, g);
+    value = f2(fmaf(-c.x, tail.x, fmaxf(u.x, 0.f)), fmaf(-c.y, tail.y, fmaxf(u.y, 0.f)));
+    // f' = Phi(u) + u phi(u); for u < 0 it is 1 - f'(-u), and with
+    // s = 1/2 - (Phi(-c) - c phi(c)) it is 1/2 +- s
+    const F2 q = fma2(mul2(c, f2(0.3989422804014327f)), g, f2(0.5f));
+    return f2(0.5f + copysignf(q.x - tail.x, u.x), 0.5f + copysignf(q.y - tail.y, u.y));
+  } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
+    const F2 c = f2(copysignf(abs_upto(u.x, kGaussEnd), u.x),
+                    copysignf(abs_upto(u.y, kGaussEnd), u.y));
+    const F2 c2 = mul2(mul2(c, c), f2(kTanhCubic));
+    const F2 s = sigmoid2(mul2(mul2(c, f2(kTanhScale)), add2(c2, f2(1.f))));
+    value = mul2(u, s);
+    const F2 w = fma2(c2, f2(3.f * kTanhScale), f2(kTanhScale));
+    const F2 b = mul2(mul2(c, s), fma2(s, f2(-1.f), f2(1.f)));
+    return fma2(b, w, s);
+  } else if constexpr (ACT == MLP_ACT_SILU) {
+    const F2 c = f2(copysignf(abs_upto(u.x, kLogisticEnd), u.x),
+                    copysignf(abs_upto(u.y, kLogisticEnd), u.y));
+    const F2 s = sigmoid2(c);
+    value = mul2(u, s);
+    return fma2(mul2(c, s), fma2(s, f2(-1.f), f2(1.f)), s);
+  } else {
+    value = u;
+    return f2(1.f);
   }
 }
 
-// f'(u); f(u) into `value`.  Arguments of the bell-shaped parts are held to
-// where those parts are below the smallest fp32 (|u| = 14 for the Gaussian
-// and the cubic, 104 for the logistic), so that an infinite u gives the
-// limits 0 and 1 rather than 0 times infinity.
-template <bool ACC>
-__device__ __forceinline__ float act_grad(float u, int act, float slope, float& value) {
+// ------------------------------------------------------------ one value
+
+// f(u)
+template <bool ACC, int ACT>
+__device__ __forceinline__ float act_value_of(float u, float slope) {
+  if constexpr (!ACC || ACT <= MLP_ACT_LEAKY_RELU_SQ) {
+    return act_value2<ACT>(f2(u), slope).x;
+  } else if constexpr (ACT == MLP_ACT_GELU) {
+    return u * 0.5f * erfcf(-0.70710678118654752f * u);
+  } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
+    return u / (1.f + expf(-kTanhScale * fmaf(kTanhCubic * u * u, u, u)));
+  } else {
+    return u / (1.f + expf(-u));
+  }
+}
+
+// f'(u); f(u) into `value`
+template <bool ACC, int ACT>
+__device__ __forceinline__ float act_grad_of(float u, float slope, float& value) {
+  if constexpr (!ACC || ACT <= MLP_ACT_LEAKY_RELU_SQ) {
+    F2 v;
+    const float d = act_grad2<ACT>(f2(u), slope, v).x;
+    value = v.x;
+    return d;
+  } else if constexpr (ACT == MLP_ACT_GELU) {
+    const float c = copysignf(abs_upto(u, kGaussEnd), u);
+    const float phi = 0.5f * erfcf(-0.70710678118654752f * c);
+    value = u * phi;
+    return fmaf(0.3989422804014327f * c, expf(-0.5f * c * c), phi);
+  } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
+    const float c = copysignf(abs_upto(u, kGaussEnd), u);
+    const float c2 = kTanhCubic * c * c;
+    const float s = 1.f / (1.f + expf(-kTanhScale * fmaf(c2, c, c)));
+    value = u * s;
+    return fmaf(c * s * (1.f - s), kTanhScale * fmaf(3.f, c2, 1.f), s);
+  } else {
+    const float c = copysignf(abs_upto(u, kLogisticEnd), u);
+    const float s = 1.f / (1.f + expf(-c));
+    value = u * s;
+    return fmaf(c * s, 1.f - s, s);
+  }
+}
+
+// Calls f with the activation as a compile-time constant: one branch per call
+// instead of one per value.
+template <int ACT>
+struct ActTag {
+  static constexpr int value = ACT;
+};
+template <typename F>
+__device__ __forceinline__ void with_act(int act, F&& f) {
   switch (act) {
-    case MLP_ACT_RELU:
-      value = u <= 0.f ? 0.f : u;
-      return u <= 0.f ? 0.f : 1.f;
-    case MLP_ACT_LEAKY_RELU_SQ: {
-      const float s = u > 0.f ? 1.f : slope;
-      const float t = s * u;
-      value = t * t;
-      return 2.f * s * t;
-    }
-    case MLP_ACT_GELU: {
-      const float c = fabsf(u) > 14.f ? copysignf(14.f, u) : u;
-      float g;
-      const float phi = act_phi<ACC>(c, g);
-      value = u * phi;
-      return fmaf(0.3989422804014327f * c, g, phi);
-    }
-    case MLP_ACT_GELU_TANH: {
-      const float c = fabsf(u) > 14.f ? copysignf(14.f, u) : u;
-      const float c2 = 0.044715f * c * c;
-      const float s = act_sigmoid<ACC>(1.5957691216057308f * fmaf(c2, c, c));
-      value = u * s;
-      return fmaf(c * s * (1.f - s), 1.5957691216057308f * fmaf(3.f, c2, 1.f), s);
-    }
-    case MLP_ACT_SILU: {
-      const float c = fabsf(u) > 104.f ? copysignf(104.f, u) : u;
-      const float s = act_sigmoid<ACC>(c);
-      value = u * s;
-      return fmaf(c * s, 1.f - s, s);
-    }
-    default:
-      value = u;
-      return 1.f;
+    case MLP_ACT_RELU: f(ActTag<MLP_ACT_RELU>{}); break;
+    case MLP_ACT_LEAKY_RELU_SQ: f(ActTag<MLP_ACT_LEAKY_RELU_SQ>{}); break;
+    case MLP_ACT_GELU: f(ActTag<MLP_ACT_GELU>{}); break;
+    case MLP_ACT_GELU_TANH: f(ActTag<MLP_ACT_GELU_TANH>{}); break;
+    case MLP_ACT_SILU: f(ActTag<MLP_ACT_SILU>{}); break;
+    default: f(ActTag<MLP_ACT_NONE>{}); break;
   }
 }
 

@@ -15,8 +15,8 @@ namespace mlp {
 constexpr int kCkptGroup = 32;
 constexpr uint32_t kCkptMinByte = 7, kCkptNanByte = 255;
 
-// Scale byte of a group from the largest |x| of it as fp32 bits (compared as
-// whole numbers, in which NaN and infinity are the largest).
+// Scale byte of a group from the bits of its largest |x| (whose exponent field
+// is 255 for infinity and NaN).
 __device__ __forceinline__ uint32_t ckpt8_byte(uint32_t amax_bits) {
   const uint32_t e = amax_bits >> 23;
   return e < kCkptMinByte ? kCkptMinByte : e;
@@ -33,16 +33,28 @@ __device__ __forceinline__ float ckpt8_step(uint32_t b) {
   return __uint_as_float(b == kCkptNanByte ? 0x7fffffffu : (b - 6u) << 23);
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+// The larger of a running maximum of magnitudes and |x|; a NaN is kept.
+__device__ __forceinline__ float amax_step(float amax, float x) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(amax), "f"(fabsf(x)));
+  return r;
+}
 
-// q of one value as the low byte of the result.  Adding 1.5 2^23 rounds
-// x inv_step to a whole number (the product is exact, so the fused
-// multiply-add rounds once) and leaves its two's complement in the low bits;
-// the clamp is on the sum, where whole steps are exact.
+// Magnitudes of 127.5 steps and more round to 128 and are held to 127 (a group
+// can only hold them when its largest has a mantissa of at least 255/128).
+__device__ __forceinline__ bool ckpt8_must_hold(uint32_t amax_bits) {
+  return (amax_bits & 0x7fffffu) >= 0x7f0000u;
+}
+__device__ __forceinline__ float ckpt8_hold(float x, float step) {
+  return fminf(fmaxf(x, -127.f * step), 127.f * step);
+}
+
+// q of one value (held to 127 steps) as the low byte of the result.  Adding
+// 1.5 2^23 rounds x inv_step to a whole number (the product is exact, so the
+// fused multiply-add rounds once) and leaves its two's complement in the low
+// bits.
 __device__ __forceinline__ uint32_t ckpt8_q(float x, float inv_step) {
-  constexpr float kMagic = 12582912.f;
-  const float t = fmaf(x, inv_step, kMagic);
-  return __float_as_uint(fminf(fmaxf(t, kMagic - 127.f), kMagic + 127.f));
+  return __float_as_uint(fmaf(x, inv_step, 12582912.f));
 }
 
 // Four q bytes packed (first value lowest).
@@ -53,11 +65,52 @@ __device__ __forceinline__ uint32_t ckpt8_pack4(float a, float b, float c, float
   return __byte_perm(lo, hi, 0x5410);
 }
 
+// A piece of a group: its q bytes, given the largest magnitude of the whole
+// group as bits.  Returns the scale byte.
+template <int N>
+__device__ __forceinline__ uint32_t ckpt8_piece(const float (&v)[N], uint32_t amax_bits,
+                                                uint32_t (&w)[N / 4]) {
+  const uint32_t b = ckpt8_byte(amax_bits);
+  const float inv = ckpt8_inv_step(b);
+  if (ckpt8_must_hold(amax_bits)) {  // few groups, and those that are not finite
+    const float step = ckpt8_step(b);
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k)
+      w[k] = b == kCkptNanByte
+                 ? 0u
+                 : ckpt8_pack4(ckpt8_hold(v[4 * k], step), ckpt8_hold(v[4 * k + 1], step),
+                               ckpt8_hold(v[4 * k + 2], step), ckpt8_hold(v[4 * k + 3], step), inv);
+  } else {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k)
+      w[k] = b == kCkptNanByte
+                 ? 0u
+                 : ckpt8_pack4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+  }
+  return b;
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t amax_bits_of(const float (&v)[N]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; ++j) m = amax_step(m, v[j]);
+  return __float_as_uint(m) & 0x7fffffffu;
+}
+
+// A whole group held by one thread.
+__device__ __forceinline__ uint32_t ckpt8_group(const float (&v)[32], uint32_t (&w)[8]) {
+  return ckpt8_piece(v, amax_bits_of(v), w);
+}
+
 // The value of byte `i` of a packed word.  Flipping the sign bit makes the
 // byte q + 128, which dropped into the low mantissa of 2^23 is an exact float.
+constexpr float kCkptBias = 8388736.f;  // 2^23 + 128
+__device__ __forceinline__ float ckpt8_biased(uint32_t word_flipped, int i) {
+  return __uint_as_float(__byte_perm(word_flipped, 0x4B000000u, 0x7540 + i));
+}
 __device__ __forceinline__ float ckpt8_value(uint32_t word_flipped, int i, float step) {
-  const uint32_t f = __byte_perm(word_flipped, 0x4B000000u, 0x7540 + i);
-  return (__uint_as_float(f) - 8388736.f) * step;
+  return (ckpt8_biased(word_flipped, i) - kCkptBias) * step;
 }
 __device__ __forceinline__ uint32_t ckpt8_flip(uint32_t word) { return word ^ 0x80808080u; }
 

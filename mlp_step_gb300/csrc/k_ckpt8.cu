@@ -65,20 +65,12 @@ __global__ void __launch_bounds__(kThreads)
   for (int k = 0; k < kItems; ++k) {
     float v[N];
     unpack_piece<T>(raw[k], v);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) amax = max(amax, abs_bits(v[j]));
+    uint32_t amax = amax_bits_of(v);
 #pragma unroll
     for (int o = LANES / 2; o > 0; o >>= 1)
       amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const uint32_t b = ckpt8_byte(amax);
-    const float inv = ckpt8_inv_step(b);
     uint32_t w[N / 4];
-#pragma unroll
-    for (int j = 0; j < N / 4; ++j)
-      w[j] = b == kCkptNanByte
-                 ? 0u
-                 : ckpt8_pack4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv);
+    const uint32_t b = ckpt8_piece(v, amax, w);
     if (row[k] < rows && col[k] < cols) {
       store_q<N>(q + row[k] * ldq + col[k], cols - col[k], q_vec, w);
       if ((threadIdx.x & (LANES - 1)) == 0) scale[row[k] * lds + col[k] / kCkptGroup] = (uint8_t)b;

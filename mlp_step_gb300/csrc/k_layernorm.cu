@@ -91,20 +91,12 @@ template <typename T>
 __device__ __forceinline__ void store_ckpt(const float (&v)[RowVec<T>::N], int8_t* qrow,
                                            uint8_t* srow, int c, int n, bool vec) {
   constexpr int N = RowVec<T>::N, LANES = kCkptGroup / N;
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < N; ++j) amax = max(amax, abs_bits(v[j]));
+  uint32_t amax = amax_bits_of(v);
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1)
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const uint32_t b = ckpt8_byte(amax);
-  const float inv = ckpt8_inv_step(b);
   uint32_t w[N / 4];
-#pragma unroll
-  for (int j = 0; j < N / 4; ++j)
-    w[j] = b == kCkptNanByte
-               ? 0u
-               : ckpt8_pack4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3], inv);
+  const uint32_t b = ckpt8_piece(v, amax, w);
   if (n > 0) {
     store_q<N>(qrow + c, n, vec, w);
     if ((threadIdx.x & (LANES - 1)) == 0) srow[c / kCkptGroup] = (uint8_t)b;

@@ -14,9 +14,9 @@
 // of them to fill the GPU, single CTAs on 128 x 128 or 128 x 64 tiles
 // otherwise, with the contraction split over CTAs when even those are few
 // (raw sums to a workspace, finished by launch_linear_finish).  Warps: TMA
-// producer, MMA issuer, eight epilogue warps (a tensor-memory lane quarter
-// and half of the columns each); two accumulators, so that the epilogue of one
-// tile overlaps the MMAs of the next.  W is read as it is stored: [K][N] as an
+// producer, MMA issuer, eight or sixteen epilogue warps (a tensor-memory lane
+// quarter and a share of the columns each); two accumulators, so that the
+// epilogue of one tile overlaps the MMAs of the next.  W is read as it is stored: [K][N] as an
 // N-major operand, [N][K] (backward) as a K-major one.
 //
 // Bound: the MMAs for long K; for K of a few hundred, the epilogue's
@@ -34,9 +34,7 @@ namespace mlp {
 namespace {
 
 constexpr int BK = 64;
-constexpr int kThreads = 320;  // producer, MMA issuer, 8 epilogue warps
-constexpr int kEpiWarps = 8;
-constexpr int kStage = 8192;   // output staging bytes per epilogue warp
+constexpr int kStage = 4096;  // output staging bytes per epilogue warp
 
 struct LinParams {
   LinearArgs a;
@@ -52,9 +50,15 @@ struct LinLayout {
   static constexpr int B_COLS = PAIR ? 128 : BN;  // operand columns staged per CTA
   static constexpr int B_BYTES = B_COLS * BK * 2;
   static constexpr int ACC = PAIR ? 256 : BN;     // accumulator columns per CTA
-  static constexpr int BAR_BYTES = 2048;          // barriers, then 8 x 32 bias floats at 1024
+  // Epilogue warps: four per scheduler, where the tile has 32 columns for
+  // each; with two per scheduler the epilogue's latencies (tensor-memory
+  // loads, the proxy fence before each store) left half of the issue slots
+  // empty.
+  static constexpr int EPI_WARPS = ACC >= 128 ? 16 : 8;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;  // + producer, MMA issuer
+  static constexpr int BAR_BYTES = 1024;
   static constexpr int SMEM =
-      1024 + STAGES * (A_BYTES + B_BYTES) + BAR_BYTES + kEpiWarps * kStage;
+      1024 + STAGES * (A_BYTES + B_BYTES) + BAR_BYTES + EPI_WARPS * kStage;
   static constexpr uint32_t TMEM_COLS = 2 * ACC;
   static_assert(SMEM <= 232448, "shared memory");
 };
@@ -73,19 +77,17 @@ __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm
 // ------------------------------------------------------------ epilogue pieces
 
 template <int H16>
-__device__ __forceinline__ void unpack2(uint32_t w, float& a, float& b) {
+__device__ __forceinline__ F2 unpack2(uint32_t w) {
   if constexpr (H16) {
     const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w));
-    a = f.x;
-    b = f.y;
+    return f2(f.x, f.y);
   } else {
-    a = __uint_as_float(w << 16);
-    b = __uint_as_float(w & 0xffff0000u);
+    return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
   }
 }
 
 // 32 consecutive values of a row as they lie in memory: 64 bytes of a 16-bit
-// type, or 32 int8 and a scale byte.  Loaded one piece ahead of their use.
+// type, or 32 int8 and a scale byte.
 struct Saved {
   uint4 q[4];
   uint32_t b;
@@ -126,130 +128,50 @@ __device__ __forceinline__ void load_row8(const LinearArgs& a, long long m, int 
   }
 }
 
-template <int H16>
-__device__ __forceinline__ void saved16(const Saved& s, float (&v)[32]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(s.q);
-#pragma unroll
-  for (int k = 0; k < 16; ++k) unpack2<H16>(w[k], v[2 * k], v[2 * k + 1]);
-}
-
-__device__ __forceinline__ void saved8(const Saved& s, float (&v)[32]) {
-  const uint32_t* w = reinterpret_cast<const uint32_t*>(s.q);
-  const float step = ckpt8_step(s.b);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t f = ckpt8_flip(w[k]);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[4 * k + e] = ckpt8_value(f, e, step);
-  }
-}
-
-// 32 values of a row to memory from registers (ragged or unaligned rows, and
-// matrices too small for staging to pay).
-template <int H16>
-__device__ __forceinline__ void store_row(void* base, long long ld, int f32, long long m, int n0,
-                                          int N, const float (&v)[32]) {
-  if (f32) {
-    float* p = static_cast<float*>(base) + m * ld + n0;
-    if (n0 + 32 <= N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        reinterpret_cast<float4*>(p)[k] =
-            make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (n0 + j < N) p[j] = v[j];
-    }
-    return;
-  }
-  uint16_t* p = static_cast<uint16_t*>(base) + m * ld + n0;
-  if (n0 + 32 <= N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      reinterpret_cast<uint4*>(p)[k] =
-          make_uint4(pack16x2<H16>(v[8 * k], v[8 * k + 1]), pack16x2<H16>(v[8 * k + 2], v[8 * k + 3]),
-                     pack16x2<H16>(v[8 * k + 4], v[8 * k + 5]),
-                     pack16x2<H16>(v[8 * k + 6], v[8 * k + 7]));
-  } else {
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (n0 + j < N) p[j] = f32_to_16<H16>(v[j]);
-  }
-}
-
-// A warp's ring of staging boxes for TMA stores: 32 rows x 32 columns each, a
-// 16-bit box in the 64-byte swizzle its tensor map names, an fp32 box in the
-// 128-byte one.  With an fp32 output every box takes 4 KiB (two in turn), else
-// 2 KiB (four in turn); a box is reused once its store has read it.
-struct Ring {
-  uint8_t* base;
-  int wide, used;
-  __device__ __forceinline__ uint8_t* next(int lane) {
-    const int boxes = wide ? 2 : 4;
-    if (used >= boxes) {
-      if (lane == 0) {
-        if (wide) ptx::bulk_wait_group_read<1>();
-        else ptx::bulk_wait_group_read<3>();
-      }
-      __syncwarp();
-    }
-    uint8_t* b = base + (used % boxes) * (kStage / boxes);
-    ++used;
-    return b;
-  }
+// Where a piece's 32 values of one output go: a row of a staging box that a
+// TMA store then moves (32 rows x 32 columns; 16-bit boxes in the 64-byte
+// swizzle their tensor map names, fp32 ones in the 128-byte swizzle), or the
+// matrix itself, for ragged pieces, unaligned rows and small outputs.
+struct Sink {
+  uint8_t* box;  // this lane's row of the box, or nullptr
+  uint8_t* mem;  // this lane's row of the matrix at the piece's first column
+  int f32, lane, n;  // n: columns that exist (0: a row past the end)
 };
 
 template <int H16>
-__device__ __forceinline__ void stage_store(Ring& ring, const CUtensorMap* map, int f32,
-                                            const float (&v)[32], int n0, int row0, int lane) {
-  uint8_t* box = ring.next(lane);
-  if (f32) {
-    uint8_t* row = box + lane * 128;
+__device__ __forceinline__ void sink8(const Sink& s, int k, const F2 (&v)[4]) {
+  if (s.f32) {
+    const float4 lo = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    const float4 hi = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    if (s.box) {
+      *reinterpret_cast<float4*>(s.box + (((2 * k) ^ (s.lane & 7)) << 4)) = lo;
+      *reinterpret_cast<float4*>(s.box + (((2 * k + 1) ^ (s.lane & 7)) << 4)) = hi;
+    } else {
+      float* p = reinterpret_cast<float*>(s.mem) + 8 * k;
+      if (8 * k + 8 <= s.n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        reinterpret_cast<float4*>(p)[0] = lo;
+        reinterpret_cast<float4*>(p)[1] = hi;
+      } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      *reinterpret_cast<float4*>(row + ((k ^ (lane & 7)) << 4)) =
-          make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-  } else {
-    uint8_t* row = box + lane * 64;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      *reinterpret_cast<uint4*>(row + ((k ^ ((lane >> 1) & 3)) << 4)) =
-          make_uint4(pack16x2<H16>(v[8 * k], v[8 * k + 1]), pack16x2<H16>(v[8 * k + 2], v[8 * k + 3]),
-                     pack16x2<H16>(v[8 * k + 4], v[8 * k + 5]),
-                     pack16x2<H16>(v[8 * k + 6], v[8 * k + 7]));
+        for (int j = 0; j < 8; ++j)
+          if (8 * k + j < s.n) p[j] = j & 1 ? v[j / 2].y : v[j / 2].x;
+      }
+    }
+    return;
   }
-  ptx::fence_proxy_async_smem();
-  __syncwarp();
-  if (lane == 0) {
-    ptx::tma_store_2d(map, box, n0, row0);
-    ptx::bulk_commit_group();
-  }
-}
-
-// The 8-bit form of a thread's 32 values.
-__device__ __forceinline__ void store_row8(const LinearArgs& a, long long m, int n0,
-                                           const float (&v)[32]) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < 32; ++j)
-    if (n0 + j < a.N) amax = max(amax, abs_bits(v[j]));
-  const uint32_t b = ckpt8_byte(amax);
-  const float inv = ckpt8_inv_step(b);
-  uint32_t w[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    w[k] = b == kCkptNanByte ? 0u
-                             : ckpt8_pack4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
-  int8_t* p = a.q + m * a.ldq + n0;
-  a.scale[m * a.lds + n0 / kCkptGroup] = (uint8_t)b;
-  if (n0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  const uint4 o = make_uint4(pack16x2<H16>(v[0].x, v[0].y), pack16x2<H16>(v[1].x, v[1].y),
+                             pack16x2<H16>(v[2].x, v[2].y), pack16x2<H16>(v[3].x, v[3].y));
+  if (s.box) {
+    *reinterpret_cast<uint4*>(s.box + ((k ^ ((s.lane >> 1) & 3)) << 4)) = o;
   } else {
+    uint16_t* p = reinterpret_cast<uint16_t*>(s.mem) + 8 * k;
+    if (8 * k + 8 <= s.n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      *reinterpret_cast<uint4*>(p) = o;
+    } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (n0 + j < a.N) p[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
+      for (int j = 0; j < 8; ++j)
+        if (8 * k + j < s.n) p[j] = f32_to_16<H16>(j & 1 ? v[j / 2].y : v[j / 2].x);
+    }
   }
 }
 
@@ -257,7 +179,8 @@ __device__ __forceinline__ void store_row8(const LinearArgs& a, long long m, int
 // half of its columns to its partner and adds the partner's half of its own,
 // so after five rounds lane j holds the sum of column j.  31 exchanges for 32
 // columns, in a fixed order.
-__device__ __forceinline__ float column_sums(float (&v)[32], int lane) {
+__device__ __forceinline__ float column_sums(F2 (&p)[16], int lane) {
+  float* v = reinterpret_cast<float*>(p);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const bool upper = lane & o;
@@ -288,14 +211,13 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * L::A_BYTES;
   uint8_t* stg = sB + STAGES * L::B_BYTES;
-  uint64_t* full = reinterpret_cast<uint64_t*>(stg + kEpiWarps * kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg + L::EPI_WARPS * kStage);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
   uint64_t* done = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* sbias = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + 1024);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
@@ -309,7 +231,7 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
     }
     for (int k = 0; k < 2; ++k) {
       ptx::mbar_init(&tfull[k], 1);
-      ptx::mbar_init(&tempty[k], PAIR ? 2 * kEpiWarps : kEpiWarps);
+      ptx::mbar_init(&tempty[k], PAIR ? 2 * L::EPI_WARPS : L::EPI_WARPS);
     }
     ptx::mbar_init(done, 1);
     *s_abort = 0;
@@ -452,11 +374,15 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
       ptx::mbar_wait_bounded(done, 0, p.wait_ns, p.err, DEVERR_TIMEOUT_TEARDOWN);
     }
   } else {
-    const int quarter = warp & 3;                  // tensor-memory lanes [32 q, 32 q + 32)
-    const int c_half = ((warp - 2) >> 2) * (ACC / 2);  // this warp's half of the columns
+    const int quarter = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
+    constexpr int SPAN = ACC / (L::EPI_WARPS / 4);  // columns of a warp
+    const int c_first = ((warp - 2) >> 2) * SPAN;
     const uint32_t tempty0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
-    float* bias_slot = sbias + (warp - 2) * 32;
-    Ring ring{stg + (warp - 2) * kStage, a.out_f32, 0};
+    // staging: both outputs' boxes (or one fp32 box) fill the warp's 4 KiB,
+    // one 16-bit output takes its two halves in turn
+    uint8_t* boxes = stg + (warp - 2) * kStage;
+    const int turns = a.out_f32 || p.tma_u ? 1 : 2;
+    int staged = 0;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int u = worker; u < p.units; u += workers) {
@@ -466,8 +392,10 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
       const int row0 = tm * TILE_M + (int)rank * 128 + quarter * 32;  // this warp's first row
       const long long m = (long long)row0 + lane;
       const bool row_ok = m < a.T;
-      const int n_end = min(a.N, tn * TILE_N + c_half + ACC / 2);
-      // what the epilogue reads beside the accumulator, a piece ahead
+      const int n_first = tn * TILE_N + c_first;
+      const int n_end = min(a.N, n_first + SPAN);
+      // what the epilogue reads beside the accumulator: requested before the
+      // wait for the accumulator, then as soon as the last piece's is used
       auto fetch = [&](int n0, Saved& s) {
         if (!row_ok || n0 >= n_end || a.splits > 1) return;
         if constexpr (BWD) {
@@ -477,11 +405,11 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
           if (a.res && !a.out_f32) load_row16(a.res, a.ldr, m, n0, a.N, s);
         }
       };
-      Saved next;
-      next.b = 0;
+      Saved cur;
+      cur.b = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) next.q[k] = make_uint4(0, 0, 0, 0);
-      fetch(tn * TILE_N + c_half, next);
+      for (int k = 0; k < 4; ++k) cur.q[k] = make_uint4(0, 0, 0, 0);
+      fetch(n_first, cur);
       const bool ready = PAIR ? ptx::mbar_wait_cluster_bounded(&tfull[acc], acc_phase, p.wait_ns,
                                                                p.err, DEVERR_TIMEOUT_EPILOGUE)
                               : ptx::mbar_wait_bounded(&tfull[acc], acc_phase, p.wait_ns, p.err,
@@ -491,22 +419,32 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
         break;
       }
       ptx::tc_fence_after();
-      for (int c0 = c_half; c0 < c_half + ACC / 2; c0 += 32) {
-        const int n0 = tn * TILE_N + c0;
-        if (n0 >= a.N) break;  // warp-uniform
-        const Saved cur = next;
-        if (c0 + 32 < c_half + ACC / 2) fetch(n0 + 32, next);
-        // a ragged last piece leaves from registers: the bulk store writes
-        // whole 16-byte units, so it would touch columns past N
-        const bool whole = n0 + 32 <= a.N;
-        uint32_t r[32];
+      // the accumulator goes back to the MMA issuer once this warp's last
+      // piece of it is in registers
+      auto release = [&] {
+        ptx::tc_fence_before();
         __syncwarp();
-        ptx::tmem_ld_32x32b_x32(
-            tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * ACC + c0), r);
-        ptx::tmem_ld_wait();
-        float v[32];
+        if (lane == 0) {
+          if (rank == 0) ptx::mbar_arrive(&tempty[acc]);
+          else ptx::mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
+        }
+      };
+      if (n_first >= a.N) release();
+#pragma unroll 1
+      for (int n0 = n_first; n0 < n_end; n0 += 32) {  // warp-uniform
+        F2 v[16];
+        {
+          uint32_t r[32];
+          __syncwarp();
+          ptx::tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(quarter * 32) << 16) +
+                                      (uint32_t)(acc * ACC + c_first + n0 - n_first),
+                                  r);
+          ptx::tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+          for (int j = 0; j < 16; ++j)
+            v[j] = f2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+        }
+        if (n0 + 32 >= n_end) release();
         if (a.splits > 1) {
           // raw sums: planes have whole 32-column pieces (ldp a multiple of 32)
           if (row_ok) {
@@ -514,99 +452,158 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
 #pragma unroll
             for (int k = 0; k < 8; ++k)
               reinterpret_cast<float4*>(pr)[k] =
-                  make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                  make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
           }
           continue;
         }
+        if (row0 >= a.T) continue;  // warp-uniform: no row of this warp exists
+
+        // A ragged last piece leaves from registers: the bulk store writes
+        // whole 16-byte units, so it would touch columns past N.
+        const int cols = a.N - n0;
+        const bool whole = cols >= 32;
+        const bool box_y = p.tma_y && whole, box_u = p.tma_u && whole;
+        uint8_t* box = boxes + (turns == 2 ? (staged & 1) * 2048 : 0);
+        if ((box_y || box_u) && staged >= turns) {
+          if (lane == 0) {
+            if (turns == 2) ptx::bulk_wait_group_read<1>();
+            else ptx::bulk_wait_group_read<0>();
+          }
+          __syncwarp();
+        }
+        const int n_ok = row_ok ? cols : 0;
+        const Sink to_y{box_y ? box + lane * (a.out_f32 ? 128 : 64) : nullptr,
+                        static_cast<uint8_t*>(a.y) + (m * a.ldy + n0) * (a.out_f32 ? 4 : 2),
+                        a.out_f32, lane, n_ok};
+        uint8_t* ubox = box + (p.tma_y ? 2048 : 0);
+        const Sink to_u{box_u ? ubox + lane * 64 : nullptr,
+                        static_cast<uint8_t*>(a.u_out) + (m * a.ldu_out + n0) * 2, 0, lane, n_ok};
+        const uint32_t* sw = reinterpret_cast<const uint32_t*>(cur.q);
+
         if constexpr (!BWD) {
           if (a.bias) {
-            __syncwarp();
-            bias_slot[lane] = n0 + lane < a.N ? __ldg(a.bias + n0 + lane) : 0.f;
-            __syncwarp();
+            if (whole) {
+              const float4* bp = reinterpret_cast<const float4*>(a.bias + n0);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float4 b4 = reinterpret_cast<const float4*>(bias_slot)[k];
-              v[4 * k] += b4.x;
-              v[4 * k + 1] += b4.y;
-              v[4 * k + 2] += b4.z;
-              v[4 * k + 3] += b4.w;
-            }
-          }
-          if (a.u_out) {
-            if (p.tma_u && whole) {
-              if (row0 < a.T) stage_store<H16>(ring, &tmU, 0, v, n0, row0, lane);
-            } else if (row_ok) {
-              store_row<H16>(a.u_out, a.ldu_out, 0, m, n0, a.N, v);
-            }
-          }
-          if (a.q && row_ok) store_row8(a, m, n0, v);
-          if (a.act != MLP_ACT_NONE) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = act_value<false>(v[j], a.act, a.slope);
-          }
-          if (a.res && row_ok) {
-            if (!a.out_f32) {
-              float rv[32];
-              saved16<H16>(cur, rv);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] += rv[j];
+              for (int k = 0; k < 8; ++k) {
+                const float4 b4 = __ldg(bp + k);
+                v[2 * k] = add2(v[2 * k], f2(b4.x, b4.y));
+                v[2 * k + 1] = add2(v[2 * k + 1], f2(b4.z, b4.w));
+              }
             } else {
-              const float* rp = static_cast<const float*>(a.res) + m * a.ldr + n0;
-              if (n0 + 32 <= a.N && (reinterpret_cast<uintptr_t>(rp) & 15) == 0) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float4 f = *(reinterpret_cast<const float4*>(rp) + k);
-                  v[4 * k] += f.x;
-                  v[4 * k + 1] += f.y;
-                  v[4 * k + 2] += f.z;
-                  v[4 * k + 3] += f.w;
-                }
-              } else {
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (n0 + j < a.N) v[j] += rp[j];
+              for (int j = 0; j < 16; ++j) {
+                if (2 * j < cols) v[j].x += __ldg(a.bias + n0 + 2 * j);
+                if (2 * j + 1 < cols) v[j].y += __ldg(a.bias + n0 + 2 * j + 1);
               }
             }
           }
-        } else {
-          float f[32];
-          if (a.act != MLP_ACT_NONE || a.u_out) {
-            float uv[32];
-            if (a.q) saved8(cur, uv);
-            else saved16<H16>(cur, uv);
+          if (a.q) {
+            if (!whole) {  // columns past N take no part in the group's scale
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= act_grad<false>(uv[j], a.act, a.slope, f[j]);
+              for (int j = 0; j < 16; ++j) {
+                if (2 * j >= cols) v[j].x = 0.f;
+                if (2 * j + 1 >= cols) v[j].y = 0.f;
+              }
+            }
+            uint32_t w[8];
+            const uint32_t b = ckpt8_group(reinterpret_cast<const float(&)[32]>(v), w);
+            if (row_ok) {
+              int8_t* qp = a.q + m * a.ldq + n0;
+              a.scale[m * a.lds + n0 / kCkptGroup] = (uint8_t)b;
+              if (whole && (reinterpret_cast<uintptr_t>(qp) & 15) == 0) {
+                reinterpret_cast<uint4*>(qp)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                reinterpret_cast<uint4*>(qp)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (j < cols) qp[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
+              }
+            }
           }
           if (a.u_out) {
-            if (p.tma_u && whole) {
-              if (row0 < a.T) stage_store<H16>(ring, &tmU, 0, f, n0, row0, lane);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              sink8<H16>(to_u, k, reinterpret_cast<const F2(&)[4]>(v[4 * k]));
+          }
+          with_act(a.act, [&](auto tag) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              v[j] = act_value2<decltype(tag)::value>(v[j], a.slope);
+          });
+          if (a.res) {
+            if (!a.out_f32) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] = add2(v[j], unpack2<H16>(sw[j]));
             } else if (row_ok) {
-              store_row<H16>(a.u_out, a.ldu_out, 0, m, n0, a.N, f);
+              const float* rp = static_cast<const float*>(a.res) + m * a.ldr + n0;
+              if (whole && (reinterpret_cast<uintptr_t>(rp) & 15) == 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float4 f = *(reinterpret_cast<const float4*>(rp) + k);
+                  v[2 * k] = add2(v[2 * k], f2(f.x, f.y));
+                  v[2 * k + 1] = add2(v[2 * k + 1], f2(f.z, f.w));
+                }
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  if (2 * j < cols) v[j].x += rp[2 * j];
+                  if (2 * j + 1 < cols) v[j].y += rp[2 * j + 1];
+                }
+              }
             }
           }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            sink8<H16>(to_y, k, reinterpret_cast<const F2(&)[4]>(v[4 * k]));
+        } else {
+          const float step = a.q ? ckpt8_step(cur.b) : 0.f;
+          with_act(a.act, [&](auto tag) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              F2 f[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                F2 uv;
+                if (a.q) {
+                  const uint32_t w = ckpt8_flip(sw[2 * k + j / 2]);
+                  uv = mul2(add2(f2(ckpt8_biased(w, 2 * (j & 1)),
+                                    ckpt8_biased(w, 2 * (j & 1) + 1)),
+                                 f2(-kCkptBias)),
+                            f2(step));
+                } else {
+                  uv = unpack2<H16>(sw[4 * k + j]);
+                }
+                v[4 * k + j] = mul2(
+                    v[4 * k + j], act_grad2<decltype(tag)::value>(uv, a.slope, f[j]));
+              }
+              if (a.u_out) sink8<H16>(to_u, k, f);
+              sink8<H16>(to_y, k, reinterpret_cast<const F2(&)[4]>(v[4 * k]));
+            }
+          });
         }
-        if (p.tma_y && whole) {
-          // rows past T are clipped by the store
-          if (row0 < a.T) stage_store<H16>(ring, &tmY, a.out_f32, v, n0, row0, lane);
-        } else if (row_ok) {
-          store_row<H16>(a.y, a.ldy, a.out_f32, m, n0, a.N, v);
+        fetch(n0 + 32, cur);
+        if (box_y || box_u) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            // rows past T are clipped by the stores
+            if (box_y) ptx::tma_store_2d(&tmY, box, n0, row0);
+            if (box_u) ptx::tma_store_2d(&tmU, ubox, n0, row0);
+            ptx::bulk_commit_group();
+          }
+          ++staged;
         }
         if constexpr (BWD) {
-          if (a.colpart && row0 < a.T) {  // warp-uniform
+          if (a.colpart) {
             if (!row_ok) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = 0.f;
+              for (int j = 0; j < 16; ++j) v[j] = f2(0.f);
             }
             const float s = column_sums(v, lane);
-            if (n0 + lane < a.N) a.colpart[(long long)(row0 / 32) * a.ldcp + n0 + lane] = s;
+            if (lane < cols) a.colpart[(long long)(row0 / 32) * a.ldcp + n0 + lane] = s;
           }
         }
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (rank == 0) ptx::mbar_arrive(&tempty[acc]);
-        else ptx::mbar_arrive_remote(tempty0 + (uint32_t)acc * 8u);
       }
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
@@ -638,7 +635,8 @@ __device__ __forceinline__ void linear_body(const CUtensorMap& tmA, const CUtens
 }
 
 template <int STAGES, int H16, int BWD>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1)
+    __launch_bounds__(LinLayout<1, 256, STAGES>::THREADS, 1)
     linear_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmY,
@@ -648,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 template <int BN, int STAGES, int H16, int BWD>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(LinLayout<0, BN, STAGES>::THREADS, 1)
     linear_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmU,
                   const __grid_constant__ LinParams p) {
@@ -704,7 +702,7 @@ mlp_status launch_single(const CUtensorMap (&tm)[4], const LinParams& p, cudaStr
   if (configured != cudaSuccess) return MLP_ERR_CUDA;
   const int grid = p.units < num_sms() ? p.units : num_sms();
   LaunchScope ls(BWD ? "linear_bwd" : "linear_fwd", st, p.a.T, p.a.N, p.a.K);
-  launch_k(linear_kernel<BN, STAGES, H16, BWD>, dim3(grid), dim3(kThreads), L::SMEM, st, tm[0],
+  launch_k(linear_kernel<BN, STAGES, H16, BWD>, dim3(grid), dim3(L::THREADS), L::SMEM, st, tm[0],
            tm[1], tm[2], tm[3], p);
   return launch_status();
 }
@@ -720,7 +718,7 @@ mlp_status launch_pair(const CUtensorMap (&tm)[4], const LinParams& p, cudaStrea
       return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(L::THREADS);
     cfg.dynamicSmemBytes = L::SMEM;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
@@ -732,7 +730,7 @@ mlp_status launch_pair(const CUtensorMap (&tm)[4], const LinParams& p, cudaStrea
   if (max_pairs < 1) return MLP_ERR_CUDA;
   const int pairs = p.units < max_pairs ? p.units : max_pairs;
   LaunchScope ls(BWD ? "linear_bwd_pair" : "linear_fwd_pair", st, p.a.T, p.a.N, p.a.K);
-  launch_k(kernel, dim3(2 * pairs), dim3(kThreads), L::SMEM, st, tm[0], tm[1], tm[2], tm[3], p);
+  launch_k(kernel, dim3(2 * pairs), dim3(L::THREADS), L::SMEM, st, tm[0], tm[1], tm[2], tm[3], p);
   return launch_status();
 }
 
@@ -787,7 +785,8 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
         return MLP_ERR_CUDA;
       p.tma_y = 1;
     }
-    if (a.u_out && a.ldu_out * 2 % 16 == 0 && aligned16(a.u_out)) {
+    // (an fp32 box leaves no room for a second one)
+    if (a.u_out && !a.out_f32 && a.ldu_out * 2 % 16 == 0 && aligned16(a.u_out)) {
       if (!encode_tmap_out_2d(&maps[3], a.u_out, 0, a.N, a.T, (unsigned long long)a.ldu_out * 2,
                               32, 32))
         return MLP_ERR_CUDA;

@@ -44,17 +44,23 @@ __device__ __forceinline__ float epi_finish(const LinearArgs& a, long long m, in
     v += bias;
     if (a.u_out && ok) from_f32(v, static_cast<T*>(a.u_out)[m * a.ldu_out + c]);
     if (a.q) {
-      const uint32_t b =
-          ckpt8_byte(__reduce_max_sync(0xffffffffu, ok ? abs_bits(v) : 0u));
+      const uint32_t top =
+          __reduce_max_sync(0xffffffffu, ok ? __float_as_uint(v) & 0x7fffffffu : 0u);
+      const uint32_t b = ckpt8_byte(top);
+      const float held = ckpt8_must_hold(top) ? ckpt8_hold(v, ckpt8_step(b)) : v;
       if (ok)
         a.q[m * a.ldq + c] =
-            b == kCkptNanByte ? (int8_t)0 : (int8_t)ckpt8_q(v, ckpt8_inv_step(b));
+            b == kCkptNanByte ? (int8_t)0 : (int8_t)ckpt8_q(held, ckpt8_inv_step(b));
       if ((c & (kCkptGroup - 1)) == 0 && ok) a.scale[m * a.lds + c / kCkptGroup] = (uint8_t)b;
     }
-    v = act_value<ACC>(v, a.act, a.slope) + extra;
+    with_act(a.act, [&](auto tag) {
+      v = act_value_of<ACC, decltype(tag)::value>(v, a.slope) + extra;
+    });
   } else if (a.act != MLP_ACT_NONE || a.u_out) {
-    float f;
-    v *= act_grad<ACC>(extra, a.act, a.slope, f);
+    float f = 0.f;
+    with_act(a.act, [&](auto tag) {
+      v *= act_grad_of<ACC, decltype(tag)::value>(extra, a.slope, f);
+    });
     if (a.u_out && ok) from_f32(f, static_cast<T*>(a.u_out)[m * a.ldu_out + c]);
   }
   if (ok) {
