@@ -5,7 +5,8 @@
 //   MLP_ACT_GELU_TANH       u (1 + tanh z) / 2 = u / (1 + e^(-2z)),
 //                           z = sqrt(2 / pi) (u + 0.044715 u^3)
 //   MLP_ACT_SILU            u / (1 + e^(-u))
-// ACC = true (fp32 layers) uses the CUDA library functions.  ACC = false
+// ACC = true (fp32 layers) uses the CUDA library's functions (and its two-ulp
+// division).  ACC = false
 // (16-bit layers, where the activation's instructions bound the epilogue of
 // short-K products) works on two values at a time with the packed fp32
 // instructions, the hardware exponential and reciprocal (a few 2^-23
@@ -161,9 +162,9 @@ __device__ __forceinline__ float act_value_of(float u, float slope) {
   } else if constexpr (ACT == MLP_ACT_GELU) {
     return u * 0.5f * erfcf(-0.70710678118654752f * u);
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
-    return u / (1.f + expf(-kTanhScale * fmaf(kTanhCubic * u * u, u, u)));
+    return __fdividef(u, 1.f + expf(-kTanhScale * fmaf(kTanhCubic * u * u, u, u)));
   } else {
-    return u / (1.f + expf(-u));
+    return __fdividef(u, 1.f + expf(-u));
   }
 }
 
@@ -183,12 +184,12 @@ __device__ __forceinline__ float act_grad_of(float u, float slope, float& value)
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
     const float c = copysignf(abs_upto(u, kGaussEnd), u);
     const float c2 = kTanhCubic * c * c;
-    const float s = 1.f / (1.f + expf(-kTanhScale * fmaf(c2, c, c)));
+    const float s = __fdividef(1.f, 1.f + expf(-kTanhScale * fmaf(c2, c, c)));
     value = u * s;
     return fmaf(c * s * (1.f - s), kTanhScale * fmaf(3.f, c2, 1.f), s);
   } else {
     const float c = copysignf(abs_upto(u, kLogisticEnd), u);
-    const float s = 1.f / (1.f + expf(-c));
+    const float s = __fdividef(1.f, 1.f + expf(-c));
     value = u * s;
     return fmaf(c * s, 1.f - s, s);
   }

@@ -143,12 +143,11 @@ mlp_status mlp_layernorm_bwd(const void* dy, int dtype, int lddy, const void* x,
 namespace {
 
 // How a product [T][K] x [K][N] runs, and its workspace: raw sums of the paths
-// that finish in a second pass, then (backward) the partial column sums and
-// the scratch of their reduction.
+// that finish in a second pass, then (backward) the partial column sums.
 struct LinearPath {
   bool few;      // launch_linear_few: no workspace
   int splits;    // planes of raw sums (0: the epilogue is in the product's kernel)
-  size_t sums, part, red;
+  size_t sums, part;
   long long ldp, ldcp;
 };
 
@@ -164,10 +163,8 @@ LinearPath linear_path(long long T, int K, int N, int dtype, bool bwd) {
   p.ldp = (N + 31) / 32 * 32;  // whole pieces of the tensor-core kernel
   p.sums = align256((size_t)p.splits * T * p.ldp * 4);
   if (bwd) {
-    p.ldcp = (N + 3) / 4 * 4;
-    const long long rows = linear_part_rows(T);
-    p.part = align256((size_t)rows * p.ldcp * 4);
-    p.red = align256(colsum_workspace_bytes((int)rows, N));
+    p.ldcp = (N + 31) / 32 * 32;  // whole 128-byte lines
+    p.part = align256((size_t)linear_part_rows(T) * p.ldcp * 4);
   }
   return p;
 }
@@ -199,8 +196,8 @@ mlp_status run_linear(LinearArgs a, const LinearPath& lp, bool bwd, float* dbias
   }
   if (lp.splits) MLP_CHECK(launch_linear_finish(a, bwd, false, st));
   if (!dbias) return MLP_OK;
-  return launch_colsum(a.colpart, MLP_DTYPE_F32, (int)linear_part_rows(a.T), a.N, (int)a.ldcp,
-                       dbias, ws + lp.sums + lp.part, st);
+  return launch_partial_sums(a.colpart, linear_part_rows(a.T), a.N, a.ldcp, dbias, a.N, nullptr,
+                             st);
 }
 
 // The shapes and types that a product's entry points share.
@@ -255,7 +252,7 @@ mlp_status mlp_linear_fwd(const void* x, int ldx, const void* w, int ldw, int T,
 size_t mlp_linear_bwd_workspace_bytes(int T, int d_in, int d_out, int dtype) {
   if (T <= 0 || d_in <= 0 || d_out <= 0 || !float_dtype(dtype)) return 0;
   const LinearPath lp = linear_path(T, d_out, d_in, dtype, true);
-  return lp.sums + lp.part + lp.red;
+  return lp.sums + lp.part;
 }
 
 mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int T, int d_in,
@@ -274,7 +271,7 @@ mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int 
   if (!all_aligned(dy, w, u, u_q, u_scale, du, a_out, workspace)) return MLP_ERR_MISALIGNED;
   if (dtype != MLP_DTYPE_F32 && (lddy % 8 != 0 || ldw % 8 != 0)) return MLP_ERR_MISALIGNED;
   const LinearPath lp = linear_path(T, d_out, d_in, dtype, true);
-  const size_t need = lp.sums + (dbias ? lp.part + lp.red : 0);
+  const size_t need = lp.sums + (dbias ? lp.part : 0);
   if (need > 0 && (!workspace || ws_bytes < need)) return MLP_ERR_INVALID_ARG;
   LinearArgs a{};
   a.dtype = dtype;
@@ -293,9 +290,7 @@ mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int 
 
 size_t mlp_act_bwd_workspace_bytes(int T, int n) {
   if (T <= 0 || n <= 0) return 0;
-  const long long rows = linear_part_rows(T);
-  return align256((size_t)rows * ((n + 3) / 4 * 4) * 4) +
-         align256(colsum_workspace_bytes((int)rows, n));
+  return align256((size_t)linear_part_rows(T) * ((n + 31) / 32 * 32) * 4);
 }
 
 mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int act, float slope,
@@ -325,14 +320,12 @@ mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int ac
   a.q = const_cast<int8_t*>(u_q); a.ldq = ldq;
   a.scale = const_cast<uint8_t*>(u_scale); a.lds = lds;
   a.splits = 1;
-  a.ldcp = (n + 3) / 4 * 4;
+  a.ldcp = (n + 31) / 32 * 32;
   a.colpart = dbias ? static_cast<float*>(workspace) : nullptr;
   MLP_CHECK(launch_linear_finish(a, true, true, S(stream)));
   if (!dbias) return MLP_OK;
-  const long long rows = linear_part_rows(T);
-  return launch_colsum(a.colpart, MLP_DTYPE_F32, (int)rows, n, (int)a.ldcp, dbias,
-                       static_cast<uint8_t*>(workspace) + align256((size_t)rows * a.ldcp * 4),
-                       S(stream));
+  return launch_partial_sums(a.colpart, linear_part_rows(T), n, a.ldcp, dbias, n, nullptr,
+                             S(stream));
 }
 
 }  // extern "C"

@@ -68,10 +68,10 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* part, int slot, 
 }
 
 // N parameter values (fp32) from column c, `fill` past n values or without a vector.
-template <int N>
+template <int N, bool FULL = false>
 __device__ __forceinline__ void load_param(const float* p, int c, int n, bool vec, float fill,
                                            float (&v)[N]) {
-  if (p && vec && n >= N) {
+  if (p && (FULL ? n > 0 : vec && n >= N)) {
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
       const float4 f = __ldg(reinterpret_cast<const float4*>(p + c + j));
@@ -83,11 +83,11 @@ __device__ __forceinline__ void load_param(const float* p, int c, int n, bool ve
     return;
   }
 #pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = p && j < n ? __ldg(p + c + j) : fill;
+  for (int j = 0; j < N; ++j) v[j] = !FULL && p && j < n ? __ldg(p + c + j) : fill;
 }
 
 // The 8-bit form of a piece at column c of a row (its group's lanes together).
-template <typename T>
+template <typename T, bool FULL = false>
 __device__ __forceinline__ void store_ckpt(const float (&v)[RowVec<T>::N], int8_t* qrow,
                                            uint8_t* srow, int c, int n, bool vec) {
   constexpr int N = RowVec<T>::N, LANES = kCkptGroup / N;
@@ -98,15 +98,19 @@ __device__ __forceinline__ void store_ckpt(const float (&v)[RowVec<T>::N], int8_
   uint32_t w[N / 4];
   const uint32_t b = ckpt8_piece(v, amax, w);
   if (n > 0) {
-    store_q<N>(qrow + c, n, vec, w);
+    store_q<N, FULL>(qrow + c, n, vec, w);
     if ((threadIdx.x & (LANES - 1)) == 0) srow[c / kCkptGroup] = (uint8_t)b;
   }
 }
 
 // ------------------------------------------------------------ forward
 
-template <typename T, int WPR>
-__global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_fwd_kernel(const LayerNormFwd p) {
+// Registers: 64 per thread (128 for fp32 rows, whose pieces are twice as many)
+// keep 32 (16) warps on an SM, each with its next row in flight.
+template <typename T, int WPR, bool FULL>
+__global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
+                                  (sizeof(T) == 2 ? 1024 : 512) / HeldBlock<WPR>::THREADS)
+    ln_fwd_kernel(const LayerNormFwd p) {
   constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
   __shared__ float part[2][ROWS][WPR];
   pdl_wait();
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_fwd_kernel(const L
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N;
-      raw[i] = load_piece(x + r * p.ldx + c, r < p.T ? p.d - c : 0, p.x_vec);
+      raw[i] = load_piece_of<FULL>(x + r * p.ldx + c, r < p.T ? p.d - c : 0, p.x_vec);
     }
   };
   load(row);
@@ -158,13 +162,13 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_fwd_kernel(const L
       const int c = (i * 32 * WPR + t) * N;
       const int n = p.d - c;
       if (p.q)
-        store_ckpt<T>(v[i], p.q + row * p.ldq, p.scale + row * p.lds, c, n, p.q_vec);
+        store_ckpt<T, FULL>(v[i], p.q + row * p.ldq, p.scale + row * p.lds, c, n, p.q_vec);
       float a[N], b[N];
-      load_param<N>(p.gain, c, n, p.p_vec, 1.f, a);
-      load_param<N>(p.shift, c, n, p.p_vec, 0.f, b);
+      load_param<N, FULL>(p.gain, c, n, p.p_vec, 1.f, a);
+      load_param<N, FULL>(p.shift, c, n, p.p_vec, 0.f, b);
 #pragma unroll
       for (int j = 0; j < N; ++j) v[i][j] = fmaf((v[i][j] - mu) * rho, a[j], b[j]);
-      store_piece(static_cast<T*>(p.y) + row * p.ldy + c, v[i], n, p.y_vec);
+      store_piece_of<FULL>(static_cast<T*>(p.y) + row * p.ldy + c, v[i], n, p.y_vec);
     }
   }
 }
@@ -226,17 +230,17 @@ __global__ void __launch_bounds__(kLoopThreads) ln_fwd_wide_kernel(const LayerNo
 
 // A piece of the forward's input: its raw 16 bytes, or the 8-bit words and the
 // group's scale byte.
-template <typename T, bool CK>
+template <typename T, bool CK, bool FULL = false>
 struct XPiece {
   static constexpr int N = RowVec<T>::N;
   uint4 raw;
   uint32_t w[N / 4], b;
   __device__ __forceinline__ void load(const LayerNormBwd& p, long long row, int c, int n) {
     if constexpr (CK) {
-      load_q<N>(p.q + row * p.ldq + c, n, p.q_vec, w);
+      load_q<N, FULL>(p.q + row * p.ldq + c, n, p.q_vec, w);
       b = n > 0 ? p.scale[row * p.lds + c / kCkptGroup] : 0u;
     } else {
-      raw = load_piece(static_cast<const T*>(p.x) + row * p.ldx + c, n, p.x_vec);
+      raw = load_piece_of<FULL>(static_cast<const T*>(p.x) + row * p.ldx + c, n, p.x_vec);
     }
   }
   __device__ __forceinline__ void values(float (&v)[N]) const {
@@ -259,8 +263,10 @@ struct XPiece {
 // columns), are added over the block's row slots in order at the end, and
 // leave as one row of partial sums per block: no atomics, so the gradients
 // are the same in every run.
-template <typename T, int WPR, bool CK>
-__global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_bwd_kernel(const LayerNormBwd p) {
+template <typename T, int WPR, bool CK, bool FULL>
+__global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
+                                  sizeof(T) == 2 ? 512 / HeldBlock<WPR>::THREADS : 1)
+    ln_bwd_kernel(const LayerNormBwd p) {
   constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
   __shared__ float part[2][ROWS][2 * WPR];
   extern __shared__ float sums[];  // ROWS > 1: one slot's values at a time
@@ -271,23 +277,21 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_bwd_kernel(const L
   long long row = (long long)blockIdx.x * ROWS + slot;
   const float inv_d = 1.f / (float)p.d;
   const T* dy = static_cast<const T*>(p.dy);
-  float gain[NV][N], dg[NV][N], ds[NV][N];
+  const T* dres = static_cast<const T*>(p.dres);
+  float dg[NV][N], ds[NV][N];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * 32 * WPR + t) * N;
-    load_param<N>(p.gain, c, p.d - c, p.p_vec, 1.f, gain[i]);
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) dg[i][j] = ds[i][j] = 0.f;
-  }
   uint4 rdy[NV];
-  XPiece<T, CK> rx[NV];
+  XPiece<T, CK, FULL> rx[NV];
   float mu_n = 0.f, rho_n = 0.f;
   auto load = [&](long long r) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N;
       const int n = r < p.T ? p.d - c : 0;
-      rdy[i] = load_piece(dy + r * p.lddy + c, n, p.dy_vec);
+      rdy[i] = load_piece_of<FULL>(dy + r * p.lddy + c, n, p.dy_vec);
       rx[i].load(p, r, c, n);
     }
     if (r < p.T) {
@@ -303,7 +307,9 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_bwd_kernel(const L
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int n = p.d - (i * 32 * WPR + t) * N;
+      const int c = (i * 32 * WPR + t) * N, n = p.d - c;
+      float gain[N];  // from L1: as registers they would cost a block per SM
+      load_param<N, FULL>(p.gain, c, n, p.p_vec, 1.f, gain);
       unpack_piece<T>(rdy[i], g[i]);
       rx[i].values(xh[i]);
 #pragma unroll
@@ -313,9 +319,17 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_bwd_kernel(const L
         xh[i][j] = j < n ? (xh[i][j] - mu) * rho : 0.f;
         dg[i][j] = fmaf(g[i][j], xh[i][j], dg[i][j]);
         ds[i][j] += g[i][j];
-        g[i][j] *= gain[i][j];
+        g[i][j] *= gain[j];
         s[0] += g[i][j];
         s[1] = fmaf(g[i][j], xh[i][j], s[1]);
+      }
+    }
+    uint4 rr[NV];  // this row's residual gradient, in flight over the reductions
+    if (dres) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * 32 * WPR + t) * N;
+        rr[i] = load_piece_of<FULL>(dres + row * p.ldr + c, p.d - c, p.r_vec);
       }
     }
     load(row + stride);
@@ -326,15 +340,13 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS) ln_bwd_kernel(const L
       const int c = (i * 32 * WPR + t) * N;
 #pragma unroll
       for (int j = 0; j < N; ++j) g[i][j] = rho * (g[i][j] - fmaf(xh[i][j], m2, m1));
-      if (p.dres) {
+      if (dres) {
         float r[N];
-        unpack_piece<T>(load_piece(static_cast<const T*>(p.dres) + row * p.ldr + c, p.d - c,
-                                   p.r_vec),
-                        r);
+        unpack_piece<T>(rr[i], r);
 #pragma unroll
         for (int j = 0; j < N; ++j) g[i][j] += r[j];
       }
-      store_piece(static_cast<T*>(p.dx) + row * p.lddx + c, g[i], p.d - c, p.dx_vec);
+      store_piece_of<FULL>(static_cast<T*>(p.dx) + row * p.lddx + c, g[i], p.d - c, p.dx_vec);
     }
   }
   // this block's partial sums, row slots added in order
@@ -460,53 +472,42 @@ __global__ void __launch_bounds__(256) ln_bwd_wide_sums_kernel(const LayerNormBw
     }
 }
 
-// dgain and dshift from the partial rows, in a fixed order: 32 columns per
-// block, one per lane (coalesced rows of 128 bytes), the rows dealt over 32
-// warps whose sums are added in warp order.
-__global__ void __launch_bounds__(1024) ln_bwd_sums_kernel(const float* __restrict__ part,
-                                                           int blocks, int d,
-                                                           float* __restrict__ dgain,
-                                                           float* __restrict__ dshift) {
-  __shared__ float s[32][33];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long c = (long long)blockIdx.x * 32 + lane;
-  float a = 0.f;
-  if (c < 2ll * d) {
-#pragma unroll 4
-    for (int r = w; r < blocks; r += 32) a += part[(long long)r * 2 * d + c];
-  }
-  s[w][lane] = a;
-  __syncthreads();
-  if (w != 0 || c >= 2ll * d) return;
-#pragma unroll
-  for (int r = 1; r < 32; ++r) a += s[r][lane];
-  if (c < d) dgain[c] = a;
-  else dshift[c - d] = a;
-}
-
 // ------------------------------------------------------------ launches
 
 bool row_vec(const void* p, long long ld, int esz, int bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * esz % bytes == 0;
 }
 
-// Blocks of a row-walking launch: enough for every SM to be full, at most one
-// per row set.
-int walk_blocks(long long T, int rows_per_block, int per_sm) {
+// Blocks of a row-walking launch: as many as are resident at once (more would
+// run as a second, ragged wave), at most one per row set.
+template <typename K>
+int walk_blocks(K kernel, int threads, int* per_sm, long long T, int rows_per_block) {
+  if (*per_sm == 0) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess) {
+      cudaGetLastError();
+      n = 1;
+    }
+    *per_sm = n > 0 ? n : 1;
+  }
   const long long need = (T + rows_per_block - 1) / rows_per_block;
-  const long long most = (long long)num_sms() * per_sm;
+  const long long most = (long long)num_sms() * *per_sm;
   return (int)(need < most ? need : most);
+}
+
+template <typename T, int WPR, bool FULL>
+mlp_status fwd_held_of(const LayerNormFwd& p, cudaStream_t st) {
+  using B = HeldBlock<WPR>;
+  static int per_sm = 0;
+  const int blocks = walk_blocks(ln_fwd_kernel<T, WPR, FULL>, B::THREADS, &per_sm, p.T, B::ROWS);
+  launch_k(ln_fwd_kernel<T, WPR, FULL>, dim3(blocks), dim3(B::THREADS), 0, st, p);
+  return launch_status();
 }
 
 template <typename T, int WPR>
 mlp_status fwd_held(const LayerNormFwd& p, cudaStream_t st) {
-  using B = HeldBlock<WPR>;
-  const int per_sm = 2048 / B::THREADS;
-  launch_k(ln_fwd_kernel<T, WPR>, dim3(walk_blocks(p.T, B::ROWS, per_sm)), dim3(B::THREADS), 0, st,
-           p);
-  return launch_status();
+  const bool full = p.d % RowVec<T>::N == 0 && p.x_vec && p.y_vec && p.p_vec && (!p.q || p.q_vec);
+  return full ? fwd_held_of<T, WPR, true>(p, st) : fwd_held_of<T, WPR, false>(p, st);
 }
 
 template <typename T>
@@ -521,28 +522,41 @@ mlp_status fwd_t(LayerNormFwd p, cudaStream_t st) {
   if (p.d <= 2048) return fwd_held<T, 4>(p, st);
   if (p.d <= 4096) return fwd_held<T, 8>(p, st);
   if (p.d <= kHeldWidth) return fwd_held<T, 16>(p, st);
-  launch_k(ln_fwd_wide_kernel<T>, dim3(walk_blocks(p.T, 1, 2048 / kLoopThreads)),
-           dim3(kLoopThreads), 0, st, p);
+  static int per_sm = 0;
+  const int blocks = walk_blocks(ln_fwd_wide_kernel<T>, kLoopThreads, &per_sm, p.T, 1);
+  launch_k(ln_fwd_wide_kernel<T>, dim3(blocks), dim3(kLoopThreads), 0, st, p);
   return launch_status();
 }
 
-template <typename T, int WPR, bool CK>
-mlp_status bwd_held(const LayerNormBwd& p, int blocks, cudaStream_t st) {
-  using B = HeldBlock<WPR>;
-  const size_t smem = B::ROWS > 1 ? (size_t)32 * WPR * kPerThread * 4 : 0;
-  LaunchScope ls("layernorm_bwd", st, p.T, p.d, sizeof(T));
-  launch_k(ln_bwd_kernel<T, WPR, CK>, dim3(blocks), dim3(B::THREADS), smem, st, p);
-  return launch_status();
-}
-
-// Partial rows of a backward launch (also sizes its workspace, so it depends
-// on the sizes alone): 304 blocks of 8 row slots (or of one wide row) are two
-// per SM; more would read and write more partial sums than they save.
+// The most partial rows of a backward launch (sizes its workspace, so it
+// depends on the sizes alone): 304 blocks of 256 threads are two per SM, all
+// that the registers hold.  Launches take as many of them as are resident.
 constexpr int kBwdBlocks = 304;
 int bwd_blocks(long long T, int d) {
   const int rows = d <= 512 ? 8 : d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
   const long long need = (T + rows - 1) / rows;
   return (int)(need < kBwdBlocks ? need : kBwdBlocks);
+}
+
+template <typename T, int WPR, bool CK, bool FULL>
+mlp_status bwd_held_of(const LayerNormBwd& p, int* blocks, cudaStream_t st) {
+  using B = HeldBlock<WPR>;
+  static int per_sm = 0;
+  const int resident =
+      walk_blocks(ln_bwd_kernel<T, WPR, CK, FULL>, B::THREADS, &per_sm, p.T, B::ROWS);
+  if (resident < *blocks) *blocks = resident;
+  const size_t smem = B::ROWS > 1 ? (size_t)32 * WPR * kPerThread * 4 : 0;
+  LaunchScope ls("layernorm_bwd", st, p.T, p.d, sizeof(T));
+  launch_k(ln_bwd_kernel<T, WPR, CK, FULL>, dim3(*blocks), dim3(B::THREADS), smem, st, p);
+  return launch_status();
+}
+
+template <typename T, int WPR, bool CK>
+mlp_status bwd_held(const LayerNormBwd& p, int* blocks, cudaStream_t st) {
+  const bool full = p.d % RowVec<T>::N == 0 && p.dy_vec && p.dx_vec && p.p_vec &&
+                    (!p.dres || p.r_vec) && (CK ? p.q_vec : p.x_vec);
+  return full ? bwd_held_of<T, WPR, CK, true>(p, blocks, st)
+              : bwd_held_of<T, WPR, CK, false>(p, blocks, st);
 }
 
 template <typename T, bool CK>
@@ -553,16 +567,18 @@ mlp_status bwd_t(LayerNormBwd p, cudaStream_t st) {
   p.r_vec = row_vec(p.dres, p.ldr, sizeof(T), 16);
   p.dx_vec = row_vec(p.dx, p.lddx, sizeof(T), 16);
   p.p_vec = row_vec(p.gain, 0, 4, 16);
-  const int blocks = bwd_blocks(p.T, p.d);
-  if (p.d <= 512) MLP_CHECK((bwd_held<T, 1, CK>(p, blocks, st)));
-  else if (p.d <= 1024) MLP_CHECK((bwd_held<T, 2, CK>(p, blocks, st)));
-  else if (p.d <= 2048) MLP_CHECK((bwd_held<T, 4, CK>(p, blocks, st)));
-  else if (p.d <= 4096) MLP_CHECK((bwd_held<T, 8, CK>(p, blocks, st)));
-  else if (p.d <= kHeldWidth) MLP_CHECK((bwd_held<T, 16, CK>(p, blocks, st)));
+  int blocks = bwd_blocks(p.T, p.d);
+  if (p.d <= 512) MLP_CHECK((bwd_held<T, 1, CK>(p, &blocks, st)));
+  else if (p.d <= 1024) MLP_CHECK((bwd_held<T, 2, CK>(p, &blocks, st)));
+  else if (p.d <= 2048) MLP_CHECK((bwd_held<T, 4, CK>(p, &blocks, st)));
+  else if (p.d <= 4096) MLP_CHECK((bwd_held<T, 8, CK>(p, &blocks, st)));
+  else if (p.d <= kHeldWidth) MLP_CHECK((bwd_held<T, 16, CK>(p, &blocks, st)));
   else {
     {
       LaunchScope ls("layernorm_bwd_wide", st, p.T, p.d, sizeof(T));
-      launch_k(ln_bwd_wide_kernel<T, CK>, dim3(walk_blocks(p.T, 1, 2048 / kLoopThreads)),
+      static int per_sm = 0;
+      launch_k(ln_bwd_wide_kernel<T, CK>,
+               dim3(walk_blocks(ln_bwd_wide_kernel<T, CK>, kLoopThreads, &per_sm, p.T, 1)),
                dim3(kLoopThreads), 0, st, p);
       MLP_CHECK(launch_status());
     }
@@ -572,10 +588,7 @@ mlp_status bwd_t(LayerNormBwd p, cudaStream_t st) {
              0, st, p);
     MLP_CHECK(launch_status());
   }
-  LaunchScope ls("layernorm_bwd_sums", st, blocks, p.d);
-  launch_k(ln_bwd_sums_kernel, dim3((2 * p.d + 31) / 32), dim3(1024), 0, st,
-           static_cast<const float*>(p.part), blocks, p.d, p.dgain, p.dshift);
-  return launch_status();
+  return launch_partial_sums(p.part, blocks, 2 * p.d, 2 * p.d, p.dgain, p.d, p.dshift, st);
 }
 
 template <typename T>

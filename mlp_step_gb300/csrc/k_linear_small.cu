@@ -73,6 +73,7 @@ __device__ __forceinline__ float epi_finish(const LinearArgs& a, long long m, in
 // ------------------------------------------------------------ epilogue pass
 
 constexpr int kRowsAhead = 4;  // rows loaded before the first is finished
+constexpr int kUnitRows = 32;  // rows of a backward unit (one row of colpart)
 
 // Warp unit: `unit_rows` rows of 32 columns; in the backward 32 rows, whose
 // column sums it adds in row order into one row of colpart.
@@ -119,19 +120,28 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
 
 // ------------------------------------------------------------ a few rows
 //
-// Up to 8 rows: bound by reading W once.  A cluster of S CTAs takes 64 output
-// columns, each CTA one slice of K; the S partial results meet in distributed
-// shared memory and the cluster's warps run the epilogue, so the call is one
-// launch without a workspace.  Each CTA: 256 threads, 16-byte loads of W
-// straight to registers (every element is used by this CTA alone; shared
-// memory would only add a hop), the rows of x in shared memory as fp32.
+// Up to 8 rows: bound by reading W once.  A cluster of S CTAs takes 64 or 128
+// output columns, each CTA one slice of K; the S partial results meet in
+// distributed shared memory and the cluster's warps run the epilogue, so the
+// call is one launch without a workspace.  Each CTA: 256 threads, 16-byte
+// loads of W straight to registers (every element is used by this CTA alone;
+// shared memory would only add a hop), the rows of x in shared memory as fp32.
 //   forward, W [K][N]: a thread keeps 16 bytes of columns and walks down K
-//   (128-byte runs of W per 64 columns);
+//   (256-byte runs of W per 128 columns), the next loads in flight while the
+//   last are used;
 //   backward, W [N][K]: a warp keeps 8 of the 64 columns and its lanes walk
 //   along K.
+// All CTAs of a launch are resident at once: a second wave of a few would
+// double the time.
 
-constexpr int kFewCols = 64;
-constexpr int kFewChunk = 512;  // K values of x staged at a time
+constexpr int kFewX = 4096;  // values of x staged at a time (all rows)
+
+// CTAs that an SM holds (by registers), and the K values staged at a time.
+template <int MT, bool BWD>
+struct FewShape {
+  static constexpr int kPerSm = (MT == 1 ? 4 : MT == 2 ? 3 : MT == 4 ? 3 : 2) - (BWD ? 1 : 0);
+  static constexpr int kChunk = kFewX / MT;
+};
 
 // Sums of V <= 32 values over the warp's lanes: lane L gets that of value
 // L % V.  Halving rounds as in a transposition, then a butterfly.
@@ -158,23 +168,23 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
-template <typename T, int MT, bool BWD>
-__global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a, int cluster,
-                                                              int slice, int w_vec,
-                                                              float* dbias) {
+template <typename T, int MT, bool BWD, int COLS>
+__global__ void __launch_bounds__(kThreads, FewShape<MT, BWD>::kPerSm)
+    linear_few_kernel(const LinearArgs a, int cluster, int slice, int w_vec, float* dbias) {
   constexpr int N = RowVec<T>::N;
-  constexpr int LPR = kFewCols / N;      // forward: lanes across the 64 columns
-  constexpr int KP = kThreads / LPR;     // forward: rows of W per step
-  constexpr int U = 8;                   // loads in flight per thread
-  static_assert(kFewChunk % (KP * U) == 0 || KP * U % kFewChunk == 0, "chunking");
-  __shared__ float xs[kFewChunk * MT];               // forward [k][MT], backward [MT][k]
-  __shared__ float red[BWD ? 1 : 8 * MT * kFewCols]; // forward: [warp][MT][64]
-  __shared__ float part[MT * kFewCols];              // this CTA's sums, read by the cluster
+  constexpr int LPR = COLS / N < 32 ? COLS / N : 32;  // forward: lanes across the columns
+  constexpr int KP = kThreads / LPR;                  // forward: rows of W per step
+  constexpr int U = 4;                                // loads a thread issues together
+  constexpr int CHUNK = FewShape<MT, BWD>::kChunk;
+  static_assert(LPR * N == COLS && (!BWD || COLS == 64), "columns of a CTA");
+  __shared__ __align__(16) float xs[CHUNK * MT];   // forward [k][MT], backward [MT][k]
+  __shared__ float red[BWD ? 1 : 8 * MT * COLS];   // forward: [warp][MT][COLS]
+  __shared__ float part[MT * COLS];                // this CTA's sums, read by the cluster
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % cluster;
-  const int c0 = (int)(blockIdx.x / cluster) * kFewCols;
+  const int c0 = (int)(blockIdx.x / cluster) * COLS;
   const int k_lo = rank * slice, k_hi = min(a.K, k_lo + slice);
   const T* x = static_cast<const T*>(a.x);
   const T* w = static_cast<const T*>(a.w);
@@ -186,31 +196,44 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a
 #pragma unroll
     for (int j = 0; j < V; ++j) acc[m][j] = 0.f;
 
-  for (int kc = k_lo; kc < k_hi; kc += kFewChunk) {
-    const int len = min(kFewChunk, k_hi - kc);
-    __syncthreads();  // the previous chunk has been read
-    for (int i = tid; i < kFewChunk * MT; i += kThreads) {
-      const int m = i / kFewChunk, k = i % kFewChunk;  // coalesced along k
-      const float v = m < a.T && k < len ? to_f32(x[m * a.ldx + kc + k]) : 0.f;
-      xs[BWD ? m * kFewChunk + k : k * MT + m] = v;
-    }
-    __syncthreads();
+  for (int kc = k_lo; kc < k_hi; kc += CHUNK) {
+    const int len = min(CHUNK, k_hi - kc);
+    if (kc > k_lo) __syncthreads();  // the previous chunk has been read
+    auto stage_x = [&] {
+#pragma unroll 4
+      for (int i = tid; i < len * MT; i += kThreads) {
+        const int m = MT == 1 ? 0 : i / len, k = i - m * len;  // coalesced along k
+        xs[BWD ? m * CHUNK + k : k * MT + m] = m < a.T ? to_f32(x[m * a.ldx + kc + k]) : 0.f;
+      }
+      if (BWD)  // the last piece of a row of W may reach past K; its x reads as zero
+        for (int i = tid; i < MT * N; i += kThreads)
+          if (len + i % N < CHUNK) xs[i / N * CHUNK + len + i % N] = 0.f;
+      __syncthreads();
+    };
     if constexpr (!BWD) {
       const int c = c0 + (tid % LPR) * N;
       const int cols = a.N - c;
-      for (int k0 = tid / LPR; k0 < len; k0 += KP * U) {
-        uint4 raw[U];
+      const T* wp = w + (long long)(kc + tid / LPR) * a.ldw + c;
+      uint4 raw[U];
+      auto load = [&](int k0) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          raw[i] = load_piece(wp + (long long)(k0 + i * KP) * a.ldw,
+                              k0 + tid / LPR + i * KP < len ? cols : 0, w_vec);
+      };
+      load(0);
+      stage_x();
+      for (int k0 = 0; k0 < len; k0 += KP * U) {
+        uint4 cur[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) cur[i] = raw[i];
+        if (k0 + KP * U < len) load(k0 + KP * U);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const int k = k0 + i * KP;
-          raw[i] = load_piece(w + (long long)(kc + k) * a.ldw + c, k < len ? cols : 0, w_vec);
-        }
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int k = k0 + i * KP;
+          const int k = k0 + tid / LPR + i * KP;
           if (k >= len) break;
           float wv[N], xv[MT];
-          unpack_piece<T>(raw[i], wv);
+          unpack_piece<T>(cur[i], wv);
 #pragma unroll
           for (int m = 0; m < MT; ++m) xv[m] = xs[k * MT + m];
 #pragma unroll
@@ -220,24 +243,31 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a
         }
       }
     } else {
-      for (int k = lane * N; k < len; k += 32 * N) {
-        uint4 raw[8];
+      // steps of four of the warp's eight columns and 32 N of K
+      uint4 raw[4];
+      auto load = [&](int k, int h) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = c0 + warp * 8 + j;
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + warp * 8 + h + j;
           raw[j] = load_piece(w + (long long)c * a.ldw + kc + k, c < a.N ? len - k : 0, w_vec);
         }
+      };
+      load(lane * N, 0);
+      stage_x();
+      for (int k = lane * N; k < len; k += 32 * N) {
 #pragma unroll
         for (int h = 0; h < 8; h += 4) {
           float wv[4][N];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) unpack_piece<T>(raw[h + j], wv[j]);
+          for (int j = 0; j < 4; ++j) unpack_piece<T>(raw[j], wv[j]);
+          if (h == 0) load(k, 4);
+          else if (k + 32 * N < len) load(k + 32 * N, 0);
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             float xv[N];
 #pragma unroll
             for (int e = 0; e < N; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(xs + m * kFewChunk + k + e);
+              const float4 f = *reinterpret_cast<const float4*>(xs + m * CHUNK + k + e);
               xv[e] = f.x;
               xv[e + 1] = f.y;
               xv[e + 2] = f.z;
@@ -261,13 +291,13 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a
       for (int j = 0; j < N; ++j) {
 #pragma unroll
         for (int o = LPR; o < 32; o <<= 1) acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], o);
-        if (lane < LPR) red[(warp * MT + m) * kFewCols + lane * N + j] = acc[m][j];
+        if (lane < LPR) red[(warp * MT + m) * COLS + lane * N + j] = acc[m][j];
       }
     __syncthreads();
-    for (int i = tid; i < MT * kFewCols; i += kThreads) {
+    for (int i = tid; i < MT * COLS; i += kThreads) {
       float s = red[i];
 #pragma unroll
-      for (int q = 1; q < 8; ++q) s += red[q * MT * kFewCols + i];
+      for (int q = 1; q < 8; ++q) s += red[q * MT * COLS + i];
       part[i] = s;
     }
   } else {
@@ -281,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[m * 8 + j] = acc[mb + m][j];
       const float s = lane_sums<MB * 8>(v, lane);
-      if (lane < MB * 8) part[(mb + lane / 8) * kFewCols + warp * 8 + lane % 8] = s;
+      if (lane < MB * 8) part[(mb + lane / 8) * COLS + warp * 8 + lane % 8] = s;
     }
   }
   ptx::cluster_sync();  // every CTA's sums are in place (a cluster of one: a block barrier)
@@ -289,21 +319,22 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a
   // Epilogue: (row, 32-column group) units dealt over the cluster's warps; in
   // the backward a unit takes all rows, so it also has the column sums.
   const uint32_t part0 = ptx::smem_u32(part);
-  const int units = BWD ? 2 : 2 * (int)a.T;
+  constexpr int G = COLS / 32;
+  const int units = BWD ? G : G * (int)a.T;
   for (int u = rank + cluster * warp; u < units; u += cluster * (kThreads / 32)) {
-    const int g = u & 1;
+    const int g = u % G;
     const int c = c0 + g * 32 + lane;
     if (c0 + g * 32 >= a.N) continue;  // warp-uniform
     const bool ok = c < a.N;
     const float bias = !BWD && a.bias && ok ? __ldg(a.bias + c) : 0.f;
     float sum = 0.f;
-    const int m_lo = BWD ? 0 : u >> 1, m_hi = BWD ? (int)a.T : m_lo + 1;
+    const int m_lo = BWD ? 0 : u / G, m_hi = BWD ? (int)a.T : m_lo + 1;
     for (int m = m_lo; m < m_hi; ++m) {
       const float extra = epi_load<T, BWD>(a, m, c, ok);
       float v = 0.f;
       for (int r = 0; r < cluster; ++r)  // in slice order
         v += ld_cluster_f32(ptx::mapa_shared(
-            part0 + (uint32_t)(m * kFewCols + g * 32 + lane) * 4u, (uint32_t)r));
+            part0 + (uint32_t)(m * COLS + g * 32 + lane) * 4u, (uint32_t)r));
       sum += epi_finish<T, BWD>(a, m, c, ok, v, bias, extra);
     }
     if (BWD && dbias && ok) dbias[c] = sum;
@@ -311,12 +342,15 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const LinearArgs a
   ptx::cluster_sync();  // no CTA leaves while its sums may still be read
 }
 
-template <typename T, int MT, bool BWD>
+template <typename T, int MT, bool BWD, int COLS>
 mlp_status few_launch(const LinearArgs& a, float* dbias, cudaStream_t st) {
-  // CTAs: about four per SM, each with at least 256 of K
-  const long long tiles = (a.N + kFewCols - 1) / kFewCols;
+  // the widest cluster with which all CTAs are resident (on 152 SMs) and each
+  // still has 128 of K
+  const long long tiles = (a.N + COLS - 1) / COLS;
   int cluster = 8;
-  while (cluster > 1 && (tiles * cluster > 4 * 152 || a.K < 256 * cluster)) cluster >>= 1;
+  while (cluster > 1 &&
+         (tiles * cluster > 152 * FewShape<MT, BWD>::kPerSm || a.K < 128 * cluster))
+    --cluster;
   const int per = (a.K + cluster - 1) / cluster;
   const int slice = (per + 63) / 64 * 64;  // slices start on whole 16-byte pieces
   if (tiles * cluster > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
@@ -334,22 +368,31 @@ mlp_status few_launch(const LinearArgs& a, float* dbias, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   LaunchScope ls(BWD ? "linear_bwd_few" : "linear_fwd_few", st, a.T, a.N, a.K);
-  cudaLaunchKernelEx(&cfg, linear_few_kernel<T, MT, BWD>, a, cluster, slice, w_vec, dbias);
+  cudaLaunchKernelEx(&cfg, linear_few_kernel<T, MT, BWD, COLS>, a, cluster, slice, w_vec, dbias);
   return launch_status();
+}
+
+template <typename T, int MT, bool BWD>
+mlp_status few_cols(const LinearArgs& a, float* dbias, cudaStream_t st) {
+  // 128 columns a cluster (longer runs of W) where they still give enough CTAs
+  if constexpr (!BWD && MT <= 4) {
+    if ((long long)a.N / 128 * 8 >= 304) return few_launch<T, MT, BWD, 128>(a, dbias, st);
+  }
+  return few_launch<T, MT, BWD, 64>(a, dbias, st);
 }
 
 template <typename T, bool BWD>
 mlp_status few_rows(const LinearArgs& a, float* dbias, cudaStream_t st) {
-  if (a.T <= 1) return few_launch<T, 1, BWD>(a, dbias, st);
-  if (a.T <= 2) return few_launch<T, 2, BWD>(a, dbias, st);
-  if (a.T <= 4) return few_launch<T, 4, BWD>(a, dbias, st);
-  return few_launch<T, 8, BWD>(a, dbias, st);
+  if (a.T <= 1) return few_cols<T, 1, BWD>(a, dbias, st);
+  if (a.T <= 2) return few_cols<T, 2, BWD>(a, dbias, st);
+  if (a.T <= 4) return few_cols<T, 4, BWD>(a, dbias, st);
+  return few_cols<T, 8, BWD>(a, dbias, st);
 }
 
 template <typename T, bool BWD, bool ELT>
 mlp_status finish_launch(const LinearArgs& a, cudaStream_t st) {
   const int groups = (a.N + 31) / 32;
-  const int unit_rows = BWD ? 32 : kRowsAhead;
+  const int unit_rows = BWD ? kUnitRows : kRowsAhead;
   const long long units = (a.T + unit_rows - 1) / unit_rows * groups;
   const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;

@@ -162,6 +162,11 @@ mlp_status launch_ckpt8_decode(const int8_t* q, long long ldq, const uint8_t* sc
                                long long rows, int cols, void* out, int dtype, long long ldo,
                                cudaStream_t st);
 
+// k_elementwise.cu: column sums of fp32 partial rows [rows][ld], in a fixed
+// order and one launch; columns [0, n_a) into out_a, the rest into out_b.
+mlp_status launch_partial_sums(const float* part, long long rows, int cols, long long ld,
+                               float* out_a, int n_a, float* out_b, cudaStream_t st);
+
 // k_layernorm.cu.  The *_vec flags (16-byte pieces of each matrix's rows are
 // aligned) are the launchers' own.
 struct LayerNormFwd {

@@ -75,11 +75,32 @@ __device__ __forceinline__ void store_piece(T* p, const float (&v)[RowVec<T>::N]
     if (j < n) from_f32(v[j], p[j]);
 }
 
+// FULL: every piece that exists is whole and aligned (rows of whole pieces,
+// checked at launch), which leaves only the vector access.
+template <bool FULL, typename T>
+__device__ __forceinline__ uint4 load_piece_of(const T* p, int n, bool vec) {
+  if constexpr (FULL) {
+    (void)vec;
+    return n > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+  } else {
+    return load_piece(p, n, vec);
+  }
+}
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_piece_of(T* p, const float (&v)[RowVec<T>::N], int n,
+                                               bool vec) {
+  if constexpr (FULL) {
+    if (n > 0) store_piece(p, v, RowVec<T>::N, true);
+  } else {
+    store_piece(p, v, n, vec);
+  }
+}
+
 // N consecutive int8 checkpoint values (N 4 or 8) as packed words; the same
 // rules, with `vec` meaning the piece starts on N bytes.
-template <int N>
+template <int N, bool FULL = false>
 __device__ __forceinline__ void load_q(const int8_t* p, int n, bool vec, uint32_t (&w)[N / 4]) {
-  if (vec && n >= N) {
+  if (FULL ? n > 0 : vec && n >= N) {
     if constexpr (N == 8) {
       const uint2 q = *reinterpret_cast<const uint2*>(p);
       w[0] = q.x;
@@ -94,20 +115,20 @@ __device__ __forceinline__ void load_q(const int8_t* p, int n, bool vec, uint32_
     w[k] = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (4 * k + j < n) w[k] |= (uint32_t)(uint8_t)p[4 * k + j] << (8 * j);
+      if (!FULL && 4 * k + j < n) w[k] |= (uint32_t)(uint8_t)p[4 * k + j] << (8 * j);
   }
 }
 
-template <int N>
+template <int N, bool FULL = false>
 __device__ __forceinline__ void store_q(int8_t* p, int n, bool vec, const uint32_t (&w)[N / 4]) {
-  if (vec && n >= N) {
+  if (FULL ? n > 0 : vec && n >= N) {
     if constexpr (N == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
     return;
   }
 #pragma unroll
   for (int j = 0; j < N; ++j)
-    if (j < n) p[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
+    if (!FULL && j < n) p[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
 }
 
 }  // namespace mlp
