@@ -454,76 +454,91 @@ def mlp_stack_train_step(n_blocks, T, d, hidden, x0, target, params, velocity, g
 # checkpoint: a pair (q, scale) of an int8 [rows, cols] and a uint8
 # [rows, mlp_ckpt8_scale_cols(cols)] matrix.
 
-def _on_device(t, what):
+# These checks run on every call, and a call of a few microseconds is mostly
+# host time: they look at each property once.
+
+def _device(t, what):
+    """The CUDA device of t, which must be the current one (launches and streams go there)."""
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError("%s must be on the current CUDA device (got %s)" % (what, t.device))
+    return dev
 
 
-def _mat(t, what, rows, cols, dtype=None):
-    """(address, row pitch) of a [rows, cols] matrix; (None, 0) for None."""
+def _mat(t, what, rows, cols, dev, dtype=None):
+    """(address, row pitch) of a [rows, cols] matrix on device dev; (None, 0) for None."""
     if t is None:
         return None, 0
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise ValueError("%s must be [%d, %d] (got %s)" % (what, rows, cols, tuple(t.shape)))
     if dtype is not None and t.dtype != dtype:
         raise TypeError("%s must be %s (got %s)" % (what, dtype, t.dtype))
-    _on_device(t, what)
-    if cols > 1 and t.stride(1) != 1:
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device (got %s)" % (what, t.device))
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError("%s: the values of a row must be adjacent (strides %s)"
-                         % (what, tuple(t.stride())))
+                         % (what, (pitch, step)))
     # the pitch of a single row is never used; a whole number of 16-byte
     # pieces keeps it acceptable for any width
-    return t.data_ptr(), t.stride(0) if rows > 1 else (cols + 15) // 16 * 16
+    return t.data_ptr(), pitch if rows > 1 else (cols + 15) // 16 * 16
 
 
-def _vec(t, what, n):
-    """Address of a contiguous fp32 vector of n values; None for None."""
-    import torch
+def _vec(t, what, n, dev):
+    """Address of a contiguous fp32 vector of n values on device dev; None for None."""
     if t is None:
         return None
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or (n > 1 and t.stride(0) != 1):
         raise ValueError("%s must be %d contiguous values (got %s)" % (what, n, tuple(t.shape)))
-    if t.dtype != torch.float32:
-        raise TypeError("%s must be float32 (got %s)" % (what, t.dtype))
-    _on_device(t, what)
+    if _code_of(t.dtype) != MLP_DTYPE_F32:
+        raise TypeError("%s must be torch.float32 (got %s)" % (what, t.dtype))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current CUDA device (got %s)" % (what, t.device))
     return t.data_ptr()
 
 
-def _ckpt(ckpt, what, rows, cols):
+def _ckpt(ckpt, what, rows, cols, dev):
     """(q address, pitch, scale address, pitch) of an 8-bit checkpoint."""
-    import torch
     if ckpt is None:
         return None, 0, None, 0
+    import torch
     q, scale = ckpt
     groups = (cols + MLP_CKPT8_GROUP - 1) // MLP_CKPT8_GROUP
-    return (*_mat(q, what + " values", rows, cols, torch.int8),
-            *_mat(scale, what + " scales", rows, groups, torch.uint8))
+    return (*_mat(q, what + " values", rows, cols, dev, torch.int8),
+            *_mat(scale, what + " scales", rows, groups, dev, torch.uint8))
 
 
-def _ws(t):
+def _ws(t, dev):
     if t is None:
         return None, 0
-    _on_device(t, "workspace")
+    if t.get_device() != dev:
+        raise ValueError("workspace must be on the current CUDA device (got %s)" % t.device)
     if not t.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def _float_code(t):
-    code = _dtype_code(t)
-    if code == MLP_DTYPE_U8:
-        raise TypeError("unsupported dtype %s" % t.dtype)
-    return code
+_FLOAT_CODES = {}
 
 
 def _code_of(dtype):
-    import torch
-    code = {torch.float32: MLP_DTYPE_F32, torch.bfloat16: MLP_DTYPE_BF16,
-            torch.float16: MLP_DTYPE_F16}.get(dtype)
+    """MLP_DTYPE_* of a floating torch dtype."""
+    if not _FLOAT_CODES:
+        import torch
+        _FLOAT_CODES.update({torch.float32: MLP_DTYPE_F32, torch.bfloat16: MLP_DTYPE_BF16,
+                             torch.float16: MLP_DTYPE_F16})
+    code = _FLOAT_CODES.get(dtype)
     if code is None:
         raise TypeError("unsupported dtype %s" % dtype)
     return code
+
+
+def _stream_of(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch.cuda.current_stream().cuda_stream
 
 
 def mlp_ckpt8_scale_cols(cols: int) -> int:
@@ -534,19 +549,21 @@ def mlp_ckpt8_scale_cols(cols: int) -> int:
 def mlp_ckpt8_encode(x, q, scale, stream=None):
     """x [rows, cols] (fp32, bf16 or fp16) into the 8-bit checkpoint (q, scale)."""
     T, d = x.shape
-    xp, ldx = _mat(x, "x", T, d)
-    qp, ldq, sp, lds = _ckpt((q, scale), "checkpoint", T, d)
-    _check(load().mlp_ckpt8_encode(xp, _float_code(x), T, d, ldx, qp, ldq, sp, lds,
-                                   _stream(stream)), "mlp_ckpt8_encode")
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", T, d, dev)
+    qp, ldq, sp, lds = _ckpt((q, scale), "checkpoint", T, d, dev)
+    _check(load().mlp_ckpt8_encode(xp, _code_of(x.dtype), T, d, ldx, qp, ldq, sp, lds,
+                                   _stream_of(stream)), "mlp_ckpt8_encode")
 
 
 def mlp_ckpt8_decode(q, scale, out, stream=None):
     """The values of the 8-bit checkpoint (q, scale) into out (fp32, bf16 or fp16)."""
     T, d = out.shape
-    op, ldo = _mat(out, "out", T, d)
-    qp, ldq, sp, lds = _ckpt((q, scale), "checkpoint", T, d)
-    _check(load().mlp_ckpt8_decode(qp, ldq, sp, lds, T, d, op, _float_code(out), ldo,
-                                   _stream(stream)), "mlp_ckpt8_decode")
+    dev = _device(out, "out")
+    op, ldo = _mat(out, "out", T, d, dev)
+    qp, ldq, sp, lds = _ckpt((q, scale), "checkpoint", T, d, dev)
+    _check(load().mlp_ckpt8_decode(qp, ldq, sp, lds, T, d, op, _code_of(out.dtype), ldo,
+                                   _stream_of(stream)), "mlp_ckpt8_decode")
 
 
 def mlp_layernorm_fwd(x, y, gain=None, shift=None, mean=None, rstd=None, ckpt=None, eps=1e-5,
@@ -554,13 +571,14 @@ def mlp_layernorm_fwd(x, y, gain=None, shift=None, mean=None, rstd=None, ckpt=No
     """Layer norm of the rows of x into y (same dtype); mean, rstd: fp32 [T]
     kept for the backward; ckpt: receives x in 8 bits."""
     T, d = x.shape
-    xp, ldx = _mat(x, "x", T, d)
-    yp, ldy = _mat(y, "y", T, d, x.dtype)
-    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, d)
-    _check(load().mlp_layernorm_fwd(xp, _float_code(x), ldx, _vec(gain, "gain", d),
-                                    _vec(shift, "shift", d), T, d, eps, yp, ldy,
-                                    _vec(mean, "mean", T), _vec(rstd, "rstd", T), qp, ldq, sp,
-                                    lds, _stream(stream)), "mlp_layernorm_fwd")
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", T, d, dev)
+    yp, ldy = _mat(y, "y", T, d, dev, x.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, d, dev)
+    _check(load().mlp_layernorm_fwd(xp, _code_of(x.dtype), ldx, _vec(gain, "gain", d, dev),
+                                    _vec(shift, "shift", d, dev), T, d, eps, yp, ldy,
+                                    _vec(mean, "mean", T, dev), _vec(rstd, "rstd", T, dev), qp,
+                                    ldq, sp, lds, _stream_of(stream)), "mlp_layernorm_fwd")
 
 
 def mlp_layernorm_workspace_bytes(T: int, d: int) -> int:
@@ -572,17 +590,18 @@ def mlp_layernorm_bwd(dy, mean, rstd, dx, dgain, dshift, workspace, x=None, ckpt
     """Backward of mlp_layernorm_fwd from its input x or the 8-bit checkpoint
     of it; dx (+ dres, the gradient past the norm), dgain and dshift fp32."""
     T, d = dy.shape
-    dyp, lddy = _mat(dy, "dy", T, d)
-    xp, ldx = _mat(x, "x", T, d, dy.dtype)
-    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, d)
-    rp, ldr = _mat(dres, "dres", T, d, dy.dtype)
-    dxp, lddx = _mat(dx, "dx", T, d, dy.dtype)
-    wp, wsb = _ws(workspace)
-    _check(load().mlp_layernorm_bwd(dyp, _float_code(dy), lddy, xp, ldx, qp, ldq, sp, lds,
-                                    _vec(mean, "mean", T), _vec(rstd, "rstd", T),
-                                    _vec(gain, "gain", d), rp, ldr, T, d, dxp, lddx,
-                                    _vec(dgain, "dgain", d), _vec(dshift, "dshift", d), wp, wsb,
-                                    _stream(stream)), "mlp_layernorm_bwd")
+    dev = _device(dy, "dy")
+    dyp, lddy = _mat(dy, "dy", T, d, dev)
+    xp, ldx = _mat(x, "x", T, d, dev, dy.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, d, dev)
+    rp, ldr = _mat(dres, "dres", T, d, dev, dy.dtype)
+    dxp, lddx = _mat(dx, "dx", T, d, dev, dy.dtype)
+    wp, wsb = _ws(workspace, dev)
+    _check(load().mlp_layernorm_bwd(dyp, _code_of(dy.dtype), lddy, xp, ldx, qp, ldq, sp, lds,
+                                    _vec(mean, "mean", T, dev), _vec(rstd, "rstd", T, dev),
+                                    _vec(gain, "gain", d, dev), rp, ldr, T, d, dxp, lddx,
+                                    _vec(dgain, "dgain", d, dev), _vec(dshift, "dshift", d, dev), wp,
+                                    wsb, _stream_of(stream)), "mlp_layernorm_bwd")
 
 
 def mlp_linear_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
@@ -597,16 +616,17 @@ def mlp_linear_fwd(x, w, y, bias=None, act=MLP_ACT_NONE, slope=0.5, residual=Non
     receives them in 8 bits."""
     T, k = x.shape
     n = w.shape[1]
-    xp, ldx = _mat(x, "x", T, k)
-    wp, ldw = _mat(w, "w", k, n, x.dtype)
-    yp, ldy = _mat(y, "y", T, n)
-    rp, ldr = _mat(residual, "residual", T, n, y.dtype)
-    up, ldu = _mat(u, "u", T, n, x.dtype)
-    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n)
-    ws, wsb = _ws(workspace)
-    _check(load().mlp_linear_fwd(xp, ldx, wp, ldw, T, k, n, _float_code(x), _vec(bias, "bias", n),
-                                 act, slope, rp, ldr, yp, ldy, _float_code(y), up, ldu, qp, ldq,
-                                 sp, lds, ws, wsb, _stream(stream)), "mlp_linear_fwd")
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", T, k, dev)
+    wp, ldw = _mat(w, "w", k, n, dev, x.dtype)
+    yp, ldy = _mat(y, "y", T, n, dev)
+    rp, ldr = _mat(residual, "residual", T, n, dev, y.dtype)
+    up, ldu = _mat(u, "u", T, n, dev, x.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n, dev)
+    ws, wsb = _ws(workspace, dev)
+    _check(load().mlp_linear_fwd(xp, ldx, wp, ldw, T, k, n, _code_of(x.dtype), _vec(bias, "bias", n, dev),
+                                 act, slope, rp, ldr, yp, ldy, _code_of(y.dtype), up, ldu, qp, ldq,
+                                 sp, lds, ws, wsb, _stream_of(stream)), "mlp_linear_fwd")
 
 
 def mlp_linear_bwd_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
@@ -621,16 +641,17 @@ def mlp_linear_bwd(dy, w, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, db
     sums of du, a (dy's dtype) the activations f(u)."""
     T, k = dy.shape
     n = w.shape[0]
-    dyp, lddy = _mat(dy, "dy", T, k)
-    wp, ldw = _mat(w, "w", n, k, dy.dtype)
-    dup, lddu = _mat(du, "du", T, n)
-    up, ldu = _mat(u, "u", T, n, dy.dtype)
-    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n)
-    ap, lda = _mat(a, "a", T, n, dy.dtype)
-    ws, wsb = _ws(workspace)
-    _check(load().mlp_linear_bwd(dyp, lddy, wp, ldw, T, n, k, _float_code(dy), act, slope, up, ldu,
-                                 qp, ldq, sp, lds, dup, lddu, _float_code(du),
-                                 _vec(dbias, "dbias", n), ap, lda, ws, wsb, _stream(stream)),
+    dev = _device(dy, "dy")
+    dyp, lddy = _mat(dy, "dy", T, k, dev)
+    wp, ldw = _mat(w, "w", n, k, dev, dy.dtype)
+    dup, lddu = _mat(du, "du", T, n, dev)
+    up, ldu = _mat(u, "u", T, n, dev, dy.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n, dev)
+    ap, lda = _mat(a, "a", T, n, dev, dy.dtype)
+    ws, wsb = _ws(workspace, dev)
+    _check(load().mlp_linear_bwd(dyp, lddy, wp, ldw, T, n, k, _code_of(dy.dtype), act, slope, up, ldu,
+                                 qp, ldq, sp, lds, dup, lddu, _code_of(du.dtype),
+                                 _vec(dbias, "dbias", n, dev), ap, lda, ws, wsb, _stream_of(stream)),
            "mlp_linear_bwd")
 
 
@@ -643,12 +664,13 @@ def mlp_act_bwd(dy, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, dbias=No
     """du = dy f'(u) with the column sums and activations of mlp_linear_bwd,
     without a product (a layer whose own output has the activation)."""
     T, n = dy.shape
-    dyp, lddy = _mat(dy, "dy", T, n)
-    dup, lddu = _mat(du, "du", T, n, dy.dtype)
-    up, ldu = _mat(u, "u", T, n, dy.dtype)
-    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n)
-    ap, lda = _mat(a, "a", T, n, dy.dtype)
-    ws, wsb = _ws(workspace)
-    _check(load().mlp_act_bwd(dyp, lddy, T, n, _float_code(dy), act, slope, up, ldu, qp, ldq, sp,
-                              lds, dup, lddu, _vec(dbias, "dbias", n), ap, lda, ws, wsb,
-                              _stream(stream)), "mlp_act_bwd")
+    dev = _device(dy, "dy")
+    dyp, lddy = _mat(dy, "dy", T, n, dev)
+    dup, lddu = _mat(du, "du", T, n, dev, dy.dtype)
+    up, ldu = _mat(u, "u", T, n, dev, dy.dtype)
+    qp, ldq, sp, lds = _ckpt(ckpt, "ckpt", T, n, dev)
+    ap, lda = _mat(a, "a", T, n, dev, dy.dtype)
+    ws, wsb = _ws(workspace, dev)
+    _check(load().mlp_act_bwd(dyp, lddy, T, n, _code_of(dy.dtype), act, slope, up, ldu, qp, ldq, sp,
+                              lds, dup, lddu, _vec(dbias, "dbias", n, dev), ap, lda, ws, wsb,
+                              _stream_of(stream)), "mlp_act_bwd")

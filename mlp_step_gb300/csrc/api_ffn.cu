@@ -148,12 +148,14 @@ struct LinearPath {
   bool few;      // launch_linear_few: no workspace
   int splits;    // planes of raw sums (0: the epilogue is in the product's kernel)
   size_t sums, part;
+  int part_rows;
   long long ldp, ldcp;
+  long long parts(long long T) const { return (T + part_rows - 1) / part_rows; }
 };
 
 LinearPath linear_path(long long T, int K, int N, int dtype, bool bwd) {
   LinearPath p{};
-  p.few = T <= kLinearFewRows;
+  p.few = linear_takes_few(T, K, N, dtype);
   if (p.few) return p;
   p.splits = 1;
   if (dtype != MLP_DTYPE_F32) {
@@ -164,7 +166,8 @@ LinearPath linear_path(long long T, int K, int N, int dtype, bool bwd) {
   p.sums = align256((size_t)p.splits * T * p.ldp * 4);
   if (bwd) {
     p.ldcp = (N + 31) / 32 * 32;  // whole 128-byte lines
-    p.part = align256((size_t)linear_part_rows(T) * p.ldcp * 4);
+    p.part_rows = p.splits && T < 2048 ? kPartRowsFew : kPartRows;
+    p.part = align256((size_t)p.parts(T) * p.ldcp * 4);
   }
   return p;
 }
@@ -183,6 +186,7 @@ mlp_status run_linear(LinearArgs a, const LinearPath& lp, bool bwd, float* dbias
   a.ldp = lp.ldp;
   a.colpart = dbias ? reinterpret_cast<float*>(ws + lp.sums) : nullptr;
   a.ldcp = lp.ldcp;
+  a.part_rows = lp.part_rows;
   if (a.dtype == MLP_DTYPE_F32) {
     GemmArgs g{};
     g.M = (int)a.T; g.N = a.N; g.K = a.K;
@@ -194,9 +198,9 @@ mlp_status run_linear(LinearArgs a, const LinearPath& lp, bool bwd, float* dbias
   } else {
     MLP_CHECK(launch_linear_tc(a, bwd, st));
   }
-  if (lp.splits) MLP_CHECK(launch_linear_finish(a, bwd, false, st));
+  if (lp.splits) MLP_CHECK(launch_linear_finish(a, bwd, st));
   if (!dbias) return MLP_OK;
-  return launch_partial_sums(a.colpart, linear_part_rows(a.T), a.N, a.ldcp, dbias, a.N, nullptr,
+  return launch_partial_sums(a.colpart, lp.parts(a.T), a.N, a.ldcp, dbias, a.N, nullptr,
                              st);
 }
 
@@ -290,7 +294,7 @@ mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int 
 
 size_t mlp_act_bwd_workspace_bytes(int T, int n) {
   if (T <= 0 || n <= 0) return 0;
-  return align256((size_t)linear_part_rows(T) * ((n + 31) / 32 * 32) * 4);
+  return align256((size_t)(((long long)T + kPartRows - 1) / kPartRows) * ((n + 31) / 32 * 32) * 4);
 }
 
 mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int act, float slope,
@@ -319,13 +323,12 @@ mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int ac
   a.u_in = u; a.ldu_in = ldu;
   a.q = const_cast<int8_t*>(u_q); a.ldq = ldq;
   a.scale = const_cast<uint8_t*>(u_scale); a.lds = lds;
-  a.splits = 1;
   a.ldcp = (n + 31) / 32 * 32;
   a.colpart = dbias ? static_cast<float*>(workspace) : nullptr;
-  MLP_CHECK(launch_linear_finish(a, true, true, S(stream)));
+  MLP_CHECK(launch_act_bwd(a, S(stream)));
   if (!dbias) return MLP_OK;
-  return launch_partial_sums(a.colpart, linear_part_rows(T), n, a.ldcp, dbias, n, nullptr,
-                             S(stream));
+  return launch_partial_sums(a.colpart, ((long long)T + kPartRows - 1) / kPartRows, n, a.ldcp,
+                             dbias, n, nullptr, S(stream));
 }
 
 }  // extern "C"

@@ -130,45 +130,60 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   };
   load(row);
   for (; row < p.T; row += stride) {  // uniform over the warps that share a row
-    float v[NV][N];
-    float s[1] = {0.f};
+    F2 v[NV][N / 2];
+    F2 s2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       unpack_piece<T>(raw[i], v[i]);
 #pragma unroll
-      for (int j = 0; j < N; ++j) s[0] += v[i][j];
+      for (int j = 0; j < N / 2; ++j) s2 = add2(s2, v[i][j]);
     }
     load(row + stride);
+    float s[1] = {s2.x + s2.y};
     row_sums<WPR>(s, part[0][slot], slot, t >> 5);
     const float mu = s[0] * inv_d;
-    s[0] = 0.f;
+    s2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int n = p.d - (i * 32 * WPR + t) * N;
+      if (FULL ? n > 0 : n >= N) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const float c = j < n ? v[i][j] - mu : 0.f;
-        s[0] = fmaf(c, c, s[0]);
+        for (int j = 0; j < N / 2; ++j) {
+          const F2 c = add2(v[i][j], f2(-mu));
+          s2 = fma2(c, c, s2);
+        }
+      } else if (!FULL) {
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          const float c0 = 2 * j < n ? v[i][j].x - mu : 0.f;
+          const float c1 = 2 * j + 1 < n ? v[i][j].y - mu : 0.f;
+          s2 = fma2(f2(c0, c1), f2(c0, c1), s2);
+        }
       }
     }
+    s[0] = s2.x + s2.y;
     row_sums<WPR>(s, part[1][slot], slot, t >> 5);
     const float rho = 1.f / sqrtf(s[0] * inv_d + p.eps);
     if (t == 0) {
       if (p.mean) p.mean[row] = mu;
       if (p.rstd) p.rstd[row] = rho;
     }
+    T* y = static_cast<T*>(p.y) + row * p.ldy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N;
       const int n = p.d - c;
       if (p.q)
-        store_ckpt<T, FULL>(v[i], p.q + row * p.ldq, p.scale + row * p.lds, c, n, p.q_vec);
+        store_ckpt<T, FULL>(reinterpret_cast<const float(&)[N]>(v[i]), p.q + row * p.ldq,
+                            p.scale + row * p.lds, c, n, p.q_vec);
       float a[N], b[N];
       load_param<N, FULL>(p.gain, c, n, p.p_vec, 1.f, a);
       load_param<N, FULL>(p.shift, c, n, p.p_vec, 0.f, b);
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[i][j] = fmaf((v[i][j] - mu) * rho, a[j], b[j]);
-      store_piece_of<FULL>(static_cast<T*>(p.y) + row * p.ldy + c, v[i], n, p.y_vec);
+      for (int j = 0; j < N / 2; ++j)
+        v[i][j] = fma2(mul2(add2(v[i][j], f2(-mu)), f2(rho)), f2(a[2 * j], a[2 * j + 1]),
+                       f2(b[2 * j], b[2 * j + 1]));
+      store_piece_of<FULL>(y + c, reinterpret_cast<const float(&)[N]>(v[i]), n, p.y_vec);
     }
   }
 }
@@ -243,6 +258,22 @@ struct XPiece {
       raw = load_piece_of<FULL>(static_cast<const T*>(p.x) + row * p.ldx + c, n, p.x_vec);
     }
   }
+  __device__ __forceinline__ void values(F2 (&v)[N / 2]) const {
+    if constexpr (CK) {
+      const float step = ckpt8_step(b);
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const uint32_t f = ckpt8_flip(w[k]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          v[2 * k + e] = mul2(add2(f2(ckpt8_biased(f, 2 * e), ckpt8_biased(f, 2 * e + 1)),
+                                   f2(-kCkptBias)),
+                              f2(step));
+      }
+    } else {
+      unpack_piece<T>(raw, v);
+    }
+  }
   __device__ __forceinline__ void values(float (&v)[N]) const {
     if constexpr (CK) {
       const float step = ckpt8_step(b);
@@ -269,7 +300,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
     ln_bwd_kernel(const LayerNormBwd p) {
   constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
   __shared__ float part[2][ROWS][2 * WPR];
-  extern __shared__ float sums[];  // ROWS > 1: one slot's values at a time
+  extern __shared__ __align__(16) float sums_mem[];  // ROWS > 1: one slot's values at a time
   pdl_wait();
   pdl_launch_dependents();
   const int slot = threadIdx.x / (32 * WPR), t = threadIdx.x % (32 * WPR);
@@ -278,23 +309,24 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   const float inv_d = 1.f / (float)p.d;
   const T* dy = static_cast<const T*>(p.dy);
   const T* dres = static_cast<const T*>(p.dres);
-  float dg[NV][N], ds[NV][N];
+  F2 dg[NV][N / 2], ds[NV][N / 2];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < N; ++j) dg[i][j] = ds[i][j] = 0.f;
+    for (int j = 0; j < N / 2; ++j) dg[i][j] = ds[i][j] = f2(0.f);
   uint4 rdy[NV];
   XPiece<T, CK, FULL> rx[NV];
   float mu_n = 0.f, rho_n = 0.f;
   auto load = [&](long long r) {
+    const bool in = r < p.T;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N;
-      const int n = r < p.T ? p.d - c : 0;
+      const int n = in ? p.d - c : 0;
       rdy[i] = load_piece_of<FULL>(dy + r * p.lddy + c, n, p.dy_vec);
       rx[i].load(p, r, c, n);
     }
-    if (r < p.T) {
+    if (in) {
       mu_n = p.mean[r];
       rho_n = p.rstd[r];
     }
@@ -303,8 +335,8 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   int turn = 0;
   for (; row < p.T; row += stride, turn ^= 1) {
     const float mu = mu_n, rho = rho_n;
-    float g[NV][N], xh[NV][N];
-    float s[2] = {0.f, 0.f};
+    F2 g[NV][N / 2], xh[NV][N / 2];
+    F2 s1 = f2(0.f), s2 = f2(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N, n = p.d - c;
@@ -313,15 +345,23 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       unpack_piece<T>(rdy[i], g[i]);
       rx[i].values(xh[i]);
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        // past the row's end xh is set to 0 (dy reads as 0 there, but 0 times
-        // a mean or scale that is not finite would not be)
-        xh[i][j] = j < n ? (xh[i][j] - mu) * rho : 0.f;
-        dg[i][j] = fmaf(g[i][j], xh[i][j], dg[i][j]);
-        ds[i][j] += g[i][j];
-        g[i][j] *= gain[j];
-        s[0] += g[i][j];
-        s[1] = fmaf(g[i][j], xh[i][j], s[1]);
+      for (int j = 0; j < N / 2; ++j) xh[i][j] = mul2(add2(xh[i][j], f2(-mu)), f2(rho));
+      // past the row's end xh is set to 0 (dy reads as 0 there, but 0 times a
+      // mean or scale that is not finite would not be)
+      if (FULL ? n <= 0 : n < N) {
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          if (FULL || 2 * j >= n) xh[i][j].x = 0.f;
+          if (FULL || 2 * j + 1 >= n) xh[i][j].y = 0.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        dg[i][j] = fma2(g[i][j], xh[i][j], dg[i][j]);
+        ds[i][j] = add2(ds[i][j], g[i][j]);
+        g[i][j] = mul2(g[i][j], f2(gain[2 * j], gain[2 * j + 1]));
+        s1 = add2(s1, g[i][j]);
+        s2 = fma2(g[i][j], xh[i][j], s2);
       }
     }
     uint4 rr[NV];  // this row's residual gradient, in flight over the reductions
@@ -333,50 +373,59 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       }
     }
     load(row + stride);
+    float s[2] = {s1.x + s1.y, s2.x + s2.y};
     row_sums<WPR>(s, part[turn][slot], slot, t >> 5);
     const float m1 = s[0] * inv_d, m2 = s[1] * inv_d;
+    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N;
+      // rho (g - (m1 + xh m2))
 #pragma unroll
-      for (int j = 0; j < N; ++j) g[i][j] = rho * (g[i][j] - fmaf(xh[i][j], m2, m1));
+      for (int j = 0; j < N / 2; ++j)
+        g[i][j] = mul2(add2(g[i][j], fma2(xh[i][j], f2(-m2), f2(-m1))), f2(rho));
       if (dres) {
-        float r[N];
+        F2 r[N / 2];
         unpack_piece<T>(rr[i], r);
 #pragma unroll
-        for (int j = 0; j < N; ++j) g[i][j] += r[j];
+        for (int j = 0; j < N / 2; ++j) g[i][j] = add2(g[i][j], r[j]);
       }
-      store_piece_of<FULL>(static_cast<T*>(p.dx) + row * p.lddx + c, g[i], p.d - c, p.dx_vec);
+      store_piece_of<FULL>(dx + c, reinterpret_cast<const float(&)[N]>(g[i]), p.d - c, p.dx_vec);
     }
   }
   // this block's partial sums, row slots added in order
   float* out = p.part + (long long)blockIdx.x * 2 * p.d;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float(&a)[NV][N] = which ? ds : dg;
+    F2(&a)[NV][N / 2] = which ? ds : dg;
     if constexpr (ROWS > 1) {
+      F2* sums = reinterpret_cast<F2*>(sums_mem) + t;  // value k at [k * 32 WPR]
       for (int k = 1; k < ROWS; ++k) {
         __syncthreads();
         if (slot == k)
 #pragma unroll
           for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) sums[(i * N + j) * 32 * WPR + t] = a[i][j];
+            for (int j = 0; j < N / 2; ++j) sums[(i * N / 2 + j) * 32 * WPR] = a[i][j];
         __syncthreads();
         if (slot == 0)
 #pragma unroll
           for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int j = 0; j < N; ++j) a[i][j] += sums[(i * N + j) * 32 * WPR + t];
+            for (int j = 0; j < N / 2; ++j)
+              a[i][j] = add2(a[i][j], sums[(i * N / 2 + j) * 32 * WPR]);
       }
     }
     if (slot == 0)
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * 32 * WPR + t) * N;
+        float* o = out + (long long)which * p.d + c;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-          if (c + j < p.d) out[(long long)which * p.d + c + j] = a[i][j];
+        for (int j = 0; j < N / 2; ++j) {
+          if (FULL ? c < p.d : c + 2 * j < p.d) o[2 * j] = a[i][j].x;
+          if (FULL ? c < p.d : c + 2 * j + 1 < p.d) o[2 * j + 1] = a[i][j].y;
+        }
       }
   }
 }

@@ -42,6 +42,7 @@ constexpr int kBox = 4096, kWarpStage = kBox + 2048;
 struct LinParams {
   LinearArgs a;
   int tiles_m, tiles_n, units, k_blocks, kb_per_split;
+  int a_bytes;  // of a stage's x tile: fewer than 128 rows when there are fewer
   // What moves by TMA between the matrices and the warps' staging boxes:
   int y64;     // y / du in boxes of 64 columns, stored once per unit
   int tma_y;   // y / du in boxes of 32 columns (with u_out, or fp32)
@@ -57,10 +58,12 @@ struct LinMaps {
   CUtensorMap a, b, y, u, in, q;
 };
 
-// EW: epilogue warps.
-template <int PAIR, int BN, int STAGES, int EW>
+// EW: epilogue warps.  AROWS: rows of x that a stage holds; with fewer than 128
+// the MMA reads on into what follows, which only feeds accumulator rows that
+// are never stored.
+template <int PAIR, int BN, int STAGES, int EW, int AROWS = 128>
 struct LinLayout {
-  static constexpr int A_BYTES = 128 * BK * 2;
+  static constexpr int A_BYTES = AROWS * BK * 2;
   static constexpr int B_COLS = PAIR ? 128 : BN;  // operand columns staged per CTA
   static constexpr int B_BYTES = B_COLS * BK * 2;
   static constexpr int ACC = PAIR ? 256 : BN;     // accumulator columns per CTA
@@ -210,9 +213,10 @@ __device__ __forceinline__ float column_sums(F2 (&p)[16], int lane) {
 
 // ------------------------------------------------------------ the kernel
 
-template <int PAIR, int BN, int STAGES, int EW, int H16, int BWD>
+template <int PAIR, int BN, int STAGES, int EW, int AROWS, int H16, int BWD>
 __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams& p) {
-  using L = LinLayout<PAIR, BN, STAGES, EW>;
+  using L = LinLayout<PAIR, BN, STAGES, EW, AROWS>;
+  static_assert(AROWS == 128 || (STAGES * L::B_BYTES >= 16384 && !PAIR), "reads past the x ring");
   constexpr int ACC = L::ACC;
   constexpr int TILE_M = PAIR ? 256 : 128, TILE_N = ACC;
   constexpr bool B_MN = !BWD;  // W [K][N] is an N-major operand, W [N][K] a K-major one
@@ -316,7 +320,7 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
           } else {
             // 64-wide boxes entirely past N are not loaded: they only feed
             // accumulator columns that are never stored
-            uint32_t bytes = L::A_BYTES + L::B_BYTES;
+            uint32_t bytes = p.a_bytes + L::B_BYTES;
             if constexpr (B_MN) {
 #pragma unroll
               for (int j = 1; j < BN / 64; ++j)
@@ -784,13 +788,13 @@ template <int STAGES, int EW, int H16, int BWD>
 __global__ void __cluster_dims__(2, 1, 1)
     __launch_bounds__(LinLayout<1, 256, STAGES, EW>::THREADS, 1)
     linear_pair_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinParams p) {
-  linear_body<1, 256, STAGES, EW, H16, BWD>(maps, p);
+  linear_body<1, 256, STAGES, EW, 128, H16, BWD>(maps, p);
 }
 
-template <int BN, int STAGES, int EW, int H16, int BWD>
-__global__ void __launch_bounds__(LinLayout<0, BN, STAGES, EW>::THREADS, 1)
+template <int BN, int STAGES, int EW, int AROWS, int H16, int BWD>
+__global__ void __launch_bounds__(LinLayout<0, BN, STAGES, EW, AROWS>::THREADS, 1)
     linear_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinParams p) {
-  linear_body<0, BN, STAGES, EW, H16, BWD>(maps, p);
+  linear_body<0, BN, STAGES, EW, AROWS, H16, BWD>(maps, p);
 }
 
 // ------------------------------------------------------------ plan and launch
@@ -833,10 +837,10 @@ LinPlan linear_plan(long long T, int K, int N) {
   return pl;
 }
 
-template <int BN, int STAGES, int EW, int H16, int BWD>
+template <int BN, int STAGES, int EW, int AROWS, int H16, int BWD>
 mlp_status launch_single(const LinMaps& maps, const LinParams& p, cudaStream_t st) {
-  using L = LinLayout<0, BN, STAGES, EW>;
-  auto kernel = linear_kernel<BN, STAGES, EW, H16, BWD>;
+  using L = LinLayout<0, BN, STAGES, EW, AROWS>;
+  auto kernel = linear_kernel<BN, STAGES, EW, AROWS, H16, BWD>;
   static const cudaError_t configured =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (configured != cudaSuccess) return MLP_ERR_CUDA;
@@ -885,8 +889,12 @@ mlp_status launch_tile(const LinMaps& maps, const LinParams& p, Tile tile, cudaS
     case kPair:
       return p.k_blocks <= kShortK ? launch_pair<4, 16, H16, BWD>(maps, p, st)
                                    : launch_pair<5, 8, H16, BWD>(maps, p, st);
-    case kWide: return launch_single<128, 5, 8, H16, BWD>(maps, p, st);
-    default: return launch_single<64, 7, 4, H16, BWD>(maps, p, st);
+    case kWide: return launch_single<128, 5, 8, 128, H16, BWD>(maps, p, st);
+    default:
+      // few rows stream W: the ring's depth sets the rate (16 rows x 8,192 x
+      // 8,192: 42 us with seven stages of 24 KiB)
+      return p.a.T <= 32 ? launch_single<64, 15, 4, 32, H16, BWD>(maps, p, st)
+                         : launch_single<64, 7, 4, 128, H16, BWD>(maps, p, st);
   }
 }
 
@@ -919,7 +927,12 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
     return encode_tmap_bf16_2d(map, base, cols, rows, (unsigned long long)ld * 2, box_cols,
                                box_rows);
   };
-  if (!map16(&maps.a, a.x, a.K, a.T, a.ldx, BK, 128)) return MLP_ERR_CUDA;
+  // A single-CTA tile of few rows loads just those (in eights): the stale rows
+  // behind them only feed accumulator rows that are never stored, and boxes of
+  // mostly fill are slow to deliver (16 rows x 8,192 x 8,192: 43 us with them).
+  const int a_rows = pl.tile != kPair && a.T < 128 ? (int)(a.T + 7) / 8 * 8 : 128;
+  p.a_bytes = a_rows * BK * 2;
+  if (!map16(&maps.a, a.x, a.K, a.T, a.ldx, BK, a_rows)) return MLP_ERR_CUDA;
   if (!(bwd ? map16(&maps.b, a.w, a.K, a.N, a.ldw, BK, pl.tile == kNarrow ? 64 : 128)
             : map16(&maps.b, a.w, a.N, a.K, a.ldw, 64, BK)))
     return MLP_ERR_CUDA;

@@ -1,11 +1,11 @@
 // Linear layers outside the tensor-core tiles (formulas: k_linear.cu): the
-// one-launch kernel for a few rows (single tokens), and the epilogue as a pass
-// of its own over raw sums (split-K partial planes, fp32 products) or over dy
-// (the activation's backward without a product).
+// one-launch kernel for a few rows (single tokens), the epilogue as a pass of
+// its own over raw sums (split-K partial planes, fp32 products), and the
+// activation's backward without a product.
 //
-// In both a warp finishes 32 columns of a row at a time, one per lane: memory
-// is touched in whole rows of 32 values and a group of the 8-bit form is one
-// warp, its largest magnitude one warp reduction.
+// In the first two a warp finishes 32 columns of a row at a time, one per
+// lane: memory is touched in whole rows of 32 values and a group of the 8-bit
+// form is one warp, its largest magnitude one warp reduction.
 #include "act.cuh"
 #include "ckpt8.cuh"
 #include "kernels.cuh"
@@ -36,7 +36,7 @@ __device__ __forceinline__ float epi_load(const LinearArgs& a, long long m, int 
 
 // Finishes element (m, c) from its raw sum; whole warps, lane = column of a
 // 32-column group.  Returns the stored value before rounding.
-template <typename T, bool BWD>
+template <typename T, bool BWD, int ACT>
 __device__ __forceinline__ float epi_finish(const LinearArgs& a, long long m, int c, bool ok,
                                             float v, float bias, float extra) {
   constexpr bool ACC = sizeof(T) == 4;  // fp32 layers: the exact functions
@@ -53,14 +53,10 @@ __device__ __forceinline__ float epi_finish(const LinearArgs& a, long long m, in
             b == kCkptNanByte ? (int8_t)0 : (int8_t)ckpt8_q(held, ckpt8_inv_step(b));
       if ((c & (kCkptGroup - 1)) == 0 && ok) a.scale[m * a.lds + c / kCkptGroup] = (uint8_t)b;
     }
-    with_act(a.act, [&](auto tag) {
-      v = act_value_of<ACC, decltype(tag)::value>(v, a.slope) + extra;
-    });
-  } else if (a.act != MLP_ACT_NONE || a.u_out) {
-    float f = 0.f;
-    with_act(a.act, [&](auto tag) {
-      v *= act_grad_of<ACC, decltype(tag)::value>(extra, a.slope, f);
-    });
+    v = act_value_of<ACC, ACT>(v, a.slope) + extra;
+  } else if (ACT != MLP_ACT_NONE || a.u_out) {
+    float f;
+    v *= act_grad_of<ACC, ACT>(extra, a.slope, f);
     if (a.u_out && ok) from_f32(f, static_cast<T*>(a.u_out)[m * a.ldu_out + c]);
   }
   if (ok) {
@@ -73,11 +69,10 @@ __device__ __forceinline__ float epi_finish(const LinearArgs& a, long long m, in
 // ------------------------------------------------------------ epilogue pass
 
 constexpr int kRowsAhead = 4;  // rows loaded before the first is finished
-constexpr int kUnitRows = 32;  // rows of a backward unit (one row of colpart)
 
-// Warp unit: `unit_rows` rows of 32 columns; in the backward 32 rows, whose
-// column sums it adds in row order into one row of colpart.
-template <typename T, bool BWD, bool ELT>
+// Warp unit: `unit_rows` rows of 32 columns; in the backward it adds their
+// column sums in row order into one row of colpart.
+template <typename T, bool BWD>
 __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArgs a, int groups,
                                                                  int unit_rows,
                                                                  long long units) {
@@ -92,30 +87,158 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
   const long long m_end = min(a.T, (rb + 1) * unit_rows);
   const float bias = !BWD && a.bias && ok ? __ldg(a.bias + c) : 0.f;
   float sum = 0.f;
-  for (long long m0 = rb * unit_rows; m0 < m_end; m0 += kRowsAhead) {
-    float v[kRowsAhead], extra[kRowsAhead];
+  with_act(a.act, [&](auto tag) {
+    for (long long m0 = rb * unit_rows; m0 < m_end; m0 += kRowsAhead) {
+      float v[kRowsAhead], extra[kRowsAhead];
 #pragma unroll
-    for (int k = 0; k < kRowsAhead; ++k) {
-      const bool in = ok && m0 + k < m_end;
-      if constexpr (ELT) {
-        v[k] = in ? to_f32(static_cast<const T*>(a.x)[(m0 + k) * a.ldx + c]) : 0.f;
-      } else {
+      for (int k = 0; k < kRowsAhead; ++k) {
+        const bool in = ok && m0 + k < m_end;
         v[k] = 0.f;
         if (in) {
           const float* p = a.partial + (m0 + k) * a.ldp + c;
           for (int s = 0; s < a.splits; ++s) v[k] += __ldcs(p + (long long)s * a.T * a.ldp);
         }
+        extra[k] = epi_load<T, BWD>(a, m0 + k, c, in);
       }
-      extra[k] = epi_load<T, BWD>(a, m0 + k, c, in);
-    }
 #pragma unroll
-    for (int k = 0; k < kRowsAhead; ++k) {
-      if (m0 + k >= m_end) break;  // warp-uniform
-      v[k] = epi_finish<T, BWD>(a, m0 + k, c, ok, v[k], bias, extra[k]);
-      sum += v[k];
+      for (int k = 0; k < kRowsAhead; ++k) {
+        if (m0 + k >= m_end) break;  // warp-uniform
+        v[k] = epi_finish<T, BWD, decltype(tag)::value>(a, m0 + k, c, ok, v[k], bias, extra[k]);
+        sum += v[k];
+      }
+    }
+  });
+  if (BWD && a.colpart && ok) a.colpart[rb * a.ldcp + c] = sum;
+}
+
+// ------------------------------------------------------------ activation backward
+//
+// du = dy f'(u), a = f(u) and partial column sums: bound by HBM.  A warp takes
+// 32 rows of 32 V columns, V per lane: four where all rows keep them aligned
+// (8- and 16-byte accesses), else one (whole 32-value runs at any alignment).
+// Two batches of rows are in flight: the next one's loads are issued before
+// this one's arithmetic (one batch at a time, 10,007 x 1,001 fp32: 52 us).
+
+template <typename T, int V>
+__device__ __forceinline__ void load_cols(const T* p, bool in, int n, float (&v)[V]) {
+  if constexpr (V == 1) {
+    v[0] = in && n > 0 ? to_f32(*p) : 0.f;
+  } else {
+    if (in && n >= V) {
+      union {
+        uint4 q4;
+        uint2 q2;
+        T t[V];
+      } u;
+      if constexpr (sizeof(T) == 4) u.q4 = *reinterpret_cast<const uint4*>(p);
+      else u.q2 = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = to_f32(u.t[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = in && j < n ? to_f32(p[j]) : 0.f;
     }
   }
-  if (BWD && a.colpart && ok) a.colpart[rb * a.ldcp + c] = sum;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_cols(T* p, int n, const float (&v)[V]) {
+  if (V > 1 && n >= V) {
+    union {
+      uint4 q4;
+      uint2 q2;
+      T t[V];
+    } u;
+#pragma unroll
+    for (int j = 0; j < V; ++j) from_f32(v[j], u.t[j]);
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(p) = u.q4;
+    else *reinterpret_cast<uint2*>(p) = u.q2;
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) from_f32(v[j], p[j]);
+  }
+}
+
+template <typename T, int V, bool CK>
+__global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a, int groups,
+                                                              long long units) {
+  constexpr int R = V == 1 ? 4 : 2;  // rows of a batch
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const long long rb = unit / groups;
+  const int c = ((int)(unit - rb * groups) * 32 + lane) * V;
+  const int n = a.N - c;  // this lane's columns that exist
+  const long long m0 = rb * kPartRows;
+  const int rows = (int)min((long long)kPartRows, a.T - m0);
+  const bool has_u = CK || a.u_in != nullptr;
+  const T* dy = static_cast<const T*>(a.x) + m0 * a.ldx + c;
+  const T* u = static_cast<const T*>(a.u_in) + m0 * a.ldu_in + c;
+  const int8_t* q = a.q + m0 * a.ldq + c;
+  const uint8_t* sc = a.scale + m0 * a.lds + c / kCkptGroup;
+  T* du = static_cast<T*>(a.y) + m0 * a.ldy + c;
+  T* ao = static_cast<T*>(a.u_out) + m0 * a.ldu_out + c;
+  float g[R][V], x[R][V];
+  float sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[j] = 0.f;
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int r = r0 + k;
+      const bool in = r < rows;
+      load_cols<T, V>(dy + (long long)r * a.ldx, in, n, g[k]);
+      if constexpr (CK) {
+        const float step = in && n > 0 ? ckpt8_step(sc[(long long)r * a.lds]) : 0.f;
+        const int8_t* p = q + (long long)r * a.ldq;
+        if (V == 4 && in && n >= V) {
+          const uint32_t w = ckpt8_flip(*reinterpret_cast<const uint32_t*>(p));
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[k][j] = ckpt8_value(w, j, step);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[k][j] = in && j < n ? (float)p[j] * step : 0.f;
+        }
+      } else if (has_u) {
+        load_cols<T, V>(u + (long long)r * a.ldu_in, in, n, x[k]);
+      }
+    }
+  };
+  load(0);
+  with_act(a.act, [&](auto tag) {
+    constexpr int ACT = decltype(tag)::value;
+    for (int r0 = 0; r0 < rows; r0 += R) {
+      float gc[R][V], xc[R][V];
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          gc[k][j] = g[k][j];
+          xc[k][j] = has_u ? x[k][j] : 0.f;
+        }
+      if (r0 + R < rows) load(r0 + R);
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (r0 + k >= rows) break;  // warp-uniform
+        float f[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          gc[k][j] *= act_grad_of<sizeof(T) == 4, ACT>(xc[k][j], a.slope, f[j]);
+          sum[j] += gc[k][j];
+        }
+        store_cols<T, V>(du + (long long)(r0 + k) * a.ldy, n, gc[k]);
+        if (a.u_out) store_cols<T, V>(ao + (long long)(r0 + k) * a.ldu_out, n, f);
+      }
+    }
+  });
+  if (a.colpart) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < n) a.colpart[rb * a.ldcp + c + j] = sum[j];
+  }
 }
 
 // ------------------------------------------------------------ a few rows
@@ -123,25 +246,47 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
 // Up to 8 rows: bound by reading W once.  A cluster of S CTAs takes 64 or 128
 // output columns, each CTA one slice of K; the S partial results meet in
 // distributed shared memory and the cluster's warps run the epilogue, so the
-// call is one launch without a workspace.  Each CTA: 256 threads, 16-byte
-// loads of W straight to registers (every element is used by this CTA alone;
-// shared memory would only add a hop), the rows of x in shared memory as fp32.
+// call is one launch without a workspace.  Each CTA: 256 threads, each with a
+// ring of 16-byte pieces of W that it alone fills (asynchronous copies) and
+// reads, so the stream needs no barriers and the depth of the ring, not the
+// registers, sets the bytes in flight; the rows of x are in shared memory as
+// fp32.
 //   forward, W [K][N]: a thread keeps 16 bytes of columns and walks down K
-//   (256-byte runs of W per 128 columns), the next loads in flight while the
-//   last are used;
+//   (256-byte runs of W per 128 columns);
 //   backward, W [N][K]: a warp keeps 8 of the 64 columns and its lanes walk
 //   along K.
 // All CTAs of a launch are resident at once: a second wave of a few would
-// double the time.
+// double the time (8,192 x 8,192 bf16, one row: 70 us).
 
-constexpr int kFewX = 4096;  // values of x staged at a time (all rows)
+constexpr int kFewX = 4096;   // values of x staged at a time (all rows)
+constexpr int kFewRing = 8;   // pieces of a thread's ring
 
-// CTAs that an SM holds (by registers), and the K values staged at a time.
-template <int MT, bool BWD>
+template <int MT, bool BWD, int COLS>
 struct FewShape {
-  static constexpr int kPerSm = (MT == 1 ? 4 : MT == 2 ? 3 : MT == 4 ? 3 : 2) - (BWD ? 1 : 0);
+  static constexpr int kPerSm = MT <= 2 ? 4 : MT == 4 ? 3 : 2;  // CTAs an SM holds (registers)
   static constexpr int kChunk = kFewX / MT;
+  // ring (the forward's reduction takes its place), x, this CTA's sums
+  static constexpr int kRing = kFewRing * kThreads * 16;
+  static constexpr int kSmem = kRing + kFewX * 4 + MT * COLS * 4;
+  static_assert(8 * MT * COLS * 4 <= kRing, "reduction in the ring's place");
 };
+
+// One piece of W into the thread's slot: asynchronously where it is whole and
+// aligned, else value by value (the same thread reads it, in program order).
+template <typename T>
+__device__ __forceinline__ void few_issue(uint4* slot, const T* p, int n, bool vec) {
+  if (vec && n >= RowVec<T>::N) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(slot)), "l"(p)
+                 : "memory");
+  } else {
+    *slot = load_piece(p, n, false);
+  }
+}
+__device__ __forceinline__ void few_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void few_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 // Sums of V <= 32 values over the warp's lanes: lane L gets that of value
 // L % V.  Halving rounds as in a transposition, then a butterfly.
@@ -169,20 +314,23 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 }
 
 template <typename T, int MT, bool BWD, int COLS>
-__global__ void __launch_bounds__(kThreads, FewShape<MT, BWD>::kPerSm)
+__global__ void __launch_bounds__(kThreads, FewShape<MT, BWD, COLS>::kPerSm)
     linear_few_kernel(const LinearArgs a, int cluster, int slice, int w_vec, float* dbias) {
+  using Shape = FewShape<MT, BWD, COLS>;
   constexpr int N = RowVec<T>::N;
-  constexpr int LPR = COLS / N < 32 ? COLS / N : 32;  // forward: lanes across the columns
-  constexpr int KP = kThreads / LPR;                  // forward: rows of W per step
-  constexpr int U = 4;                                // loads a thread issues together
-  constexpr int CHUNK = FewShape<MT, BWD>::kChunk;
-  static_assert(LPR * N == COLS && (!BWD || COLS == 64), "columns of a CTA");
-  __shared__ __align__(16) float xs[CHUNK * MT];   // forward [k][MT], backward [MT][k]
-  __shared__ float red[BWD ? 1 : 8 * MT * COLS];   // forward: [warp][MT][COLS]
-  __shared__ float part[MT * COLS];                // this CTA's sums, read by the cluster
+  constexpr int LPR = COLS / N;       // forward: lanes across the columns
+  constexpr int KP = kThreads / LPR;  // forward: rows of W per step
+  constexpr int CHUNK = Shape::kChunk;
+  constexpr int D = kFewRing;
+  static_assert(LPR <= 32 && (!BWD || COLS == 64), "columns of a CTA");
+  extern __shared__ __align__(16) uint8_t few_smem[];
+  float* xs = reinterpret_cast<float*>(few_smem + Shape::kRing);  // forward [k][MT], backward [MT][k]
+  float* red = reinterpret_cast<float*>(few_smem);                // forward: [warp][MT][COLS]
+  float* part = xs + kFewX;  // [MT][COLS]: this CTA's sums, read by the cluster
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint4* ring = reinterpret_cast<uint4*>(few_smem) + tid;  // slot i at [i * kThreads]
   pdl_wait();
   pdl_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % cluster;
   const int c0 = (int)(blockIdx.x / cluster) * COLS;
   const int k_lo = rank * slice, k_hi = min(a.K, k_lo + slice);
@@ -211,80 +359,105 @@ __global__ void __launch_bounds__(kThreads, FewShape<MT, BWD>::kPerSm)
       __syncthreads();
     };
     if constexpr (!BWD) {
-      const int c = c0 + (tid % LPR) * N;
-      const int cols = a.N - c;
-      const T* wp = w + (long long)(kc + tid / LPR) * a.ldw + c;
-      uint4 raw[U];
-      auto load = [&](int k0) {
-#pragma unroll
-        for (int i = 0; i < U; ++i)
-          raw[i] = load_piece(wp + (long long)(k0 + i * KP) * a.ldw,
-                              k0 + tid / LPR + i * KP < len ? cols : 0, w_vec);
+      // step s: row tid / LPR + s KP of the chunk
+      const int k_first = tid / LPR;
+      const int c = c0 + (tid % LPR) * N, cols = a.N - c;
+      const T* wp = w + (long long)(kc + k_first) * a.ldw + c;
+      const long long step = (long long)KP * a.ldw;
+      const int steps = (len - k_first + KP - 1) / KP;
+      auto issue = [&](int st, int slot) {
+        if (st < steps) few_issue(ring + slot * kThreads, wp + st * step, cols, w_vec);
+        few_commit();
       };
-      load(0);
+#pragma unroll
+      for (int i = 0; i < D - 1; ++i) issue(i, i);
       stage_x();
-      for (int k0 = 0; k0 < len; k0 += KP * U) {
-        uint4 cur[U];
+      for (int s0 = 0; s0 < steps; s0 += D) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) cur[i] = raw[i];
-        if (k0 + KP * U < len) load(k0 + KP * U);
+        for (int i = 0; i < D; ++i) {
+          few_wait<D - 2>();  // step s0 + i has landed
+          if (s0 + i < steps) {
+            F2 wv[N / 2];
+            float xv[MT];
+            unpack_piece<T>(ring[i * kThreads], wv);
+            const float* xk = xs + (k_first + (s0 + i) * KP) * MT;
+            if constexpr (MT >= 4) {
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-          const int k = k0 + tid / LPR + i * KP;
-          if (k >= len) break;
-          float wv[N], xv[MT];
-          unpack_piece<T>(cur[i], wv);
+              for (int m = 0; m < MT; m += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(xk + m);
+                xv[m] = f.x;
+                xv[m + 1] = f.y;
+                xv[m + 2] = f.z;
+                xv[m + 3] = f.w;
+              }
+            } else {
 #pragma unroll
-          for (int m = 0; m < MT; ++m) xv[m] = xs[k * MT + m];
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int j = 0; j < N; ++j) acc[m][j] = fmaf(xv[m], wv[j], acc[m][j]);
-        }
-      }
-    } else {
-      // steps of four of the warp's eight columns and 32 N of K
-      uint4 raw[4];
-      auto load = [&](int k, int h) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = c0 + warp * 8 + h + j;
-          raw[j] = load_piece(w + (long long)c * a.ldw + kc + k, c < a.N ? len - k : 0, w_vec);
-        }
-      };
-      load(lane * N, 0);
-      stage_x();
-      for (int k = lane * N; k < len; k += 32 * N) {
-#pragma unroll
-        for (int h = 0; h < 8; h += 4) {
-          float wv[4][N];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) unpack_piece<T>(raw[j], wv[j]);
-          if (h == 0) load(k, 4);
-          else if (k + 32 * N < len) load(k + 32 * N, 0);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            float xv[N];
-#pragma unroll
-            for (int e = 0; e < N; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(xs + m * CHUNK + k + e);
-              xv[e] = f.x;
-              xv[e + 1] = f.y;
-              xv[e + 2] = f.z;
-              xv[e + 3] = f.w;
+              for (int m = 0; m < MT; ++m) xv[m] = xk[m];
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int m = 0; m < MT; ++m)
 #pragma unroll
-              for (int e = 0; e < N; ++e) acc[m][h + j] = fmaf(xv[e], wv[j][e], acc[m][h + j]);
+              for (int j = 0; j < N; j += 2) {
+                const F2 r = fma2(f2(xv[m]), wv[j / 2], f2(acc[m][j], acc[m][j + 1]));
+                acc[m][j] = r.x;
+                acc[m][j + 1] = r.y;
+              }
           }
+          issue(s0 + i + D - 1, (i + D - 1) % D);
         }
       }
+      few_wait<0>();
+    } else {
+      // step s: column s % 8 of the warp, piece lane + 32 (s / 8) of the chunk
+      static_assert(D == 8, "a ring turn is the warp's eight columns");
+      const T* wp = w + (long long)(c0 + warp * 8) * a.ldw + kc + lane * N;
+      auto issue = [&](int k, int j) {  // k: offset from the lane's first piece
+        if (k + lane * N < len)
+          few_issue(ring + j * kThreads, wp + j * a.ldw + k,
+                    c0 + warp * 8 + j < a.N ? len - k - lane * N : 0, w_vec);
+        few_commit();
+      };
+#pragma unroll
+      for (int j = 0; j < D - 1; ++j) issue(0, j);
+      stage_x();
+      for (int k = 0; k < len; k += 32 * N) {  // warp-uniform
+        const bool in = k + lane * N < len;
+#pragma unroll
+        for (int j = 0; j < D; j += 2) {
+          // two columns share the x fragments
+          few_wait<D - 3>();
+          if (in) {
+            F2 w0[N / 2], w1[N / 2];
+            unpack_piece<T>(ring[j * kThreads], w0);
+            unpack_piece<T>(ring[(j + 1) * kThreads], w1);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              F2 s0 = f2(acc[m][j], 0.f), s1 = f2(acc[m][j + 1], 0.f);
+#pragma unroll
+              for (int e = 0; e < N; e += 4) {
+                const float4 f =
+                    *reinterpret_cast<const float4*>(xs + m * CHUNK + k + lane * N + e);
+                s0 = fma2(f2(f.x, f.y), w0[e / 2], s0);
+                s1 = fma2(f2(f.x, f.y), w1[e / 2], s1);
+                s0 = fma2(f2(f.z, f.w), w0[e / 2 + 1], s0);
+                s1 = fma2(f2(f.z, f.w), w1[e / 2 + 1], s1);
+              }
+              acc[m][j] = s0.x + s0.y;
+              acc[m][j + 1] = s1.x + s1.y;
+            }
+          }
+          if (j == 0) issue(k, D - 1);
+          else issue(k + 32 * N, j - 1);
+          issue(k + 32 * N, j);
+        }
+      }
+      few_wait<0>();
     }
   }
 
   // this CTA's sums into part[m][column]
   if constexpr (!BWD) {
+    __syncthreads();  // every thread is done with its ring
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -335,7 +508,9 @@ __global__ void __launch_bounds__(kThreads, FewShape<MT, BWD>::kPerSm)
       for (int r = 0; r < cluster; ++r)  // in slice order
         v += ld_cluster_f32(ptx::mapa_shared(
             part0 + (uint32_t)(m * COLS + g * 32 + lane) * 4u, (uint32_t)r));
-      sum += epi_finish<T, BWD>(a, m, c, ok, v, bias, extra);
+      with_act(a.act, [&](auto tag) {
+        sum += epi_finish<T, BWD, decltype(tag)::value>(a, m, c, ok, v, bias, extra);
+      });
     }
     if (BWD && dbias && ok) dbias[c] = sum;
   }
@@ -344,12 +519,17 @@ __global__ void __launch_bounds__(kThreads, FewShape<MT, BWD>::kPerSm)
 
 template <typename T, int MT, bool BWD, int COLS>
 mlp_status few_launch(const LinearArgs& a, float* dbias, cudaStream_t st) {
+  using Shape = FewShape<MT, BWD, COLS>;
+  static const cudaError_t configured =
+      cudaFuncSetAttribute(linear_few_kernel<T, MT, BWD, COLS>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+  if (configured != cudaSuccess) return MLP_ERR_CUDA;
   // the widest cluster with which all CTAs are resident (on 152 SMs) and each
   // still has 128 of K
   const long long tiles = (a.N + COLS - 1) / COLS;
   int cluster = 8;
   while (cluster > 1 &&
-         (tiles * cluster > 152 * FewShape<MT, BWD>::kPerSm || a.K < 128 * cluster))
+         (tiles * cluster > 152 * Shape::kPerSm || a.K < 128 * cluster))
     --cluster;
   const int per = (a.K + cluster - 1) / cluster;
   const int slice = (per + 63) / 64 * 64;  // slices start on whole 16-byte pieces
@@ -358,6 +538,7 @@ mlp_status few_launch(const LinearArgs& a, float* dbias, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * cluster));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -389,27 +570,50 @@ mlp_status few_rows(const LinearArgs& a, float* dbias, cudaStream_t st) {
   return few_cols<T, 8, BWD>(a, dbias, st);
 }
 
-template <typename T, bool BWD, bool ELT>
+template <typename T, bool BWD>
 mlp_status finish_launch(const LinearArgs& a, cudaStream_t st) {
   const int groups = (a.N + 31) / 32;
-  const int unit_rows = BWD ? kUnitRows : kRowsAhead;
+  const int unit_rows = BWD ? a.part_rows : kRowsAhead;
   const long long units = (a.T + unit_rows - 1) / unit_rows * groups;
   const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
-  LaunchScope ls(ELT ? "act_bwd" : BWD ? "linear_bwd_finish" : "linear_fwd_finish", st, a.T, a.N,
-                 a.splits);
-  launch_k(linear_finish_kernel<T, BWD, ELT>, dim3((unsigned)blocks), dim3(kThreads), 0, st, a,
-           groups, unit_rows, units);
+  LaunchScope ls(BWD ? "linear_bwd_finish" : "linear_fwd_finish", st, a.T, a.N, a.splits);
+  launch_k(linear_finish_kernel<T, BWD>, dim3((unsigned)blocks), dim3(kThreads), 0, st, a, groups,
+           unit_rows, units);
+  return launch_status();
+}
+
+template <typename T, int V, bool CK>
+mlp_status act_launch(const LinearArgs& a, cudaStream_t st) {
+  const int groups = (a.N + 32 * V - 1) / (32 * V);
+  const long long units = (a.T + kPartRows - 1) / kPartRows * groups;
+  const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
+  LaunchScope ls("act_bwd", st, a.T, a.N, sizeof(T));
+  launch_k(act_bwd_kernel<T, V, CK>, dim3((unsigned)blocks), dim3(kThreads), 0, st, a, groups,
+           units);
   return launch_status();
 }
 
 template <typename T>
-mlp_status finish_t(const LinearArgs& a, bool bwd, bool elementwise, cudaStream_t st) {
-  if (elementwise) return finish_launch<T, true, true>(a, st);
-  return bwd ? finish_launch<T, true, false>(a, st) : finish_launch<T, false, false>(a, st);
+mlp_status act_t(const LinearArgs& a, cudaStream_t st) {
+  // four columns per lane where every matrix keeps them aligned (base pointers
+  // are 16-byte aligned)
+  const bool vec = a.ldx % 4 == 0 && a.ldy % 4 == 0 && (!a.u_in || a.ldu_in % 4 == 0) &&
+                   (!a.q || a.ldq % 4 == 0) && (!a.u_out || a.ldu_out % 4 == 0);
+  if (a.q) return vec ? act_launch<T, 4, true>(a, st) : act_launch<T, 1, true>(a, st);
+  return vec ? act_launch<T, 4, false>(a, st) : act_launch<T, 1, false>(a, st);
 }
 
 }  // namespace
+
+// Up to 8 rows for fp32 (whose tiled kernel computes 64 rows whatever T is);
+// in 16 bits the tensor cores take over once the products' FMAs, not the reading
+// of W, bound this kernel.
+bool linear_takes_few(long long T, int K, int N, int dtype) {
+  if (dtype == MLP_DTYPE_F32) return T <= 8;
+  return T <= 2 || (T <= 8 && (long long)K * N <= (1ll << 22));
+}
 
 mlp_status launch_linear_few(const LinearArgs& a, bool bwd, float* dbias, cudaStream_t st) {
   switch (a.dtype) {
@@ -423,11 +627,22 @@ mlp_status launch_linear_few(const LinearArgs& a, bool bwd, float* dbias, cudaSt
   }
 }
 
-mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, bool elementwise, cudaStream_t st) {
+mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, cudaStream_t st) {
   switch (a.dtype) {
-    case MLP_DTYPE_BF16: return finish_t<__nv_bfloat16>(a, bwd, elementwise, st);
-    case MLP_DTYPE_F16: return finish_t<__half>(a, bwd, elementwise, st);
-    default: return finish_t<float>(a, bwd, elementwise, st);
+    case MLP_DTYPE_BF16:
+      return bwd ? finish_launch<__nv_bfloat16, true>(a, st)
+                 : finish_launch<__nv_bfloat16, false>(a, st);
+    case MLP_DTYPE_F16:
+      return bwd ? finish_launch<__half, true>(a, st) : finish_launch<__half, false>(a, st);
+    default: return bwd ? finish_launch<float, true>(a, st) : finish_launch<float, false>(a, st);
+  }
+}
+
+mlp_status launch_act_bwd(const LinearArgs& a, cudaStream_t st) {
+  switch (a.dtype) {
+    case MLP_DTYPE_BF16: return act_t<__nv_bfloat16>(a, st);
+    case MLP_DTYPE_F16: return act_t<__half>(a, st);
+    default: return act_t<float>(a, st);
   }
 }
 

@@ -244,26 +244,29 @@ struct LinearArgs {
   long long ldq;
   uint8_t* scale;
   long long lds;
-  float* colpart;    // backward: fp32 [linear_part_rows(T)][ldcp] partial column sums (nullable)
+  float* colpart;    // backward: fp32 [ceil(T / part_rows)][ldcp] partial column sums (nullable)
+  int part_rows;     // rows of du to a row of colpart: 32 but in launch_linear_finish
   long long ldcp;
   float* partial;    // fp32 [splits][T][ldp] raw sums
   long long ldp;
   int splits;
 };
-// Rows of colpart: one per 32 rows of du.
-inline long long linear_part_rows(long long T) { return (T + 31) / 32; }
+constexpr int kPartRows = 32;
+// ... where few rows would leave a pass over raw sums with few warps
+constexpr int kPartRowsFew = 4;
 // k_linear.cu: tcgen05 kernel of 16-bit operands.  splits > 1: raw partial
 // sums into a.partial, to be finished by launch_linear_finish.
 mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st);
 // Split count of that kernel (from the shape alone).
 int linear_tc_splits(long long T, int K, int N);
-// k_linear_small.cu: up to kLinearFewRows rows, all types, one launch; in the
-// backward it writes the column sums to `dbias` itself.
-constexpr int kLinearFewRows = 8;
+// k_linear_small.cu: a few rows, all types, one launch; in the backward it
+// writes the column sums to `dbias` itself.
+bool linear_takes_few(long long T, int K, int N, int dtype);
 mlp_status launch_linear_few(const LinearArgs& a, bool bwd, float* dbias, cudaStream_t st);
-// k_linear_small.cu: the epilogue over a.splits planes of raw sums
-// (a.partial), or, with elementwise set, over dy itself (a.x).
-mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, bool elementwise, cudaStream_t st);
+// k_linear_small.cu: the epilogue over a.splits planes of raw sums (a.partial).
+mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, cudaStream_t st);
+// k_linear_small.cu: the backward epilogue with dy (a.x) in the product's place.
+mlp_status launch_act_bwd(const LinearArgs& a, cudaStream_t st);
 
 // Host helpers (api.cu)
 unsigned long long wait_limit_ns();

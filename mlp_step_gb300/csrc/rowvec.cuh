@@ -6,7 +6,7 @@
 
 #include <type_traits>
 
-#include "common.cuh"
+#include "f32x2.cuh"
 
 namespace mlp {
 
@@ -53,6 +53,26 @@ __device__ __forceinline__ void unpack_piece(const uint4& q, float (&v)[RowVec<T
   const T* h = reinterpret_cast<const T*>(&q);
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = to_f32(h[j]);
+}
+
+// The same in pairs.
+template <typename T>
+__device__ __forceinline__ void unpack_piece(const uint4& q, F2 (&v)[RowVec<T>::N / 2]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (sizeof(T) == 4) {
+    v[0] = f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[1] = f2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        v[j] = f2(f.x, f.y);
+      } else {
+        v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+      }
+    }
+  }
 }
 
 template <typename T>

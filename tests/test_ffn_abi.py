@@ -142,14 +142,18 @@ def test_binding_refuses_what_the_library_cannot_read():
     with pytest.raises(ValueError, match="CUDA device"):
         M.mlp_act_bwd(x, x, u=x)
     with pytest.raises(ValueError, match=r"\[4, 64\]"):
-        M._mat(x[:, :32], "y", 4, 64)
+        M._mat(x[:, :32], "y", 4, 64, 0)
     with pytest.raises(TypeError):
-        M._mat(x, "y", 4, 64, torch.bfloat16)
-    with pytest.raises(ValueError):
-        M._vec(v[:32], "gain", 64)
-    with pytest.raises(TypeError):
-        M._vec(v.double(), "gain", 64)
+        M._mat(x, "y", 4, 64, 0, torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA device"):
-        M._ws(x)
+        M._mat(x, "y", 4, 64, 0)
+    with pytest.raises(ValueError, match="adjacent"):
+        M._mat(torch.zeros(64, 4).t(), "y", 4, 64, -1)
+    with pytest.raises(ValueError):
+        M._vec(v[:32], "gain", 64, 0)
+    with pytest.raises(TypeError):
+        M._vec(v.double(), "gain", 64, 0)
+    with pytest.raises(ValueError, match="CUDA device"):
+        M._ws(x, 0)
     with pytest.raises(TypeError):
         M.mlp_linear_workspace_bytes(4, 64, 64, torch.float64)
