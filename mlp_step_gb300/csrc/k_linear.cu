@@ -34,21 +34,22 @@ namespace mlp {
 namespace {
 
 constexpr int BK = 64;
-// Staging bytes of an epilogue warp: a box of 32 rows x 128 bytes for y / du
-// (or two boxes of 32 rows x 64 bytes, for y / du and u / a), then 32 rows x 64
-// bytes of 8-bit values.
+// Staging bytes of an epilogue warp: 32 rows x 128 bytes for y / du (or two
+// boxes of 32 rows x 64 bytes, for y / du and u / a), then 32 rows x 64 bytes
+// of 8-bit values.  Everything that the epilogue reads and writes beside the
+// accumulator passes through these boxes, so its arithmetic has one form; rows
+// that TMA cannot address, and ragged columns, are moved between box and
+// matrix by the warp's own copies.
 constexpr int kBox = 4096, kWarpStage = kBox + 2048;
 
 struct LinParams {
   LinearArgs a;
   int tiles_m, tiles_n, units, k_blocks, kb_per_split;
   int a_bytes;  // of a stage's x tile: fewer than 128 rows when there are fewer
-  // What moves by TMA between the matrices and the warps' staging boxes:
-  int y64;     // y / du in boxes of 64 columns, stored once per unit
-  int tma_y;   // y / du in boxes of 32 columns (with u_out, or fp32)
-  int tma_u;   // u_out likewise
-  int tma_in;  // the 16-bit residual / u, loaded into the y64 box and replaced there
-  int tma_q;   // the 8-bit values, in (backward) or out (forward)
+  int y64;  // y / du in boxes of 64 columns (16-bit, no u_out), else of 32
+  // What moves by TMA: y / du; u_out; the 16-bit residual / u (into the y64 box,
+  // where the output replaces it); the 8-bit values
+  int tma_y, tma_u, tma_in, tma_q;
   unsigned long long wait_ns;
   int* err;
 };
@@ -100,86 +101,65 @@ __device__ __forceinline__ F2 unpack2(uint32_t w) {
   }
 }
 
-// 32 consecutive 16-bit values of a row from memory (where TMA does not bring
-// them: unaligned rows, fp32 layers' shapes); values past n read as zero.
-__device__ __forceinline__ void load_row16(const void* row, int n, uint4 (&q)[4]) {
-  const uint16_t* p = static_cast<const uint16_t*>(row);
-  if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) q[k] = *(reinterpret_cast<const uint4*>(p) + k);
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(q);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t lo = 2 * k < n ? p[2 * k] : 0u;
-      const uint32_t hi = 2 * k + 1 < n ? p[2 * k + 1] : 0u;
-      w[k] = lo | hi << 16;
-    }
-  }
+// 16-byte chunk c of row r of a box whose rows are 64 or 128 bytes, in the
+// swizzle that a tensor map of that width names.
+__device__ __forceinline__ uint8_t* chunk_at(uint8_t* box, int row_bytes, int r, int c) {
+  const int swz = row_bytes == 128 ? r & 7 : (r >> 1) & 3;
+  return box + r * row_bytes + ((c ^ swz) << 4);
 }
 
-__device__ __forceinline__ void load_row8(const int8_t* p, int n, uint4 (&q)[2]) {
-  if (n >= 32 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-    q[0] = *reinterpret_cast<const uint4*>(p);
-    q[1] = *(reinterpret_cast<const uint4*>(p) + 1);
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(q);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      w[k] = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * k + e < n) w[k] |= (uint32_t)(uint8_t)p[4 * k + e] << (8 * e);
+// The warp's own copy between a box and a matrix: `rows` rows of `bytes` bytes,
+// `esz` per value, at mem with a pitch of ld bytes.  16-byte pieces where rows
+// and widths allow, else one value per lane (runs of 32 values either way).
+template <bool OUT>
+__device__ __forceinline__ void warp_copy(uint8_t* box, int row_bytes, uint8_t* mem, long long ld,
+                                          int rows, int bytes, int esz, int lane) {
+  __syncwarp();
+  if ((reinterpret_cast<uintptr_t>(mem) & 15) == 0 && (ld & 15) == 0 && (bytes & 15) == 0) {
+    const int per = bytes >> 4;
+#pragma unroll 1
+    for (int i = lane; i < rows * per; i += 32) {
+      const int r = i / per, c = i - r * per;
+      uint4* b = reinterpret_cast<uint4*>(chunk_at(box, row_bytes, r, c));
+      uint4* m = reinterpret_cast<uint4*>(mem + r * ld + c * 16);
+      if (OUT) *m = *b;
+      else *b = *m;
     }
+  } else {
+    const int n = bytes / esz;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r)
+#pragma unroll 1
+      for (int j = lane; j < n; j += 32) {
+        const int o = j * esz;
+        uint8_t* b = chunk_at(box, row_bytes, r, o >> 4) + (o & 15);
+        uint8_t* m = mem + r * ld + o;
+        if (esz == 1) {
+          if (OUT) *m = *b;
+          else *b = *m;
+        } else if (esz == 2) {
+          if (OUT) *reinterpret_cast<uint16_t*>(m) = *reinterpret_cast<uint16_t*>(b);
+          else *reinterpret_cast<uint16_t*>(b) = *reinterpret_cast<uint16_t*>(m);
+        } else {
+          if (OUT) *reinterpret_cast<uint32_t*>(m) = *reinterpret_cast<uint32_t*>(b);
+          else *reinterpret_cast<uint32_t*>(b) = *reinterpret_cast<uint32_t*>(m);
+        }
+      }
   }
+  __syncwarp();
 }
 
-// Values [8k, 8k + 8) of a piece into this lane's row of a staging box, whose
-// 16-byte chunk c lies at c ^ swz (the swizzle that the box's tensor map
-// names); `chunk`: the piece's first chunk of a 16-bit row.
+// A piece's 32 values into this lane's row of a 16-bit box (from chunk `c0`).
 template <int H16>
-__device__ __forceinline__ void box8(uint8_t* row, int chunk, int swz, int f32, int k,
-                                     const F2 (&v)[4]) {
-  if (f32) {
-    *reinterpret_cast<float4*>(row + (((2 * k) ^ swz) << 4)) =
-        make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-    *reinterpret_cast<float4*>(row + (((2 * k + 1) ^ swz) << 4)) =
-        make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-  } else {
-    *reinterpret_cast<uint4*>(row + (((chunk + k) ^ swz) << 4)) =
-        make_uint4(pack16x2<H16>(v[0].x, v[0].y), pack16x2<H16>(v[1].x, v[1].y),
-                   pack16x2<H16>(v[2].x, v[2].y), pack16x2<H16>(v[3].x, v[3].y));
-  }
-}
-
-// The same into the matrix, for ragged units, unaligned rows and small
-// outputs: `off` is the offset of the piece's first column, n its columns that
-// exist (0: a row past the end).
-template <int H16>
-__device__ __forceinline__ void mem8(void* base, long long off, int f32, int k, int n,
-                                     const F2 (&v)[4]) {
-  if (f32) {
-    float* p = static_cast<float*>(base) + off + 8 * k;
-    if (8 * k + 8 <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-      reinterpret_cast<float4*>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-      reinterpret_cast<float4*>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-    } else {
+__device__ __forceinline__ void pack_row(uint8_t* box, int row_bytes, int lane, int c0,
+                                         const F2 (&v)[16]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (8 * k + j < n) p[j] = j & 1 ? v[j / 2].y : v[j / 2].x;
-    }
-  } else {
-    uint16_t* p = static_cast<uint16_t*>(base) + off + 8 * k;
-    if (8 * k + 8 <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
-      *reinterpret_cast<uint4*>(p) =
-          make_uint4(pack16x2<H16>(v[0].x, v[0].y), pack16x2<H16>(v[1].x, v[1].y),
-                     pack16x2<H16>(v[2].x, v[2].y), pack16x2<H16>(v[3].x, v[3].y));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (8 * k + j < n) p[j] = f32_to_16<H16>(j & 1 ? v[j / 2].y : v[j / 2].x);
-    }
-  }
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4*>(chunk_at(box, row_bytes, lane, c0 + k)) =
+        make_uint4(pack16x2<H16>(v[4 * k].x, v[4 * k].y),
+                   pack16x2<H16>(v[4 * k + 1].x, v[4 * k + 1].y),
+                   pack16x2<H16>(v[4 * k + 2].x, v[4 * k + 2].y),
+                   pack16x2<H16>(v[4 * k + 3].x, v[4 * k + 3].y));
 }
 
 // Four consecutive bias values.  Volatile, so that the loads stay ahead of the
@@ -256,7 +236,7 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&maps.a);
     ptx::prefetch_tensormap(&maps.b);
-    if (p.y64 || p.tma_y) ptx::prefetch_tensormap(&maps.y);
+    if (p.tma_y) ptx::prefetch_tensormap(&maps.y);
     if (p.tma_u) ptx::prefetch_tensormap(&maps.u);
     if (p.tma_in) ptx::prefetch_tensormap(&maps.in);
     if (p.tma_q) ptx::prefetch_tensormap(&maps.q);
@@ -406,8 +386,6 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
     const uint32_t tempty0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
     uint8_t* box = stg + ew * kWarpStage;
     uint8_t* qbox = box + kBox;
-    uint8_t* qrow = qbox + lane * 64;
-    const int swz64 = (lane >> 1) & 3, swz128 = lane & 7;
     bool stores = false;      // a store of this warp may still read its boxes
     bool in_flight = false;   // an input box is on its way
     uint32_t in_phase = 0;
@@ -514,27 +492,41 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
             in_flight = false;
           }
         }
-        // Ragged units leave from registers: the bulk stores write whole
-        // 16-byte units, so they would touch columns past N.
+        // Ragged units do not leave by TMA: the bulk stores write whole 16-byte
+        // units, so they would touch columns past N.
         const bool whole = t.n0 + 64 <= a.N;
-        const bool y64 = p.y64 && whole, y32 = p.tma_y && whole, u32 = p.tma_u && whole;
-        const bool q64 = p.tma_q && whole;
+        const int rows = (int)min(32ll, a.T - t.row0);
+        const int esz = a.out_f32 ? 4 : 2;
+        const int y_bytes = p.y64 || a.out_f32 ? 128 : 64;  // of a box row
+        // the 16-bit input: residual (forward) or u (backward)
+        const uint8_t* in16 = reinterpret_cast<const uint8_t*>(BWD ? a.u_in : a.out_f32 ? nullptr : a.res);
+        const long long ld_in = (BWD ? a.ldu_in : a.ldr) * 2;
+        uint8_t* y_mem = static_cast<uint8_t*>(a.y) + ((long long)t.row0 * a.ldy + t.n0) * esz;
+        if (real && a.splits == 1) {
+          const int cols = min(64, a.N - t.n0);
+          if (in16 && p.y64 && !p.tma_in)
+            warp_copy<false>(box, 128,
+                             const_cast<uint8_t*>(in16) + t.row0 * ld_in + (long long)t.n0 * 2,
+                             ld_in, rows, cols * 2, 2, lane);
+          if (BWD && a.q && !p.tma_q)
+            warp_copy<false>(qbox, 64, reinterpret_cast<uint8_t*>(a.q) + t.row0 * a.ldq + t.n0,
+                             a.ldq, rows, cols, 1, lane);
+        }
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int n0 = t.n0 + 32 * h;
-          const int cols = a.N - n0;
+          const int cols = min(32, a.N - n0);
           const bool last = last_unit && h == 1;
           if (!real || cols <= 0) {  // warp-uniform
             if (last) release();
             continue;
           }
-          const int n_ok = row_ok ? cols : 0;
+          const bool end = h == 1 || a.N - n0 <= 32;  // the unit's last piece
           F2 v[16];
           {
             float4 b4[8];
-            const bool bias_vec = !BWD && a.bias && cols >= 32 && a.splits == 1;
             if constexpr (!BWD) {
-              if (bias_vec) {
+              if (a.bias && cols == 32 && a.splits == 1) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) b4[k] = load_bias4(a.bias + n0 + 4 * k);
               } else {
@@ -558,6 +550,16 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
                 v[2 * k] = add2(v[2 * k], f2(b4[k].x, b4[k].y));
                 v[2 * k + 1] = add2(v[2 * k + 1], f2(b4[k].z, b4[k].w));
               }
+              if (cols < 32 && a.splits == 1) {
+                // columns past N: zero, so that they take no part in the
+                // 8-bit group's scale
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const bool e = 2 * j < cols, o = 2 * j + 1 < cols;
+                  v[j].x = e ? v[j].x + (a.bias ? __ldg(a.bias + n0 + 2 * j) : 0.f) : 0.f;
+                  v[j].y = o ? v[j].y + (a.bias ? __ldg(a.bias + n0 + 2 * j + 1) : 0.f) : 0.f;
+                }
+              }
             }
           }
           if (a.splits > 1) {
@@ -571,166 +573,141 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
             }
             continue;
           }
-          if (h == 1 && (y32 || u32)) boxes_free();
-
-          auto put_y = [&](int k, const F2(&x)[4]) {
-            if (y64) box8<H16>(box + lane * 128, 4 * h, swz128, 0, k, x);
-            else if (y32)
-              box8<H16>(box + lane * (a.out_f32 ? 128 : 64), 0, a.out_f32 ? swz128 : swz64,
-                        a.out_f32, k, x);
-            else mem8<H16>(a.y, m * a.ldy + n0, a.out_f32, k, n_ok, x);
+          if (h == 1 && !p.y64) boxes_free();
+          // u / a leaves through the second box; beside an fp32 output, whose
+          // box is the whole space, at once and through the same space
+          auto put_u = [&](const F2(&x)[16]) {
+            uint8_t* ub = a.out_f32 ? box : box + kBox / 2;
+            pack_row<H16>(ub, 64, lane, 0, x);
+            if (!(p.tma_u && whole))
+              warp_copy<true>(ub, 64,
+                              static_cast<uint8_t*>(a.u_out) +
+                                  ((long long)t.row0 * a.ldu_out + n0) * 2,
+                              a.ldu_out * 2, rows, cols * 2, 2, lane);
           };
-          auto put_u = [&](int k, const F2(&x)[4]) {
-            if (u32) box8<H16>(box + kBox / 2 + lane * 64, 0, swz64, 0, k, x);
-            else mem8<H16>(a.u_out, m * a.ldu_out + n0, 0, k, n_ok, x);
-          };
-          // the 16-bit residual / u of this piece: in the box, or from memory
-          auto saved16 = [&](uint4 (&s)[4]) {
-            if (p.tma_in) {
+          // this piece of the 16-bit input, from the box
+          auto get16 = [&](F2(&x)[16]) {
+            if (!p.y64)
+              warp_copy<false>(box, 64,
+                               const_cast<uint8_t*>(in16) + t.row0 * ld_in + (long long)n0 * 2,
+                               ld_in, rows, cols * 2, 2, lane);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                s[k] = *reinterpret_cast<const uint4*>(box + lane * 128 +
-                                                       (((4 * h + k) ^ swz128) << 4));
-            } else if constexpr (BWD) {
-              load_row16(static_cast<const uint16_t*>(a.u_in) + m * a.ldu_in + n0, n_ok, s);
-            } else {
-              load_row16(static_cast<const uint16_t*>(a.res) + m * a.ldr + n0, n_ok, s);
+            for (int k = 0; k < 4; ++k) {
+              const uint4 q = *reinterpret_cast<const uint4*>(
+                  chunk_at(box, p.y64 ? 128 : 64, lane, (p.y64 ? 4 * h : 0) + k));
+              x[4 * k] = unpack2<H16>(q.x);
+              x[4 * k + 1] = unpack2<H16>(q.y);
+              x[4 * k + 2] = unpack2<H16>(q.z);
+              x[4 * k + 3] = unpack2<H16>(q.w);
             }
+            __syncwarp();
           };
 
           if constexpr (!BWD) {
-            if (a.bias && cols < 32) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if (2 * j < cols) v[j].x += __ldg(a.bias + n0 + 2 * j);
-                if (2 * j + 1 < cols) v[j].y += __ldg(a.bias + n0 + 2 * j + 1);
-              }
-            }
             if (a.q) {
-              if (cols < 32) {  // columns past N take no part in the group's scale
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  if (2 * j >= cols) v[j].x = 0.f;
-                  if (2 * j + 1 >= cols) v[j].y = 0.f;
-                }
-              }
               uint32_t w[8];
               const uint32_t b = ckpt8_group(reinterpret_cast<const float(&)[32]>(v), w);
-              const uint4 w0 = make_uint4(w[0], w[1], w[2], w[3]);
-              const uint4 w1 = make_uint4(w[4], w[5], w[6], w[7]);
               if (row_ok) a.scale[m * a.lds + n0 / kCkptGroup] = (uint8_t)b;
-              if (q64) {
-                *reinterpret_cast<uint4*>(qrow + (((2 * h) ^ swz64) << 4)) = w0;
-                *reinterpret_cast<uint4*>(qrow + (((2 * h + 1) ^ swz64) << 4)) = w1;
-              } else if (row_ok) {
-                int8_t* qp = a.q + m * a.ldq + n0;
-                if (cols >= 32 && (reinterpret_cast<uintptr_t>(qp) & 15) == 0) {
-                  reinterpret_cast<uint4*>(qp)[0] = w0;
-                  reinterpret_cast<uint4*>(qp)[1] = w1;
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (j < cols) qp[j] = (int8_t)(w[j / 4] >> (8 * (j & 3)));
-                }
-              }
+              *reinterpret_cast<uint4*>(chunk_at(qbox, 64, lane, 2 * h)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(chunk_at(qbox, 64, lane, 2 * h + 1)) =
+                  make_uint4(w[4], w[5], w[6], w[7]);
             }
-            if (a.u_out) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                put_u(k, reinterpret_cast<const F2(&)[4]>(v[4 * k]));
-            }
+            if (a.u_out) put_u(v);
             with_act(a.act, [&](auto tag) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 v[j] = act_value2<decltype(tag)::value>(v[j], a.slope);
             });
-            if (a.res) {
-              if (!a.out_f32) {
-                uint4 s[4];
-                saved16(s);
-                const uint32_t* sw = reinterpret_cast<const uint32_t*>(s);
+            if (in16) {
+              F2 x[16];
+              get16(x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = add2(v[j], unpack2<H16>(sw[j]));
-              } else if (row_ok) {
-                const float* rp = static_cast<const float*>(a.res) + m * a.ldr + n0;
-                if (cols >= 32 && (reinterpret_cast<uintptr_t>(rp) & 15) == 0) {
+              for (int j = 0; j < 16; ++j) v[j] = add2(v[j], x[j]);
+            } else if (a.res) {
+              warp_copy<false>(box, 128,
+                               static_cast<uint8_t*>(const_cast<void*>(a.res)) +
+                                   ((long long)t.row0 * a.ldr + n0) * 4,
+                               a.ldr * 4, rows, cols * 4, 4, lane);
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) {
-                    const float4 f = *(reinterpret_cast<const float4*>(rp) + k);
-                    v[2 * k] = add2(v[2 * k], f2(f.x, f.y));
-                    v[2 * k + 1] = add2(v[2 * k + 1], f2(f.z, f.w));
-                  }
-                } else {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) {
-                    if (2 * j < cols) v[j].x += rp[2 * j];
-                    if (2 * j + 1 < cols) v[j].y += rp[2 * j + 1];
-                  }
-                }
+              for (int k = 0; k < 8; ++k) {
+                const float4 f =
+                    *reinterpret_cast<const float4*>(chunk_at(box, 128, lane, k));
+                v[2 * k] = add2(v[2 * k], f2(f.x, f.y));
+                v[2 * k + 1] = add2(v[2 * k + 1], f2(f.z, f.w));
               }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              put_y(k, reinterpret_cast<const F2(&)[4]>(v[4 * k]));
           } else {
-            uint4 s[4];
+            F2 x[16];
             if (a.q) {
-              if (p.tma_q) {
-                s[0] = *reinterpret_cast<const uint4*>(qrow + (((2 * h) ^ swz64) << 4));
-                s[1] = *reinterpret_cast<const uint4*>(qrow + (((2 * h + 1) ^ swz64) << 4));
-              } else {
-                load_row8(a.q + m * a.ldq + n0, n_ok, reinterpret_cast<uint4(&)[2]>(s));
+              const float step = ckpt8_step(h ? sb[1] : sb[0]);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint4 q = *reinterpret_cast<const uint4*>(chunk_at(qbox, 64, lane, 2 * h + k));
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t f = ckpt8_flip(w[e]);
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+                    x[8 * k + 2 * e + j] =
+                        mul2(add2(f2(ckpt8_biased(f, 2 * j), ckpt8_biased(f, 2 * j + 1)),
+                                  f2(-kCkptBias)),
+                             f2(step));
+                }
               }
-            } else if (a.u_in) {
-              saved16(s);
+              // this unit's values are in registers: bring the next unit's
+              if (end) request(last_unit ? locate(u + workers, 0) : locate(u, c + 64));
+            } else if (in16) {
+              get16(x);
             } else {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) s[k] = make_uint4(0, 0, 0, 0);
+              for (int j = 0; j < 16; ++j) x[j] = f2(0.f);
             }
-            const uint32_t* sw = reinterpret_cast<const uint32_t*>(s);
-            const float step = a.q ? ckpt8_step(h ? sb[1] : sb[0]) : 0.f;
-            if (h == 1 || cols <= 32) {
-              // this unit's 8-bit input is in registers: bring the next one
-              if (a.q) request(last_unit ? locate(u + workers, 0) : locate(u, c + 64));
-            }
+            // v <- v f'(x), x <- f(x)
             with_act(a.act, [&](auto tag) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                F2 f[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  F2 uv;
-                  if (a.q) {
-                    const uint32_t w = ckpt8_flip(sw[2 * k + j / 2]);
-                    uv = mul2(add2(f2(ckpt8_biased(w, 2 * (j & 1)),
-                                      ckpt8_biased(w, 2 * (j & 1) + 1)),
-                                   f2(-kCkptBias)),
-                              f2(step));
-                  } else {
-                    uv = unpack2<H16>(sw[4 * k + j]);
-                  }
-                  v[4 * k + j] = mul2(
-                      v[4 * k + j], act_grad2<decltype(tag)::value>(uv, a.slope, f[j]));
-                }
-                if (a.u_out) put_u(k, f);
-                put_y(k, reinterpret_cast<const F2(&)[4]>(v[4 * k]));
+              for (int j = 0; j < 16; ++j) {
+                F2 f;
+                v[j] = mul2(v[j], act_grad2<decltype(tag)::value>(x[j], a.slope, f));
+                x[j] = f;
               }
             });
+            if (a.u_out) put_u(x);
           }
-          const bool end = h == 1;  // whole units have both pieces
-          if (y32 || u32 || (end && (y64 || (!BWD && a.q && q64)))) {
+
+          // the output into its box, and out
+          if (a.out_f32) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<float4*>(chunk_at(box, 128, lane, k)) =
+                  make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
+          } else {
+            pack_row<H16>(box, y_bytes, lane, p.y64 ? 4 * h : 0, v);
+          }
+          const bool flush_y = end || !p.y64, flush_q = !BWD && a.q && end;
+          const bool by_tma_y = flush_y && p.tma_y && whole;
+          const bool by_tma_q = flush_q && p.tma_q && whole;
+          const bool by_tma_u = a.u_out && p.tma_u && whole;
+          if (by_tma_y || by_tma_q || by_tma_u) {
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               // rows past T are clipped by the stores
-              if (y64 && end) ptx::tma_store_2d(&maps.y, box, t.n0, t.row0);
-              if (y32) ptx::tma_store_2d(&maps.y, box, n0, t.row0);
-              if (u32) ptx::tma_store_2d(&maps.u, box + kBox / 2, n0, t.row0);
-              if (!BWD && a.q && q64 && end) ptx::tma_store_2d(&maps.q, qbox, t.n0, t.row0);
+              if (by_tma_y) ptx::tma_store_2d(&maps.y, box, p.y64 ? t.n0 : n0, t.row0);
+              if (by_tma_u) ptx::tma_store_2d(&maps.u, box + kBox / 2, n0, t.row0);
+              if (by_tma_q) ptx::tma_store_2d(&maps.q, qbox, t.n0, t.row0);
               ptx::bulk_commit_group();
             }
             stores = true;
           }
+          if (flush_y && !by_tma_y)
+            warp_copy<true>(box, y_bytes, p.y64 ? y_mem : y_mem + (long long)(32 * h) * esz,
+                            a.ldy * esz, rows,
+                            (p.y64 ? min(64, a.N - t.n0) : cols) * esz, esz, lane);
+          if (flush_q && !by_tma_q)
+            warp_copy<true>(qbox, 64, reinterpret_cast<uint8_t*>(a.q) + t.row0 * a.ldq + t.n0,
+                            a.ldq, rows, min(64, a.N - t.n0), 1, lane);
           if constexpr (BWD) {
             if (a.colpart) {
               if (!row_ok) {
@@ -936,28 +913,23 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
   if (!(bwd ? map16(&maps.b, a.w, a.K, a.N, a.ldw, BK, pl.tile == kNarrow ? 64 : 128)
             : map16(&maps.b, a.w, a.N, a.K, a.ldw, 64, BK)))
     return MLP_ERR_CUDA;
-  // What the epilogue reads and writes goes through staging boxes where rows
-  // start on 16 bytes and the output is large (for small ones the staging
-  // round trip is latency): a row per thread straight to memory touches 32
-  // lines an instruction (65,536 x 512 -> 1,536: 70 us for a residual, 42 us
-  // for the 8-bit values).
-  if (pl.splits == 1 && a.T * a.N >= (1ll << 20)) {
+  // What the epilogue reads and writes moves by TMA where rows start on 16
+  // bytes.  (A row per thread straight between registers and memory touches 32
+  // lines an instruction: 65,536 x 512 -> 1,536 took 70 us more for a residual
+  // that way, 42 us for the 8-bit values.)
+  if (pl.splits == 1) {
     auto rows16 = [](const void* ptr, long long ld, int esz) {
       return ptr && aligned16(ptr) && ld * esz % 16 == 0;
     };
     const int esz = a.out_f32 ? 4 : 2;
+    p.y64 = !a.out_f32 && !a.u_out;
     if (rows16(a.y, a.ldy, esz)) {
-      if (!a.out_f32 && !a.u_out) {
-        if (!map16(&maps.y, a.y, a.N, a.T, a.ldy, 64, 32)) return MLP_ERR_CUDA;
-        p.y64 = 1;
-      } else {
-        if (!encode_tmap_out_2d(&maps.y, a.y, a.out_f32, a.N, a.T,
-                                (unsigned long long)a.ldy * esz, 32, 32))
-          return MLP_ERR_CUDA;
-        p.tma_y = 1;
-      }
+      if (!(p.y64 ? map16(&maps.y, a.y, a.N, a.T, a.ldy, 64, 32)
+                  : encode_tmap_out_2d(&maps.y, a.y, a.out_f32, a.N, a.T,
+                                       (unsigned long long)a.ldy * esz, 32, 32)))
+        return MLP_ERR_CUDA;
+      p.tma_y = 1;
     }
-    // (an fp32 box takes the place of the second one)
     if (!a.out_f32 && rows16(a.u_out, a.ldu_out, 2)) {
       if (!encode_tmap_out_2d(&maps.u, a.u_out, 0, a.N, a.T, (unsigned long long)a.ldu_out * 2, 32,
                               32))
