@@ -45,6 +45,7 @@ constexpr int kBox = 4096, kWarpStage = kBox + 2048;
 struct LinParams {
   LinearArgs a;
   int tiles_m, tiles_n, units, k_blocks, kb_per_split;
+  unsigned magic;  // of tile_of
   int a_bytes;  // of a stage's x tile: fewer than 128 rows when there are fewer
   int y64;  // y / du in boxes of 64 columns (16-bit, no u_out), else of 32
   // What moves by TMA: y / du; u_out; the 16-bit residual / u (into the y64 box,
@@ -79,14 +80,22 @@ struct LinLayout {
 };
 
 // Eight tile rows at a time sweep all tile columns, so that CTAs that run
-// together share row and column blocks in L2.
-__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
-  constexpr int G = 8;
-  const int first = t / (G * tiles_n) * G;
-  const int gm = min(tiles_m - first, G);
-  const int r = t - first * tiles_n;
-  tm = first + r % gm;
-  tn = r / gm;
+// together share row and column blocks in L2.  Every warp does this for every
+// tile, so the division by the tiles of a group is a multiplication (`magic` =
+// ceil(2^32 / (8 tiles_n)): the quotient or one more) and full groups shift.
+__device__ __forceinline__ void tile_of(const LinParams& p, int t, int& tm, int& tn) {
+  const int per = 8 * p.tiles_n;
+  int group = (int)__umulhi((unsigned)t, p.magic);
+  if (group * per > t) --group;
+  const int first = group * 8, r = t - group * per;
+  const int gm = min(p.tiles_m - first, 8);
+  if (gm == 8) {
+    tm = first + (r & 7);
+    tn = r >> 3;
+  } else {
+    tm = first + r % gm;
+    tn = r / gm;
+  }
 }
 
 // ------------------------------------------------------------ epilogue pieces
@@ -149,12 +158,12 @@ __device__ __forceinline__ void warp_copy(uint8_t* box, int row_bytes, uint8_t* 
   __syncwarp();
 }
 
-// A piece's 32 values into this lane's row of a 16-bit box (from chunk `c0`).
-template <int H16>
+// Values into this lane's row of a 16-bit box, from chunk `c0`.
+template <int H16, int PAIRS>
 __device__ __forceinline__ void pack_row(uint8_t* box, int row_bytes, int lane, int c0,
-                                         const F2 (&v)[16]) {
+                                         const F2 (&v)[PAIRS]) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < PAIRS / 4; ++k)
     *reinterpret_cast<uint4*>(chunk_at(box, row_bytes, lane, c0 + k)) =
         make_uint4(pack16x2<H16>(v[4 * k].x, v[4 * k].y),
                    pack16x2<H16>(v[4 * k + 1].x, v[4 * k + 1].y),
@@ -193,12 +202,17 @@ __device__ __forceinline__ float column_sums(F2 (&p)[16], int lane) {
 
 // ------------------------------------------------------------ the kernel
 
-template <int PAIR, int BN, int STAGES, int EW, int AROWS, int H16, int BWD>
+// MODE: forward, backward from 16-bit (or no) pre-activations, backward from
+// 8-bit ones.
+enum { kFwd, kBwd, kBwdCkpt };
+
+template <int PAIR, int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
 __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams& p) {
   using L = LinLayout<PAIR, BN, STAGES, EW, AROWS>;
   static_assert(AROWS == 128 || (STAGES * L::B_BYTES >= 16384 && !PAIR), "reads past the x ring");
   constexpr int ACC = L::ACC;
   constexpr int TILE_M = PAIR ? 256 : 128, TILE_N = ACC;
+  constexpr bool BWD = MODE != kFwd, CK = MODE == kBwdCkpt;
   constexpr bool B_MN = !BWD;  // W [K][N] is an N-major operand, W [N][K] a K-major one
   const LinearArgs& a = p.a;
   extern __shared__ uint8_t smem_raw[];
@@ -216,8 +230,10 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(in_full + EW);
   volatile int* s_abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? ptx::cluster_ctarank() : 0u;
+  // warp-uniform to the compiler, which then keeps what follows from it in
+  // uniform registers
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? blockIdx.x & 1u : 0u;  // in the cluster of two
   const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   const int workers = PAIR ? gridDim.x >> 1 : gridDim.x;
 
@@ -268,7 +284,7 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
       uint32_t phase = 0;
       for (int u = worker; u < p.units && !*s_abort; u += workers) {
         int tm, tn, kb0, kb1;
-        tile_of(u / a.splits, p.tiles_m, p.tiles_n, tm, tn);
+        tile_of(p, a.splits == 1 ? u : u / a.splits, tm, tn);
         k_range(u, kb0, kb1);
         const int m0 = tm * TILE_M + (int)rank * 128;
         const int n0 = tn * TILE_N + (int)rank * L::B_COLS;
@@ -393,13 +409,13 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
 
     // One unit is 64 columns of the warp's 32 rows; units go tile by tile.
     struct Unit {
-      int u, c, row0, n0;
+      int row0, n0;
     };
     auto locate = [&](int u, int c) {
-      Unit t{u, c, 0, a.N};
+      Unit t{0, a.N};
       if (u < p.units) {
         int tm, tn;
-        tile_of(u / a.splits, p.tiles_m, p.tiles_n, tm, tn);
+        tile_of(p, a.splits == 1 ? u : u / a.splits, tm, tn);
         t.row0 = tm * TILE_M + (int)rank * 128 + quarter * 32;
         t.n0 = tn * TILE_N + c_first + c;
       }
@@ -416,9 +432,9 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
     // Requests what the epilogue of a unit reads by TMA.
     auto request = [&](const Unit& t) {
       if (!exists(t)) return;
-      if constexpr (BWD) {
+      if constexpr (CK) {
         const long long m = (long long)t.row0 + lane;
-        if (a.q && m < a.T) {
+        if (m < a.T) {
 #pragma unroll
           for (int g = 0; g < 2; ++g)
             sb[g] = t.n0 + 32 * g < a.N ? a.scale[m * a.lds + t.n0 / kCkptGroup + g] : 0u;
@@ -432,7 +448,7 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
           in_flight = true;
         }
       }
-      if (p.tma_in) {
+      if (!CK && p.tma_in) {
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(&in_full[ew], kBox);
@@ -456,17 +472,20 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
       }
     };
 
-    if (a.splits == 1 && !p.tma_in) request(locate(worker, 0));
+    Unit next = locate(worker, 0);
+    if (CK && a.splits == 1) request(next);
     for (int u = worker; u < p.units; u += workers) {
       if (*s_abort) break;
       bool ready = false;
       for (int c = 0; c < L::SPAN; c += 64) {
-        const Unit t = locate(u, c);
+        const Unit t = next;
+        const bool last_unit = c + 64 >= L::SPAN;
+        next = last_unit ? locate(u + workers, 0) : locate(u, c + 64);
         const long long m = (long long)t.row0 + lane;
         const bool row_ok = m < a.T;
         // the 8-bit input is requested a unit ahead; one that lands in the
         // output's box once that has been read by its store
-        if (p.tma_in) {
+        if (!CK && p.tma_in) {
           boxes_free();
           request(t);
         }
@@ -478,10 +497,9 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
           if (!ready) break;
           ptx::tc_fence_after();
         }
-        const bool last_unit = c + 64 >= L::SPAN;
         const bool real = exists(t);  // warp-uniform
         if (real && a.splits == 1) {
-          if (!p.tma_in) boxes_free();
+          if (CK || !p.tma_in) boxes_free();
           if (in_flight) {
             if (!ptx::mbar_wait_bounded(&in_full[ew], in_phase, p.wait_ns, p.err,
                                         DEVERR_TIMEOUT_EPILOGUE)) {
@@ -499,16 +517,16 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
         const int esz = a.out_f32 ? 4 : 2;
         const int y_bytes = p.y64 || a.out_f32 ? 128 : 64;  // of a box row
         // the 16-bit input: residual (forward) or u (backward)
-        const uint8_t* in16 = reinterpret_cast<const uint8_t*>(BWD ? a.u_in : a.out_f32 ? nullptr : a.res);
+        const uint8_t* in16 = reinterpret_cast<const uint8_t*>(
+            CK ? nullptr : BWD ? a.u_in : a.out_f32 ? nullptr : a.res);
         const long long ld_in = (BWD ? a.ldu_in : a.ldr) * 2;
-        uint8_t* y_mem = static_cast<uint8_t*>(a.y) + ((long long)t.row0 * a.ldy + t.n0) * esz;
         if (real && a.splits == 1) {
           const int cols = min(64, a.N - t.n0);
           if (in16 && p.y64 && !p.tma_in)
             warp_copy<false>(box, 128,
                              const_cast<uint8_t*>(in16) + t.row0 * ld_in + (long long)t.n0 * 2,
                              ld_in, rows, cols * 2, 2, lane);
-          if (BWD && a.q && !p.tma_q)
+          if (CK && !p.tma_q)
             warp_copy<false>(qbox, 64, reinterpret_cast<uint8_t*>(a.q) + t.row0 * a.ldq + t.n0,
                              a.ldq, rows, cols, 1, lane);
         }
@@ -576,31 +594,20 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
           if (h == 1 && !p.y64) boxes_free();
           // u / a leaves through the second box; beside an fp32 output, whose
           // box is the whole space, at once and through the same space
-          auto put_u = [&](const F2(&x)[16]) {
-            uint8_t* ub = a.out_f32 ? box : box + kBox / 2;
-            pack_row<H16>(ub, 64, lane, 0, x);
+          uint8_t* u_box = a.out_f32 ? box : box + kBox / 2;
+          auto copy_u = [&] {
             if (!(p.tma_u && whole))
-              warp_copy<true>(ub, 64,
+              warp_copy<true>(u_box, 64,
                               static_cast<uint8_t*>(a.u_out) +
                                   ((long long)t.row0 * a.ldu_out + n0) * 2,
                               a.ldu_out * 2, rows, cols * 2, 2, lane);
           };
-          // this piece of the 16-bit input, from the box
-          auto get16 = [&](F2(&x)[16]) {
+          // the 16-bit input's piece into the box, where the unit did not bring it
+          auto stage16 = [&] {
             if (!p.y64)
               warp_copy<false>(box, 64,
                                const_cast<uint8_t*>(in16) + t.row0 * ld_in + (long long)n0 * 2,
                                ld_in, rows, cols * 2, 2, lane);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint4 q = *reinterpret_cast<const uint4*>(
-                  chunk_at(box, p.y64 ? 128 : 64, lane, (p.y64 ? 4 * h : 0) + k));
-              x[4 * k] = unpack2<H16>(q.x);
-              x[4 * k + 1] = unpack2<H16>(q.y);
-              x[4 * k + 2] = unpack2<H16>(q.z);
-              x[4 * k + 3] = unpack2<H16>(q.w);
-            }
-            __syncwarp();
           };
 
           if constexpr (!BWD) {
@@ -613,17 +620,27 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
               *reinterpret_cast<uint4*>(chunk_at(qbox, 64, lane, 2 * h + 1)) =
                   make_uint4(w[4], w[5], w[6], w[7]);
             }
-            if (a.u_out) put_u(v);
+            if (a.u_out) {
+              pack_row<H16>(u_box, 64, lane, 0, v);
+              copy_u();
+            }
             with_act(a.act, [&](auto tag) {
 #pragma unroll
               for (int j = 0; j < 16; ++j)
                 v[j] = act_value2<decltype(tag)::value>(v[j], a.slope);
             });
             if (in16) {
-              F2 x[16];
-              get16(x);
+              stage16();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] = add2(v[j], x[j]);
+              for (int k = 0; k < 4; ++k) {
+                const uint4 q = *reinterpret_cast<const uint4*>(
+                    chunk_at(box, p.y64 ? 128 : 64, lane, (p.y64 ? 4 * h : 0) + k));
+                v[4 * k] = add2(v[4 * k], unpack2<H16>(q.x));
+                v[4 * k + 1] = add2(v[4 * k + 1], unpack2<H16>(q.y));
+                v[4 * k + 2] = add2(v[4 * k + 2], unpack2<H16>(q.z));
+                v[4 * k + 3] = add2(v[4 * k + 3], unpack2<H16>(q.w));
+              }
+              __syncwarp();
             } else if (a.res) {
               warp_copy<false>(box, 128,
                                static_cast<uint8_t*>(const_cast<void*>(a.res)) +
@@ -638,42 +655,65 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
               }
             }
           } else {
-            F2 x[16];
-            if (a.q) {
-              const float step = ckpt8_step(h ? sb[1] : sb[0]);
+            // the saved values of this piece, raw (decoded half a piece at a
+            // time below, which keeps the registers within the launch's limit)
+            uint32_t raw[CK ? 8 : 16];
+            auto take = [&](int k, const uint4& q) {
+              raw[4 * k] = q.x;
+              raw[4 * k + 1] = q.y;
+              raw[4 * k + 2] = q.z;
+              raw[4 * k + 3] = q.w;
+            };
+            float step = 0.f;
+            if constexpr (CK) {
+              step = ckpt8_step(h ? sb[1] : sb[0]);
 #pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint4 q = *reinterpret_cast<const uint4*>(chunk_at(qbox, 64, lane, 2 * h + k));
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const uint32_t f = ckpt8_flip(w[e]);
-#pragma unroll
-                  for (int j = 0; j < 2; ++j)
-                    x[8 * k + 2 * e + j] =
-                        mul2(add2(f2(ckpt8_biased(f, 2 * j), ckpt8_biased(f, 2 * j + 1)),
-                                  f2(-kCkptBias)),
-                             f2(step));
-                }
-              }
+              for (int k = 0; k < 2; ++k)
+                take(k, *reinterpret_cast<const uint4*>(chunk_at(qbox, 64, lane, 2 * h + k)));
               // this unit's values are in registers: bring the next unit's
-              if (end) request(last_unit ? locate(u + workers, 0) : locate(u, c + 64));
+              if (end) request(next);
             } else if (in16) {
-              get16(x);
+              stage16();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                take(k, *reinterpret_cast<const uint4*>(
+                            chunk_at(box, p.y64 ? 128 : 64, lane, (p.y64 ? 4 * h : 0) + k)));
+              __syncwarp();
             } else {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) x[j] = f2(0.f);
+              for (int k = 0; k < 16; ++k) raw[k] = 0u;
             }
-            // v <- v f'(x), x <- f(x)
+            // v <- v f'(u), f(u) into its box
             with_act(a.act, [&](auto tag) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                F2 f;
-                v[j] = mul2(v[j], act_grad2<decltype(tag)::value>(x[j], a.slope, f));
-                x[j] = f;
+              for (int g = 0; g < 2; ++g) {
+                F2 x[8];
+                if constexpr (CK) {
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const uint32_t f = ckpt8_flip(raw[4 * g + e]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                      x[2 * e + j] = mul2(
+                          add2(f2(ckpt8_biased(f, 2 * j), ckpt8_biased(f, 2 * j + 1)),
+                               f2(-kCkptBias)),
+                          f2(step));
+                  }
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) x[j] = unpack2<H16>(raw[8 * g + j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  F2 f;
+                  v[8 * g + j] = mul2(v[8 * g + j],
+                                      act_grad2<decltype(tag)::value>(x[j], a.slope, f));
+                  x[j] = f;
+                }
+                if (a.u_out) pack_row<H16>(u_box, 64, lane, 2 * g, x);
               }
             });
-            if (a.u_out) put_u(x);
+            if (a.u_out) copy_u();
           }
 
           // the output into its box, and out
@@ -702,9 +742,11 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
             stores = true;
           }
           if (flush_y && !by_tma_y)
-            warp_copy<true>(box, y_bytes, p.y64 ? y_mem : y_mem + (long long)(32 * h) * esz,
-                            a.ldy * esz, rows,
-                            (p.y64 ? min(64, a.N - t.n0) : cols) * esz, esz, lane);
+            warp_copy<true>(box, y_bytes,
+                            static_cast<uint8_t*>(a.y) +
+                                ((long long)t.row0 * a.ldy + (p.y64 ? t.n0 : n0)) * esz,
+                            a.ldy * esz, rows, (p.y64 ? min(64, a.N - t.n0) : cols) * esz, esz,
+                            lane);
           if (flush_q && !by_tma_q)
             warp_copy<true>(qbox, 64, reinterpret_cast<uint8_t*>(a.q) + t.row0 * a.ldq + t.n0,
                             a.ldq, rows, min(64, a.N - t.n0), 1, lane);
@@ -722,8 +764,7 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
         }
         // (a unit that does not exist in this tile has none to wait for, but
         // the next one may)
-        if (BWD && a.q && !real && a.splits == 1)
-          request(last_unit ? locate(u + workers, 0) : locate(u, c + 64));
+        if (CK && !real && a.splits == 1) request(next);
       }
       if (!ready) {
         *s_abort = 1;
@@ -761,17 +802,17 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
   }
 }
 
-template <int STAGES, int EW, int H16, int BWD>
+template <int STAGES, int EW, int H16, int MODE>
 __global__ void __cluster_dims__(2, 1, 1)
     __launch_bounds__(LinLayout<1, 256, STAGES, EW>::THREADS, 1)
     linear_pair_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinParams p) {
-  linear_body<1, 256, STAGES, EW, 128, H16, BWD>(maps, p);
+  linear_body<1, 256, STAGES, EW, 128, H16, MODE>(maps, p);
 }
 
-template <int BN, int STAGES, int EW, int AROWS, int H16, int BWD>
+template <int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
 __global__ void __launch_bounds__(LinLayout<0, BN, STAGES, EW, AROWS>::THREADS, 1)
     linear_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinParams p) {
-  linear_body<0, BN, STAGES, EW, AROWS, H16, BWD>(maps, p);
+  linear_body<0, BN, STAGES, EW, AROWS, H16, MODE>(maps, p);
 }
 
 // ------------------------------------------------------------ plan and launch
@@ -814,23 +855,23 @@ LinPlan linear_plan(long long T, int K, int N) {
   return pl;
 }
 
-template <int BN, int STAGES, int EW, int AROWS, int H16, int BWD>
+template <int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
 mlp_status launch_single(const LinMaps& maps, const LinParams& p, cudaStream_t st) {
   using L = LinLayout<0, BN, STAGES, EW, AROWS>;
-  auto kernel = linear_kernel<BN, STAGES, EW, AROWS, H16, BWD>;
+  auto kernel = linear_kernel<BN, STAGES, EW, AROWS, H16, MODE>;
   static const cudaError_t configured =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
   if (configured != cudaSuccess) return MLP_ERR_CUDA;
   const int grid = p.units < num_sms() ? p.units : num_sms();
-  LaunchScope ls(BWD ? "linear_bwd" : "linear_fwd", st, p.a.T, p.a.N, p.a.K);
+  LaunchScope ls(MODE != kFwd ? "linear_bwd" : "linear_fwd", st, p.a.T, p.a.N, p.a.K);
   launch_k(kernel, dim3(grid), dim3(L::THREADS), L::SMEM, st, maps, p);
   return launch_status();
 }
 
-template <int STAGES, int EW, int H16, int BWD>
+template <int STAGES, int EW, int H16, int MODE>
 mlp_status launch_pair(const LinMaps& maps, const LinParams& p, cudaStream_t st) {
   using L = LinLayout<1, 256, STAGES, EW>;
-  auto kernel = linear_pair_kernel<STAGES, EW, H16, BWD>;
+  auto kernel = linear_pair_kernel<STAGES, EW, H16, MODE>;
   // pairs that fit at once (a GPC with an odd number of free SMs leaves one over)
   static const int max_pairs = [&] {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
@@ -849,7 +890,7 @@ mlp_status launch_pair(const LinMaps& maps, const LinParams& p, cudaStream_t st)
   }();
   if (max_pairs < 1) return MLP_ERR_CUDA;
   const int pairs = p.units < max_pairs ? p.units : max_pairs;
-  LaunchScope ls(BWD ? "linear_bwd_pair" : "linear_fwd_pair", st, p.a.T, p.a.N, p.a.K);
+  LaunchScope ls(MODE != kFwd ? "linear_bwd_pair" : "linear_fwd_pair", st, p.a.T, p.a.N, p.a.K);
   launch_k(kernel, dim3(2 * pairs), dim3(L::THREADS), L::SMEM, st, maps, p);
   return launch_status();
 }
@@ -860,18 +901,18 @@ mlp_status launch_pair(const LinMaps& maps, const LinParams& p, cudaStream_t st)
 // long K eight warps leave room for a fifth stage.
 constexpr int kShortK = 16;  // k-blocks
 
-template <int H16, int BWD>
+template <int H16, int MODE>
 mlp_status launch_tile(const LinMaps& maps, const LinParams& p, Tile tile, cudaStream_t st) {
   switch (tile) {
     case kPair:
-      return p.k_blocks <= kShortK ? launch_pair<4, 16, H16, BWD>(maps, p, st)
-                                   : launch_pair<5, 8, H16, BWD>(maps, p, st);
-    case kWide: return launch_single<128, 5, 8, 128, H16, BWD>(maps, p, st);
+      return p.k_blocks <= kShortK ? launch_pair<4, 16, H16, MODE>(maps, p, st)
+                                   : launch_pair<5, 8, H16, MODE>(maps, p, st);
+    case kWide: return launch_single<128, 5, 8, 128, H16, MODE>(maps, p, st);
     default:
       // few rows stream W: the ring's depth sets the rate (16 rows x 8,192 x
       // 8,192: 42 us with seven stages of 24 KiB)
-      return p.a.T <= 32 ? launch_single<64, 15, 4, 32, H16, BWD>(maps, p, st)
-                         : launch_single<64, 7, 4, 128, H16, BWD>(maps, p, st);
+      return p.a.T <= 32 ? launch_single<64, 15, 4, 32, H16, MODE>(maps, p, st)
+                         : launch_single<64, 7, 4, 128, H16, MODE>(maps, p, st);
   }
 }
 
@@ -891,6 +932,7 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
   p.tiles_m = (int)tm;
   p.tiles_n = (int)tn;
   p.units = (int)(tm * tn * pl.splits);
+  p.magic = (unsigned)(((1ull << 32) + 8 * tn - 1) / (8 * tn));
   p.k_blocks = (a.K + BK - 1) / BK;
   p.kb_per_split = pl.kb_per_split;
   p.wait_ns = wait_limit_ns();
@@ -948,8 +990,14 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
     }
   }
   const bool h16 = a.dtype == MLP_DTYPE_F16;
-  if (bwd) return h16 ? launch_tile<1, 1>(maps, p, pl.tile, st) : launch_tile<0, 1>(maps, p, pl.tile, st);
-  return h16 ? launch_tile<1, 0>(maps, p, pl.tile, st) : launch_tile<0, 0>(maps, p, pl.tile, st);
+  if (!bwd)
+    return h16 ? launch_tile<1, kFwd>(maps, p, pl.tile, st)
+               : launch_tile<0, kFwd>(maps, p, pl.tile, st);
+  if (a.q)
+    return h16 ? launch_tile<1, kBwdCkpt>(maps, p, pl.tile, st)
+               : launch_tile<0, kBwdCkpt>(maps, p, pl.tile, st);
+  return h16 ? launch_tile<1, kBwd>(maps, p, pl.tile, st)
+             : launch_tile<0, kBwd>(maps, p, pl.tile, st);
 }
 
 }  // namespace mlp
