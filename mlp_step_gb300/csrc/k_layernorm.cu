@@ -57,12 +57,13 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* part, int slot, 
 #pragma unroll
       for (int i = 0; i < NV; ++i) part[i * WPR + warp_in_row] = v[i];
     row_barrier<WPR>(slot);
+    // one load and log2(WPR) exchanges (a load per partial, in every thread,
+    // was two loads per value of a row of 8,192)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float s = part[i * WPR];
+      v[i] = part[i * WPR + (threadIdx.x & (WPR - 1))];
 #pragma unroll
-      for (int w = 1; w < WPR; ++w) s += part[i * WPR + w];
-      v[i] = s;
+      for (int o = WPR / 2; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
   }
 }
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
     }
     s[0] = s2.x + s2.y;
     row_sums<WPR>(s, part[1][slot], slot, t >> 5);
-    const float rho = 1.f / sqrtf(s[0] * inv_d + p.eps);
+    const float rho = rsqrtf(s[0] * inv_d + p.eps);  // two ulp
     if (t == 0) {
       if (p.mean) p.mean[row] = mu;
       if (p.rstd) p.rstd[row] = rho;
@@ -222,7 +223,7 @@ __global__ void __launch_bounds__(kLoopThreads) ln_fwd_wide_kernel(const LayerNo
       }
     }
     row_sums<WPR>(s, part[1], 0, t >> 5);
-    const float rho = 1.f / sqrtf(s[0] * inv_d + p.eps);
+    const float rho = rsqrtf(s[0] * inv_d + p.eps);  // two ulp
     if (t == 0) {
       if (p.mean) p.mean[row] = mu;
       if (p.rstd) p.rstd[row] = rho;

@@ -175,12 +175,16 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
   const long long m0 = rb * kPartRows;
   const int rows = (int)min((long long)kPartRows, a.T - m0);
   const bool has_u = CK || a.u_in != nullptr;
-  const T* dy = static_cast<const T*>(a.x) + m0 * a.ldx + c;
-  const T* u = static_cast<const T*>(a.u_in) + m0 * a.ldu_in + c;
-  const int8_t* q = a.q + m0 * a.ldq + c;
-  const uint8_t* sc = a.scale + m0 * a.lds + c / kCkptGroup;
-  T* du = static_cast<T*>(a.y) + m0 * a.ldy + c;
-  T* ao = static_cast<T*>(a.u_out) + m0 * a.ldu_out + c;
+  // pitches are ints at the C boundary: products with a row number are one
+  // widening multiplication
+  const int ldx = (int)a.ldx, ldu = (int)a.ldu_in, ldq = (int)a.ldq, lds = (int)a.lds;
+  const int ldy = (int)a.ldy, ldo = (int)a.ldu_out;
+  const T* dy = static_cast<const T*>(a.x) + m0 * ldx + c;
+  const T* u = static_cast<const T*>(a.u_in) + m0 * ldu + c;
+  const int8_t* q = a.q + m0 * ldq + c;
+  const uint8_t* sc = a.scale + m0 * lds + c / kCkptGroup;
+  T* du = static_cast<T*>(a.y) + m0 * ldy + c;
+  T* ao = static_cast<T*>(a.u_out) + m0 * ldo + c;
   float g[R][V], x[R][V];
   float sum[V];
 #pragma unroll
@@ -190,10 +194,10 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
     for (int k = 0; k < R; ++k) {
       const int r = r0 + k;
       const bool in = r < rows;
-      load_cols<T, V>(dy + (long long)r * a.ldx, in, n, g[k]);
+      load_cols<T, V>(dy + (long long)r * ldx, in, n, g[k]);
       if constexpr (CK) {
-        const float step = in && n > 0 ? ckpt8_step(sc[(long long)r * a.lds]) : 0.f;
-        const int8_t* p = q + (long long)r * a.ldq;
+        const float step = in && n > 0 ? ckpt8_step(sc[(long long)r * lds]) : 0.f;
+        const int8_t* p = q + (long long)r * ldq;
         if (V == 4 && in && n >= V) {
           const uint32_t w = ckpt8_flip(*reinterpret_cast<const uint32_t*>(p));
 #pragma unroll
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
           for (int j = 0; j < V; ++j) x[k][j] = in && j < n ? (float)p[j] * step : 0.f;
         }
       } else if (has_u) {
-        load_cols<T, V>(u + (long long)r * a.ldu_in, in, n, x[k]);
+        load_cols<T, V>(u + (long long)r * ldu, in, n, x[k]);
       }
     }
   };
@@ -229,8 +233,8 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
           gc[k][j] *= act_grad_of<sizeof(T) == 4, ACT>(xc[k][j], a.slope, f[j]);
           sum[j] += gc[k][j];
         }
-        store_cols<T, V>(du + (long long)(r0 + k) * a.ldy, n, gc[k]);
-        if (a.u_out) store_cols<T, V>(ao + (long long)(r0 + k) * a.ldu_out, n, f);
+        store_cols<T, V>(du + (long long)(r0 + k) * ldy, n, gc[k]);
+        if (a.u_out) store_cols<T, V>(ao + (long long)(r0 + k) * ldo, n, f);
       }
     }
   });
