@@ -453,6 +453,21 @@ mlp_status mlp_layernorm_bwd(const void* dy, int dtype, int lddy, const void* x,
                              float* dgain, float* dshift, void* workspace, size_t ws_bytes,
                              void* stream);
 
+/* mlp_stack_train_step with the block outputs that a later block's backward
+ * reads kept as 8-bit checkpoints: half the memory per kept activation (11
+ * blocks over 262,144 tokens: 1.5 GB and one bf16 buffer less instead of 3 GB)
+ * for one encoding and one decoding pass per block.  The forward pass and the
+ * loss are those of mlp_stack_train_step bit for bit; blocks after the first
+ * take their weight and input gradients at the 8-bit input (with the exact
+ * forward's rstd). */
+size_t mlp_stack_ckpt8_workspace_bytes(int n_blocks, int T, int d, int hidden);
+mlp_status mlp_stack_train_step_ckpt8(int n_blocks, int T, int d, int hidden, float eps,
+                                      float slope, const void* x0, const void* target,
+                                      float* params, float* velocity, float* grads,
+                                      void* params_bf16, float lr, float momentum,
+                                      float* loss_out, void* workspace, size_t ws_bytes,
+                                      void* stream);
+
 /* ---------------------------------------------------------------- linear layer
  * u = x W + bias;  y = f(u) + residual, in one product whose epilogue keeps
  * everything fp32 up to the one rounding of each output.

@@ -104,6 +104,9 @@ SIGNATURES = {
     "mlp_ckpt8_scale_cols": (_i, [_i]),
     "mlp_ckpt8_encode": (_i, [_vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp]),
     "mlp_ckpt8_decode": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _i, _i, _vp]),
+    "mlp_stack_ckpt8_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "mlp_stack_train_step_ckpt8": (_i, [_i, _i, _i, _i, _f, _f, _vp, _vp, _vp, _vp, _vp, _vp, _f,
+                                        _f, _vp, _vp, _sz, _vp]),
     "mlp_layernorm_fwd": (_i, [_vp, _i, _i, _vp, _vp, _i, _i, _f, _vp, _i, _vp, _vp, _vp, _i,
                                _vp, _i, _vp]),
     "mlp_layernorm_workspace_bytes": (_sz, [_i, _i]),
@@ -444,6 +447,22 @@ def mlp_stack_train_step(n_blocks, T, d, hidden, x0, target, params, velocity, g
                                        _ptr(params_bf16), lr, momentum, _ptr(loss_out),
                                        _ptr(workspace), wsb, _stream(stream)),
            "mlp_stack_train_step")
+
+
+def mlp_stack_ckpt8_workspace_bytes(n_blocks: int, T: int, d: int, hidden: int) -> int:
+    return load().mlp_stack_ckpt8_workspace_bytes(n_blocks, T, d, hidden)
+
+
+def mlp_stack_train_step_ckpt8(n_blocks, T, d, hidden, x0, target, params, velocity, grads,
+                               params_bf16, lr, momentum, loss_out, workspace, eps=1e-6,
+                               slope=0.5, stream=None):
+    """mlp_stack_train_step with the kept block outputs in 8 bits."""
+    wsb = workspace.numel() * workspace.element_size()
+    _check(load().mlp_stack_train_step_ckpt8(n_blocks, T, d, hidden, eps, slope, _ptr(x0),
+                                             _ptr(target), _ptr(params), _ptr(velocity),
+                                             _ptr(grads), _ptr(params_bf16), lr, momentum,
+                                             _ptr(loss_out), _ptr(workspace), wsb,
+                                             _stream(stream)), "mlp_stack_train_step_ckpt8")
 
 
 # ------------------------------------------------------------------ feed-forward operators

@@ -117,70 +117,86 @@ size_t mlp_stack_param_count(int n_blocks, int d, int hidden) {
 
 namespace {
 struct StackWs {
-  size_t xs, rstd, dy, dx, blk, mse, loss, total;
+  size_t xs, scale, rstd, dy, dx, xin, blk, mse, loss, total;
 };
-StackWs stack_ws(int n_blocks, int T, int d, int hidden) {
+// ckpt8: the block outputs that a later block's backward reads are kept in 8
+// bits (xs, with their scale bytes), and one of them at a time is expanded
+// into xin; otherwise xs holds every block output in bf16.
+StackWs stack_ws(int n_blocks, int T, int d, int hidden, bool ckpt8) {
   StackWs w;
-  w.xs = align256((size_t)n_blocks * T * d * 2);
+  const size_t td = (size_t)T * d;
+  w.xs = align256(ckpt8 ? (n_blocks - 1) * td : n_blocks * td * 2);
+  w.scale = ckpt8 ? align256((n_blocks - 1) * (size_t)T * mlp_ckpt8_scale_cols(d)) : 0;
   w.rstd = align256((size_t)n_blocks * T * 4);
-  w.dy = align256((size_t)T * d * 2);
+  w.dy = align256(td * 2);
   w.dx = w.dy;
+  w.xin = ckpt8 ? w.dy : 0;
   w.blk = align256(block_ws(T, d, hidden).total);
   w.mse = align256(mse_ws_bytes((long long)T * d));
   w.loss = 256;
-  w.total = w.xs + w.rstd + w.dy + w.dx + w.blk + w.mse + w.loss;
+  w.total = w.xs + w.scale + w.rstd + w.dy + w.dx + w.xin + w.blk + w.mse + w.loss;
   return w;
 }
-}  // namespace
 
-size_t mlp_stack_workspace_bytes(int n_blocks, int T, int d, int hidden) {
-  if (n_blocks <= 0 || !block_shape_ok(T, d, hidden)) return 0;
-  return stack_ws(n_blocks, T, d, hidden).total;
-}
-
-mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float eps, float slope,
-                                const void* x0, const void* target, float* params,
-                                float* velocity, float* grads, void* params_bf16, float lr,
-                                float momentum, float* loss_out, void* workspace,
-                                size_t ws_bytes, void* stream) {
-  NvtxRange nvtx_range("mlp_stack_train_step");
+mlp_status stack_train_step(int n_blocks, int T, int d, int hidden, float eps, float slope,
+                            const void* x0, const void* target, float* params, float* velocity,
+                            float* grads, void* params_bf16, float lr, float momentum,
+                            float* loss_out, void* workspace, size_t ws_bytes, bool ckpt8,
+                            cudaStream_t st) {
   if (n_blocks <= 0 || T < 0) return MLP_ERR_INVALID_ARG;
   if (!block_shape_ok(T, d, hidden)) return MLP_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return MLP_OK;
   if (!x0 || !target || !params || !velocity || !grads || !params_bf16 || !workspace)
     return MLP_ERR_INVALID_ARG;
-  const StackWs w = stack_ws(n_blocks, T, d, hidden);
+  const StackWs w = stack_ws(n_blocks, T, d, hidden, ckpt8);
   if (ws_bytes < w.total) return MLP_ERR_INVALID_ARG;
   if (!aligned16(x0) || !aligned16(target) || !aligned16(params) || !aligned16(velocity) ||
       !aligned16(grads) || !aligned16(params_bf16) || !aligned16(workspace) ||
       (loss_out && !aligned16(loss_out)))
     return MLP_ERR_MISALIGNED;
-  cudaStream_t st = S(stream);
-  uint8_t* base = static_cast<uint8_t*>(workspace);
-  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(base);
-  float* rstd = reinterpret_cast<float*>(base + w.xs);
-  void* dy = base + w.xs + w.rstd;
-  void* dx = base + w.xs + w.rstd + w.dy;
-  void* blk = base + w.xs + w.rstd + w.dy + w.dx;
-  void* mse = base + w.xs + w.rstd + w.dy + w.dx + w.blk;
-  float* loss = loss_out ? loss_out
-                         : reinterpret_cast<float*>(base + w.xs + w.rstd + w.dy + w.dx + w.blk +
-                                                    w.mse);
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  auto carve = [&](size_t bytes) {
+    uint8_t* at = p;
+    p += bytes;
+    return at;
+  };
+  uint8_t* xs = carve(w.xs);
+  uint8_t* scale = carve(w.scale);
+  float* rstd = reinterpret_cast<float*>(carve(w.rstd));
+  void* dy = carve(w.dy);
+  void* dx = carve(w.dx);
+  void* xin = carve(w.xin);
+  void* blk = carve(w.blk);
+  void* mse = carve(w.mse);
+  float* loss = loss_out ? loss_out : reinterpret_cast<float*>(carve(w.loss));
   const size_t per = (size_t)2 * d * hidden;
   const size_t td = (size_t)T * d;
+  const int groups = mlp_ckpt8_scale_cols(d);
   const __nv_bfloat16* wb = static_cast<const __nv_bfloat16*>(params_bf16);
-  // forward, saving every block input and rstd
+  // forward, keeping every block's output and rstd; with 8-bit checkpoints the
+  // outputs themselves take turns in the buffers that the backward uses later
   const void* cur = x0;
   for (int l = 0; l < n_blocks; ++l) {
+    void* out = ckpt8 ? (l & 1 ? xin : dx) : xs + l * td * 2;
     MLP_CHECK(launch_block_fwd(cur, wb + l * per, wb + l * per + (size_t)d * hidden, T, hidden,
-                               eps, slope, xs + l * td, rstd + (size_t)l * T, st));
-    cur = xs + l * td;
+                               eps, slope, out, rstd + (size_t)l * T, st));
+    if (ckpt8 && l + 1 < n_blocks)
+      MLP_CHECK(launch_ckpt8_encode(out, MLP_DTYPE_BF16, T, d, d,
+                                    reinterpret_cast<int8_t*>(xs + l * td), d,
+                                    scale + (size_t)l * T * groups, groups, st));
+    cur = out;
   }
   MLP_CHECK(launch_mse(cur, target, (long long)td, loss, dy, mse, st));
   for (int l = n_blocks - 1; l >= 0; --l) {
-    const void* xin = l == 0 ? x0 : (const void*)(xs + (l - 1) * td);
+    const void* in = l == 0 ? x0 : (const void*)(xs + (l - 1) * td * 2);
+    if (ckpt8 && l > 0) {
+      MLP_CHECK(launch_ckpt8_decode(reinterpret_cast<const int8_t*>(xs + (l - 1) * td), d,
+                                    scale + (size_t)(l - 1) * T * groups, groups, T, d, xin,
+                                    MLP_DTYPE_BF16, d, st));
+      in = xin;
+    }
     // the first block's input gradient is not an output of the step
-    MLP_CHECK(block_bwd_impl(xin, rstd + (size_t)l * T, wb + l * per,
+    MLP_CHECK(block_bwd_impl(in, rstd + (size_t)l * T, wb + l * per,
                              wb + l * per + (size_t)d * hidden, dy, T, d, hidden, slope,
                              l == 0 ? nullptr : dx, grads + l * per,
                              grads + l * per + (size_t)d * hidden, blk, st));
@@ -196,6 +212,40 @@ mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float ep
   segs.cols_pad[0] = 1;
   return launch_sgd(params, grads, velocity, params_bf16, MLP_DTYPE_BF16,
                     (long long)(per * n_blocks), lr, momentum, segs, st);
+}
+}  // namespace
+
+size_t mlp_stack_workspace_bytes(int n_blocks, int T, int d, int hidden) {
+  if (n_blocks <= 0 || !block_shape_ok(T, d, hidden)) return 0;
+  return stack_ws(n_blocks, T, d, hidden, false).total;
+}
+
+mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float eps, float slope,
+                                const void* x0, const void* target, float* params,
+                                float* velocity, float* grads, void* params_bf16, float lr,
+                                float momentum, float* loss_out, void* workspace,
+                                size_t ws_bytes, void* stream) {
+  NvtxRange nvtx_range("mlp_stack_train_step");
+  return stack_train_step(n_blocks, T, d, hidden, eps, slope, x0, target, params, velocity, grads,
+                          params_bf16, lr, momentum, loss_out, workspace, ws_bytes, false,
+                          S(stream));
+}
+
+size_t mlp_stack_ckpt8_workspace_bytes(int n_blocks, int T, int d, int hidden) {
+  if (n_blocks <= 0 || !block_shape_ok(T, d, hidden)) return 0;
+  return stack_ws(n_blocks, T, d, hidden, true).total;
+}
+
+mlp_status mlp_stack_train_step_ckpt8(int n_blocks, int T, int d, int hidden, float eps,
+                                      float slope, const void* x0, const void* target,
+                                      float* params, float* velocity, float* grads,
+                                      void* params_bf16, float lr, float momentum,
+                                      float* loss_out, void* workspace, size_t ws_bytes,
+                                      void* stream) {
+  NvtxRange nvtx_range("mlp_stack_train_step_ckpt8");
+  return stack_train_step(n_blocks, T, d, hidden, eps, slope, x0, target, params, velocity, grads,
+                          params_bf16, lr, momentum, loss_out, workspace, ws_bytes, true,
+                          S(stream));
 }
 
 mlp_status mlp_attn_prep_fwd(const void* x, const void* w_qkv, const float* q_gain, int T,

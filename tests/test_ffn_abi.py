@@ -129,6 +129,24 @@ def test_linear(lib):
         assert act(**{k: ODD}) == ALIGN, k
 
 
+def test_stack_with_8bit_checkpoints(lib):
+    f = ctypes.c_float
+    st = [P, P, P, P, P, P, f(0.02), f(0.95), P, P]
+    need = M.mlp_stack_ckpt8_workspace_bytes(3, 8, 512, 1536)
+    call = lambda n, T, h, ws, a=st: lib.mlp_stack_train_step_ckpt8(n, T, 512, h, f(1e-6), f(0.5),
+                                                                    *a, ws, None)
+    assert need > 0 and M.mlp_stack_ckpt8_workspace_bytes(3, 8, 512, 1000) == 0
+    assert call(0, 8, 1536, need) == BAD and call(3, -1, 1536, need) == BAD
+    assert call(3, 8, 1536, need - 1) == BAD and call(3, 8, 1000, need) == SHAPE
+    assert call(3, 0, 1536, 0) == OK
+    assert call(3, 8, 1536, need, [ODD] + st[1:]) == ALIGN
+    # the kept activations halve (and their scales: 1/32)
+    full = M.mlp_stack_workspace_bytes(11, 262144, 512, 1536)
+    small = M.mlp_stack_ckpt8_workspace_bytes(11, 262144, 512, 1536)
+    td = 262144 * 512
+    assert full - small == 11 * td * 2 - 10 * (td + td // 32) - td * 2
+
+
 def test_binding_refuses_what_the_library_cannot_read():
     """Host tensors, other shapes and types never reach a kernel."""
     x = torch.zeros(4, 64)

@@ -409,6 +409,59 @@ def test_linear_forward(T, k, n, dtype):
             assert (q.buf == -77).all() and (s.buf == 211).all()
 
 
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,k,n", [(3, 512, 200), (40, 4096, 200), (300, 520, 1001),
+                                   (1500, 328, 1200), (4100, 200, 776), (3300, 1160, 1100)])
+def test_linear_mixed_outputs(T, k, n, dtype, odd):
+    """fp32 outputs beside 16-bit and 8-bit ones, all at once, in matrices whose
+    rows TMA can address and in ones that it cannot."""
+    pitch = n + 3 if odd else None
+    x, w = rnd(100, T, k, dtype), rnd(101, k, n, dtype, std=k ** -0.5)
+    wt = w.t().contiguous()
+    if n % 8:
+        wt = rnd(102, n, k, dtype)
+        wt.copy_(w.t())
+    bias, r = vec(103, n), rnd(104, T, n, F32, pitch=pitch)
+    ru = x.double() @ w.double() + bias.double()
+    eu = (k + 8) * 2 * U24 * (x.double().abs() @ w.double().abs()) + 2 * U24 * ru.abs()
+    f, df, _ = act_ref(ru, "silu")
+    for odt in (F32, dtype):
+        y, u, (q, s) = Guarded(T, n, odt, pitch), Guarded(T, n, dtype, pitch), new_ckpt(T, n, pitch)
+        res = r if odt == F32 else rnd(104, T, n, dtype, pitch=pitch)
+        ws = torch.empty(M.mlp_linear_workspace_bytes(T, k, n, dtype), dtype=torch.uint8,
+                         device="cuda")
+        M.mlp_linear_fwd(x, w, y.v, bias=bias, act=M.MLP_ACT_SILU, residual=res, u=u.v,
+                         ckpt=(q.v, s.v), workspace=ws)
+        ref = f + res.double()
+        near(y.v, ref, rounding(odt, ref) + (df.abs() + 0.1) * eu + ACT_ERR * (1 + ru.abs()),
+             "y")
+        near(u.v, ru, rounding(dtype, ru) + eu, "u")
+        step = (s.v.to(torch.int64) - 133 + 1023).bitwise_left_shift(52).view(torch.float64)
+        near(ckpt_values(q.v, s.v), ru,
+             step.repeat_interleave(32, 1)[:, :n] * torch.where(q.v.abs() == 127, 1.0, 0.5) + eu,
+             "8-bit u")
+        assert y.intact() and u.intact() and q.intact() and s.intact()
+        # backward: dy = x, so that da = x w
+        da = x.double() @ w.double()
+        uin = rnd(105, T, n, dtype, std=1.5, pitch=pitch)
+        M.mlp_ckpt8_encode(uin, q.v, s.v)
+        bws = torch.empty(M.mlp_linear_bwd_workspace_bytes(T, n, k, dtype), dtype=torch.uint8,
+                          device="cuda")
+        for kw, seen in (({"u": uin}, uin.double()),
+                         ({"ckpt": (q.v, s.v)}, ckpt_values(q.v, s.v))):
+            du, a = Guarded(T, n, odt, pitch), Guarded(T, n, dtype, pitch)
+            db = torch.empty(n, device="cuda")
+            M.mlp_linear_bwd(x, wt, du.v, act=M.MLP_ACT_GELU, dbias=db, a=a.v, workspace=bws, **kw)
+            fg, dfg, _ = act_ref(seen, "gelu")
+            rdu = da * dfg
+            e = eu * dfg.abs() + (da.abs() + eu) * ACT_ERR * (1 + seen.abs()) + 2 * U24 * rdu.abs()
+            near(du.v, rdu, rounding(odt, rdu) + e, "du")
+            near(a.v, fg, rounding(dtype, fg) + ACT_ERR * (1 + seen.abs()) * (1 + fg.abs()), "a")
+            near(db, rdu.sum(0), e.sum(0) + (T + 8) * U24 * rdu.abs().sum(0), "dbias")
+            assert du.intact() and a.intact()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("T,k,n", [(4, 512, 200), (64, 2048, 96), (300, 520, 1001),
                                    (4100, 200, 768)])
@@ -613,6 +666,7 @@ def test_feed_forward_block(T, d, h, dtype, ck):
     # at least half, 0.08 for the chain through u.
     tol = 5 * half(dtype) + (0.13 if ck else 0)
     for k, r in ref.items():
+        r = r.detach()
         t = 3 * half(dtype) if k == "y" else tol
         err = float((o[k].double() - r).norm() / r.norm())
         assert err <= t, (k, err, t)
@@ -642,6 +696,94 @@ def test_feed_forward_block_captured():
     feed_forward(x, P, True, ws, o)
     for k, v in keep.items():
         assert torch.equal(v, o[k]), k
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    T, k, n = 64, 4096, 256
+    jobs = []
+    for i in range(2):
+        x, w, dy = rnd(110 + i, T, k, BF16), rnd(112 + i, k, n, BF16, k ** -0.5), rnd(114 + i, T, n,
+                                                                                      BF16)
+        ws = torch.empty(max(M.mlp_linear_workspace_bytes(T, k, n, BF16),
+                             M.mlp_layernorm_workspace_bytes(T, n)), dtype=torch.uint8,
+                         device="cuda")
+        o = [torch.empty(T, n, dtype=BF16, device="cuda") for _ in range(3)]
+        f = [torch.empty(z, device="cuda") for z in (T, T, n, n)]
+        jobs.append((x, w, dy, ws, o, f, torch.cuda.Stream()))
+
+    def one(x, w, dy, ws, o, f, stream):
+        M.mlp_linear_fwd(x, w, o[0], act=M.MLP_ACT_GELU, workspace=ws, stream=stream)
+        M.mlp_layernorm_fwd(o[0], o[1], mean=f[0], rstd=f[1], stream=stream)
+        M.mlp_layernorm_bwd(dy, f[0], f[1], o[2], f[2], f[3], ws, x=o[0], stream=stream)
+
+    ref = []
+    for j in jobs:
+        one(*j)
+        torch.cuda.synchronize()
+        ref.append([t.clone() for t in j[4] + j[5]])
+    for _ in range(20):
+        for j in jobs:
+            one(*j)
+    torch.cuda.synchronize()
+    for j, r in zip(jobs, ref):
+        for a, b in zip(j[4] + j[5], r):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n_blocks,T", [(1, 200), (2, 300), (3, 1000), (4, 257)])
+def test_stack_with_8bit_checkpoints(n_blocks, T):
+    """The step equals, bit for bit, the public block calls with every kept
+    block output passed through an 8-bit checkpoint; its loss equals the step's
+    without checkpoints."""
+    d, h, lr, mom = 512, 512, 0.02, 0.9
+    per = 2 * d * h
+    x0, tgt = rnd(90, T, d, BF16).contiguous(), rnd(91, T, d, BF16).contiguous()
+    p0 = (0.02 * vec(92, n_blocks * per, std=1.0)).to(BF16)
+
+    def buffers():
+        p = p0.float()
+        return p, torch.zeros_like(p), torch.zeros_like(p), p0.clone(), torch.zeros(4, device="cuda")
+
+    P, V, G, W, L = buffers()
+    ws = torch.empty(M.mlp_stack_ckpt8_workspace_bytes(n_blocks, T, d, h), dtype=torch.uint8,
+                     device="cuda")
+    M.mlp_stack_train_step_ckpt8(n_blocks, T, d, h, x0, tgt, P, V, G, W, lr, mom, L, ws)
+    P1, V1, G1, W1, L1 = buffers()
+    ws1 = torch.empty(M.mlp_stack_workspace_bytes(n_blocks, T, d, h), dtype=torch.uint8,
+                      device="cuda")
+    M.mlp_stack_train_step(n_blocks, T, d, h, x0, tgt, P1, V1, G1, W1, lr, mom, L1, ws1)
+    assert torch.equal(L[0], L1[0])
+
+    wg = lambda l: p0[l * per:l * per + d * h].view(d, h)  # noqa: E731
+    wd = lambda l: p0[l * per + d * h:(l + 1) * per].view(h, d)  # noqa: E731
+    xs, rs = [x0], []
+    for l in range(n_blocks):
+        y, r = torch.empty_like(x0), torch.empty(T, device="cuda")
+        M.mlp_block_fwd(xs[-1], wg(l), wd(l), y, r)
+        xs.append(y)
+        rs.append(r)
+    dy, loss = torch.empty_like(x0), torch.zeros(4, device="cuda")
+    M.mse_loss_fwd_bwd(xs[-1], tgt, loss, dy,
+                       torch.empty(M.mse_workspace_bytes(T * d), dtype=torch.uint8, device="cuda"))
+    bws = torch.empty(M.mlp_block_workspace_bytes(T, d, h), dtype=torch.uint8, device="cuda")
+    for l in reversed(range(n_blocks)):
+        x = xs[l]
+        if l:
+            x = ckpt_values(*ckpt_ref(x)).to(BF16)
+        dx, dg, dd = torch.empty_like(x0), torch.empty(d, h, device="cuda"), torch.empty(
+            h, d, device="cuda")
+        M.mlp_block_bwd(x, rs[l], wg(l), wd(l), dy, dx, dg, dd, bws)
+        assert torch.equal(G[l * per:l * per + d * h].view(d, h), dg), l
+        assert torch.equal(G[l * per + d * h:(l + 1) * per].view(h, d), dd), l
+        dy = dx
+    # and the gradients are those of the exact inputs up to the inputs' 8-bit
+    # error: at most 1/128 of a group's largest magnitude, sqrt(32)/128 = 0.045
+    # of its norm, in each of the two factors that depend on the input
+    if n_blocks > 1:
+        assert float((G - G1).norm() / G1.norm()) < 0.09
+    else:
+        assert torch.equal(G, G1)
 
 
 def test_offsets_past_32_bits():
