@@ -398,6 +398,19 @@ mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float ep
                                 float momentum, float* loss_out, void* workspace,
                                 size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- feed-forward operators
+ * Layer norm, linear layers with activation and residual, and 8-bit activation
+ * checkpoints.  The conventions at the top hold; further:
+ *   - outputs do not overlap inputs, but where a call says so;
+ *   - T == 0 (or no columns) writes nothing, except that gradients which are
+ *     sums over the rows are set to zero;
+ *   - sums over rows run in a fixed order without atomics, so results are the
+ *     same in every run; MLP_ORDER_LINEAR does not apply here;
+ *   - calls that take a workspace write it before they read it; calls that may
+ *     overlap on the GPU (other streams, graphs in flight together) need
+ *     workspaces of their own.
+ */
+
 /* ---------------------------------------------------------------- 8-bit checkpoints
  * Saved activations in 33/32 byte per value.  32 consecutive values of a row
  * (the last group of a row may be shorter) share one scale byte b; the stored
@@ -440,11 +453,8 @@ mlp_status mlp_layernorm_fwd(const void* x, int dtype, int ldx, const float* gai
  * The forward's input is given either as it was (x) or as its 8-bit
  * checkpoint (x_q, x_scale; x NULL), with the forward's mean and rstd either
  * way.  dres (nullable, [T][ldr]) is the gradient that reaches x past the
- * norm (the residual branch); dx may be dres itself.  Column sums run in a
- * fixed order without atomics: results are the same in every run.  T == 0
- * sets dgain and dshift to zero.  workspace: mlp_layernorm_workspace_bytes,
- * written before it is read; calls that may overlap on the GPU (other
- * streams, graphs in flight together) need workspaces of their own. */
+ * norm (the residual branch); dx may be dres itself.
+ * workspace: mlp_layernorm_workspace_bytes(T, d) bytes. */
 size_t mlp_layernorm_workspace_bytes(int T, int d);
 mlp_status mlp_layernorm_bwd(const void* dy, int dtype, int lddy, const void* x, int ldx,
                              const int8_t* x_q, int ldq, const uint8_t* x_scale, int lds,
@@ -479,8 +489,11 @@ mlp_status mlp_stack_train_step_ckpt8(int n_blocks, int T, int d, int hidden, fl
  * operand type) and / or u_q and u_scale (both or neither: an 8-bit
  * checkpoint of the unrounded u).
  * Pitches of x and W in 16-bit types are multiples of 8.  d_in >= 1.
- * workspace: mlp_linear_workspace_bytes(...) bytes (0 for most shapes; NULL is
- * then fine), with the same rule on overlapping calls as above.
+ * workspace: mlp_linear_workspace_bytes(...) bytes (0 for most 16-bit shapes;
+ * NULL is then fine).
+ * The tensor cores' fp32 accumulation truncates: sums are low by about 1e-9 of
+ * their size per unit of d_in (1e-5 at d_in = 8,192), below the rounding of
+ * 16-bit outputs.
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
 size_t mlp_linear_workspace_bytes(int T, int d_in, int d_out, int dtype);
 mlp_status mlp_linear_fwd(const void* x, int ldx, const void* w, int ldw, int T, int d_in,
@@ -499,8 +512,8 @@ mlp_status mlp_linear_fwd(const void* x, int ldx, const void* w, int ldw, int T,
  *   a_out = f(u)         (nullable, the operand type: the left operand of this
  *                         layer's weight gradient, dW = a^T dy, mlp_gemm).
  * u is given in the operand type (u) or as an 8-bit checkpoint (u_q, u_scale;
- * u NULL); with act NONE and no a_out it may be missing.  T == 0 sets dbias to
- * zero.  Pitches of dy and W in 16-bit types are multiples of 8. */
+ * u NULL); with act NONE and no a_out it may be missing.  Pitches of dy and W
+ * in 16-bit types are multiples of 8. */
 size_t mlp_linear_bwd_workspace_bytes(int T, int d_in, int d_out, int dtype);
 mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int T, int d_in,
                           int d_out, int dtype, int act, float slope, const void* u, int ldu,

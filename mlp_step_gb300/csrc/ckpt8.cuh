@@ -33,10 +33,10 @@ __device__ __forceinline__ float ckpt8_step(uint32_t b) {
   return __uint_as_float(b == kCkptNanByte ? 0x7fffffffu : (b - 6u) << 23);
 }
 
-// The larger of a running maximum of magnitudes and |x|; a NaN is kept.
-__device__ __forceinline__ float amax_step(float amax, float x) {
+// The largest of a running maximum of magnitudes, |x| and |y|; a NaN is kept.
+__device__ __forceinline__ float amax_step(float amax, float x, float y) {
   float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(amax), "f"(fabsf(x)));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(amax), "f"(fabsf(x)), "f"(fabsf(y)));
   return r;
 }
 
@@ -76,16 +76,16 @@ __device__ __forceinline__ uint32_t ckpt8_piece(const float (&v)[N], uint32_t am
     const float step = ckpt8_step(b);
 #pragma unroll
     for (int k = 0; k < N / 4; ++k)
-      w[k] = b == kCkptNanByte
-                 ? 0u
-                 : ckpt8_pack4(ckpt8_hold(v[4 * k], step), ckpt8_hold(v[4 * k + 1], step),
-                               ckpt8_hold(v[4 * k + 2], step), ckpt8_hold(v[4 * k + 3], step), inv);
+      w[k] = ckpt8_pack4(ckpt8_hold(v[4 * k], step), ckpt8_hold(v[4 * k + 1], step),
+                         ckpt8_hold(v[4 * k + 2], step), ckpt8_hold(v[4 * k + 3], step), inv);
   } else {
 #pragma unroll
     for (int k = 0; k < N / 4; ++k)
-      w[k] = b == kCkptNanByte
-                 ? 0u
-                 : ckpt8_pack4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+      w[k] = ckpt8_pack4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3], inv);
+  }
+  if (b == kCkptNanByte) {
+#pragma unroll
+    for (int k = 0; k < N / 4; ++k) w[k] = 0u;
   }
   return b;
 }
@@ -94,7 +94,7 @@ template <int N>
 __device__ __forceinline__ uint32_t amax_bits_of(const float (&v)[N]) {
   float m = 0.f;
 #pragma unroll
-  for (int j = 0; j < N; ++j) m = amax_step(m, v[j]);
+  for (int j = 0; j < N; j += 2) m = amax_step(m, v[j], v[j + 1]);
   return __float_as_uint(m) & 0x7fffffffu;
 }
 

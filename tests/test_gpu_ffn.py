@@ -698,6 +698,32 @@ def test_feed_forward_block_captured():
         assert torch.equal(v, o[k]), k
 
 
+@pytest.mark.parametrize("T", [1, 5, 8, 9, 100])
+@pytest.mark.parametrize("k,n", [(1, 1), (63, 65), (300, 129), (1030, 1500)])
+def test_linear_f32_odd_pitches(T, k, n):
+    """fp32 operands at any pitch, few and many rows."""
+    x, w = rnd(120, T, k, F32, pitch=k + 1), rnd(121, k, n, F32, std=k ** -0.5, pitch=n + 3)
+    wt = rnd(122, n, k, F32, pitch=k + 5)
+    wt.copy_(w.t())
+    y, du = Guarded(T, n, F32, n + 1), Guarded(T, n, F32, n + 2)
+    ws = torch.empty(max(M.mlp_linear_workspace_bytes(T, k, n, F32),
+                         M.mlp_linear_bwd_workspace_bytes(T, n, k, F32)), dtype=torch.uint8,
+                     device="cuda")
+    u = rnd(123, T, n, F32, std=1.5, pitch=n + 1)
+    db = torch.empty(n, device="cuda")
+    M.mlp_linear_fwd(x, w, y.v, act=M.MLP_ACT_GELU, workspace=ws)
+    M.mlp_linear_bwd(x, wt, du.v, act=M.MLP_ACT_GELU, u=u, dbias=db, workspace=ws)
+    ru = x.double() @ w.double()
+    e = (k + 8) * 2 * U24 * (x.double().abs() @ w.double().abs())
+    f, df, _ = act_ref(ru, "gelu")
+    near(y.v, f, (df.abs() + 0.1) * e + ACT_ERR * (1 + ru.abs()), "y")
+    rdu = ru * act_ref(u.double(), "gelu")[1]
+    e = 1.2 * e + (ru.abs() + e) * ACT_ERR * (1 + u.double().abs()) + 2 * U24 * rdu.abs()
+    near(du.v, rdu, e, "du")
+    near(db, rdu.sum(0), e.sum(0) + (T + 8) * U24 * rdu.abs().sum(0), "dbias")
+    assert y.intact() and du.intact()
+
+
 def test_two_streams_at_once():
     """Calls that overlap on two streams, each with a workspace of its own."""
     T, k, n = 64, 4096, 256
