@@ -155,7 +155,7 @@ struct LinearPath {
 
 LinearPath linear_path(long long T, int K, int N, int dtype, bool bwd) {
   LinearPath p{};
-  p.few = linear_takes_few(T, K, N, dtype);
+  p.few = linear_takes_few(T, K, N, dtype, bwd);
   if (p.few) return p;
   p.splits = 1;
   if (dtype != MLP_DTYPE_F32) {

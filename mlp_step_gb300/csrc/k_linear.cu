@@ -11,10 +11,10 @@
 // largest magnitude needs no exchange between threads.
 //
 // Tiles: CTA pairs (cta_group::2) on 256 x 256 tiles where there are enough
-// of them to fill the GPU, single CTAs on 128 x 128 or 128 x 64 tiles
+// of them to fill the GPU, single CTAs on 128 rows x 64 to 256 columns
 // otherwise, with the contraction split over CTAs when even those are few
 // (raw sums to a workspace, finished by launch_linear_finish).  Warps: TMA
-// producer, MMA issuer, eight or sixteen epilogue warps (a tensor-memory lane
+// producer, MMA issuer, four to sixteen epilogue warps (a tensor-memory lane
 // quarter and a share of the columns each); two accumulators, so that the
 // epilogue of one tile overlaps the MMAs of the next.  W is read as it is stored: [K][N] as an
 // N-major operand, [N][K] (backward) as a K-major one.
@@ -817,42 +817,48 @@ __global__ void __launch_bounds__(LinLayout<0, BN, STAGES, EW, AROWS>::THREADS, 
 
 // ------------------------------------------------------------ plan and launch
 
-enum Tile { kPair, kWide, kNarrow };  // 256 x 256 pairs, 128 x 128, 128 x 64
+// Output tiles: 256 x 256 of a CTA pair, or 128 rows of one CTA.
+enum Tile { kPair, kTall, kWide, kNarrow };
+constexpr int kTileN[] = {256, 256, 128, 64};
 
 struct LinPlan {
   Tile tile;
   int splits, kb_per_split;
 };
 
-// From the shape alone, so that workspace sizes do not depend on the device.
-// Pairs when their tiles fill most of ~76 pairs; otherwise single CTAs, 128
-// wide when that gives ~100 tiles, else 64 wide; and when those are fewer than
-// half of ~152 SMs and K is long, K is split over CTAs, at least four 64-deep
-// blocks each.
+// From the shape alone (so that workspace sizes do not depend on the device).
+// Pairs when their tiles fill most of ~76 pairs.  Otherwise the single-CTA tile
+// and the split of K with the smallest estimated time: rounds of units over
+// ~152 CTAs, each as long as its MMAs or its epilogue.  A 64-deep block takes
+// about 512 cycles of a CTA's MMAs whatever the tile's width (measured: 500 in
+// 128 x 64 tiles), so wide tiles win as soon as they are enough to go round,
+// and splitting K makes them enough for few rows (16 rows x 8,192 x 8,192: 42
+// us in 128 x 64 tiles, 31 in 128 x 256 with K in two).  A split costs the
+// second launch and the raw sums' way through memory.
 LinPlan linear_plan(long long T, int K, int N) {
-  LinPlan pl;
   const int kb = (K + BK - 1) / BK;
-  const long long pair = ((T + 255) / 256) * ((N + 255) / 256);
-  const long long wide = ((T + 127) / 128) * ((N + 127) / 128);
-  const long long narrow = ((T + 127) / 128) * ((N + 63) / 64);
-  int s = 1;
-  if (pair >= 48 && N > 128 && T > 128) {
-    pl.tile = kPair;
-  } else if (wide >= 100 && N > 64) {
-    pl.tile = kWide;
-  } else {
-    pl.tile = kNarrow;
-    if (narrow < 76) {
-      s = (int)(152 / narrow);
-      if (s > 16) s = 16;
-      if (s > kb / 4) s = kb / 4;
-      if (s < 1) s = 1;
+  if (T > 128 && N > 128 && (T + 255) / 256 * ((N + 255) / 256) >= 48) return {kPair, 1, kb};
+  LinPlan best{};
+  double best_cycles = 1e300;
+  for (int tile = kTall; tile <= kNarrow; ++tile) {
+    if (tile != kNarrow && N <= kTileN[tile] / 2) continue;
+    const long long tiles = (T + 127) / 128 * ((N + kTileN[tile] - 1) / kTileN[tile]);
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && (s > kb / 2 || tiles * s > 304)) break;
+      const int per = (kb + s - 1) / s, splits = (kb + per - 1) / per;
+      const double rounds = (double)((tiles * splits + 151) / 152);
+      const double epilogue = tile == kTall ? (splits > 1 ? 8000 : 12000) : 4000;
+      const double mma = per * 512., read = (double)K * N * 2 / 3500;  // W at ~6.8 TB/s
+      double cycles = rounds * (mma > epilogue ? mma : epilogue);
+      cycles = (cycles > read ? cycles : read) + epilogue;
+      if (splits > 1) cycles += 5000 + splits * (double)T * N * 8 / 1750;  // at half that
+      if (cycles < best_cycles) {
+        best_cycles = cycles;
+        best = {(Tile)tile, splits, per};
+      }
     }
   }
-  const int per = (kb + s - 1) / s;
-  pl.splits = (kb + per - 1) / per;
-  pl.kb_per_split = per;
-  return pl;
+  return best;
 }
 
 template <int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
@@ -907,12 +913,11 @@ mlp_status launch_tile(const LinMaps& maps, const LinParams& p, Tile tile, cudaS
     case kPair:
       return p.k_blocks <= kShortK ? launch_pair<4, 16, H16, MODE>(maps, p, st)
                                    : launch_pair<5, 8, H16, MODE>(maps, p, st);
+    case kTall:
+      return p.a_bytes <= 32 * BK * 2 ? launch_single<256, 5, 4, 32, H16, MODE>(maps, p, st)
+                                      : launch_single<256, 4, 4, 128, H16, MODE>(maps, p, st);
     case kWide: return launch_single<128, 5, 8, 128, H16, MODE>(maps, p, st);
-    default:
-      // few rows stream W: the ring's depth sets the rate (16 rows x 8,192 x
-      // 8,192: 42 us with seven stages of 24 KiB)
-      return p.a.T <= 32 ? launch_single<64, 15, 4, 32, H16, MODE>(maps, p, st)
-                         : launch_single<64, 7, 4, 128, H16, MODE>(maps, p, st);
+    default: return launch_single<64, 7, 4, 128, H16, MODE>(maps, p, st);
   }
 }
 
@@ -923,7 +928,7 @@ int linear_tc_splits(long long T, int K, int N) { return linear_plan(T, K, N).sp
 mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
   const LinPlan pl = linear_plan(a.T, a.K, a.N);
   const int tile_m = pl.tile == kPair ? 256 : 128;
-  const int tile_n = pl.tile == kPair ? 256 : pl.tile == kWide ? 128 : 64;
+  const int tile_n = kTileN[pl.tile];
   const long long tm = (a.T + tile_m - 1) / tile_m, tn = (a.N + tile_n - 1) / tile_n;
   if (tm * tn * pl.splits > (1ll << 30)) return MLP_ERR_UNSUPPORTED_SHAPE;
   LinParams p{};
@@ -947,12 +952,11 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st) {
                                box_rows);
   };
   // A single-CTA tile of few rows loads just those (in eights): the stale rows
-  // behind them only feed accumulator rows that are never stored, and boxes of
-  // mostly fill are slow to deliver (16 rows x 8,192 x 8,192: 43 us with them).
+  // behind them only feed accumulator rows that are never stored.
   const int a_rows = pl.tile != kPair && a.T < 128 ? (int)(a.T + 7) / 8 * 8 : 128;
   p.a_bytes = a_rows * BK * 2;
   if (!map16(&maps.a, a.x, a.K, a.T, a.ldx, BK, a_rows)) return MLP_ERR_CUDA;
-  if (!(bwd ? map16(&maps.b, a.w, a.K, a.N, a.ldw, BK, pl.tile == kNarrow ? 64 : 128)
+  if (!(bwd ? map16(&maps.b, a.w, a.K, a.N, a.ldw, BK, pl.tile == kPair ? 128 : tile_n)
             : map16(&maps.b, a.w, a.N, a.K, a.ldw, 64, BK)))
     return MLP_ERR_CUDA;
   // What the epilogue reads and writes moves by TMA where rows start on 16

@@ -92,13 +92,26 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
       float v[kRowsAhead], extra[kRowsAhead];
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
-        const bool in = ok && m0 + k < m_end;
         v[k] = 0.f;
-        if (in) {
-          const float* p = a.partial + (m0 + k) * a.ldp + c;
-          for (int s = 0; s < a.splits; ++s) v[k] += __ldcs(p + (long long)s * a.T * a.ldp);
-        }
-        extra[k] = epi_load<T, BWD>(a, m0 + k, c, in);
+        extra[k] = epi_load<T, BWD>(a, m0 + k, c, ok && m0 + k < m_end);
+      }
+      // planes in order, four of all rows at a time in flight
+      const float* p = a.partial + m0 * a.ldp + c;
+      const long long plane = a.T * a.ldp;
+#pragma unroll 1
+      for (int s = 0; s < a.splits; s += 4) {
+        float q[kRowsAhead][4];
+#pragma unroll
+        for (int k = 0; k < kRowsAhead; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            q[k][j] = ok && m0 + k < m_end && s + j < a.splits
+                          ? __ldcs(p + (s + j) * plane + k * a.ldp)
+                          : 0.f;
+#pragma unroll
+        for (int k = 0; k < kRowsAhead; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[k] += q[k][j];
       }
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
@@ -611,12 +624,15 @@ mlp_status act_t(const LinearArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Up to 8 rows for fp32 (whose tiled kernel computes 64 rows whatever T is);
-// in 16 bits the tensor cores take over once the products' FMAs, not the reading
-// of W, bound this kernel.
-bool linear_takes_few(long long T, int K, int N, int dtype) {
+// Up to 8 rows for fp32 (whose tiled kernel computes 64 rows whatever T is).
+// In 16 bits the tensor cores take over once the FMAs, not the reading of W,
+// bound this kernel: above 2 rows of a large W (8,192 x 8,192, 4 rows: 49 us
+// here, 36 there), above 8 of a small one, 4 in the backward, whose x
+// fragments are per lane (1,536 x 512, 8 rows: forward 6.3 here, 8.7 there;
+// backward 11.9 and 9.6).
+bool linear_takes_few(long long T, int K, int N, int dtype, bool bwd) {
   if (dtype == MLP_DTYPE_F32) return T <= 8;
-  return T <= 2 || (T <= 8 && (long long)K * N <= (1ll << 22));
+  return T <= 2 || (T <= (bwd ? 4 : 8) && (long long)K * N <= (1ll << 22));
 }
 
 mlp_status launch_linear_few(const LinearArgs& a, bool bwd, float* dbias, cudaStream_t st) {

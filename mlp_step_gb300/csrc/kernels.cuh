@@ -261,7 +261,7 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st);
 int linear_tc_splits(long long T, int K, int N);
 // k_linear_small.cu: a few rows, all types, one launch; in the backward it
 // writes the column sums to `dbias` itself.
-bool linear_takes_few(long long T, int K, int N, int dtype);
+bool linear_takes_few(long long T, int K, int N, int dtype, bool bwd);
 mlp_status launch_linear_few(const LinearArgs& a, bool bwd, float* dbias, cudaStream_t st);
 // k_linear_small.cu: the epilogue over a.splits planes of raw sums (a.partial).
 mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, cudaStream_t st);
