@@ -157,8 +157,9 @@ LinearPath linear_path(long long T, int K, int N, int dtype, bool bwd) {
   LinearPath p{};
   p.few = linear_takes_few(T, K, N, dtype, bwd);
   if (p.few) return p;
-  p.splits = 1;
-  if (dtype != MLP_DTYPE_F32) {
+  if (dtype == MLP_DTYPE_F32) {
+    p.splits = linear_f32_splits(T, K, N);
+  } else {
     p.splits = linear_tc_splits(T, K, N);
     if (p.splits == 1) p.splits = 0;
   }
@@ -187,17 +188,7 @@ mlp_status run_linear(LinearArgs a, const LinearPath& lp, bool bwd, float* dbias
   a.colpart = dbias ? reinterpret_cast<float*>(ws + lp.sums) : nullptr;
   a.ldcp = lp.ldcp;
   a.part_rows = lp.part_rows;
-  if (a.dtype == MLP_DTYPE_F32) {
-    GemmArgs g{};
-    g.M = (int)a.T; g.N = a.N; g.K = a.K;
-    g.A = a.x; g.lda = (int)a.ldx;
-    g.B = a.w; g.ldb = (int)a.ldw; g.b_trans = bwd ? 1 : 0;
-    g.act = MLP_ACT_NONE;
-    g.C = a.partial; g.ldc = (int)a.ldp;
-    MLP_CHECK(launch_gemm_simt(g, 0, st));
-  } else {
-    MLP_CHECK(launch_linear_tc(a, bwd, st));
-  }
+  MLP_CHECK(a.dtype == MLP_DTYPE_F32 ? launch_linear_f32(a, bwd, st) : launch_linear_tc(a, bwd, st));
   if (lp.splits) MLP_CHECK(launch_linear_finish(a, bwd, st));
   if (!dbias) return MLP_OK;
   return launch_partial_sums(a.colpart, lp.parts(a.T), a.N, a.ldcp, dbias, a.N, nullptr,

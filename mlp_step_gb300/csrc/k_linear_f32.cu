@@ -1,0 +1,189 @@
+// fp32 products of the linear layers: raw sums into planes [splits][T][ldp]
+// that launch_linear_finish turns into the layer's outputs.
+//   forward  P = x W,    W [K][N];     backward  P = dy W^T,  W [N][K]
+//
+// Bound: fp32 FMA issue (no tensor cores: their operands are 19 bits at most).
+// A block computes 128 x 128 outputs, a thread 8 x 8 of them: per step of K
+// four 16-byte shared-memory loads feed 64 FMAs, issued as 32 packed ones (the
+// 64 x 64 tiles of the general fp32 product, 4 x 4 per thread, load as much
+// for 16: 26,823 x 2,502 x 354 2,990 us there, 890 here).  Both operands lie in
+// shared memory as [k][128 rows or columns]; matrices whose rows run along K
+// are transposed by the copies themselves (4-byte asynchronous copies, which
+// take any pitch), W [K][N] goes in 16-byte pieces where its rows allow.
+// Three stages of 16 of K, so two are in flight.  Sums run over ascending k in
+// one fused multiply-add chain per output and split.
+#include "f32x2.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "trace.cuh"
+
+namespace mlp {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int TM = 128, TN = 128, TK = 16, STAGES = 3;
+constexpr int PITCH = 132;  // floats per k: rows stay 16-byte aligned
+constexpr int kSmem = STAGES * 2 * TK * PITCH * 4;
+
+// `bytes` of src into dst, zeros past the matrix (ok false reads nothing).
+template <int BYTES>
+__device__ __forceinline__ void copy(float* dst, const float* src, bool ok) {
+  const uint32_t d = ptx::smem_u32(dst);
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src),
+                 "r"(ok ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src),
+                 "r"(ok ? 4 : 0)
+                 : "memory");
+}
+
+// Rows [r0, r0 + 128) x columns [k0, k0 + 16) of a matrix whose rows run along
+// K, transposed into s[k][row].
+__device__ __forceinline__ void stage_rows(float* s, const float* base, long long ld, long long r0,
+                                           long long rows, int k0, int k_hi, int tid) {
+  const int k = tid & 15;
+  const bool k_ok = k0 + k < k_hi;
+#pragma unroll
+  for (int i = 0; i < TM / 16; ++i) {
+    const int r = (tid >> 4) + 16 * i;
+    const bool ok = k_ok && r0 + r < rows;
+    copy<4>(s + k * PITCH + r, ok ? base + (r0 + r) * ld + k0 + k : base, ok);
+  }
+}
+
+// Rows [k0, k0 + 16) x columns [c0, c0 + 128) of a matrix [K][cols].
+__device__ __forceinline__ void stage_cols(float* s, const float* base, long long ld, int c0,
+                                           int cols, int k0, int k_hi, bool vec, int tid) {
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int k = (tid >> 5) + 8 * i, c = (tid & 31) * 4;
+      const bool row = k0 + k < k_hi;
+      if (c0 + c + 4 <= cols || !row || c0 + c >= cols) {
+        const bool ok = row && c0 + c < cols;
+        copy<16>(s + k * PITCH + c, ok ? base + (long long)(k0 + k) * ld + c0 + c : base, ok);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const bool ok = c0 + c + e < cols;
+          copy<4>(s + k * PITCH + c + e, ok ? base + (long long)(k0 + k) * ld + c0 + c + e : base,
+                  ok);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int k = (tid >> 7) + 2 * i, c = tid & 127;
+      const bool ok = k0 + k < k_hi && c0 + c < cols;
+      copy<4>(s + k * PITCH + c, ok ? base + (long long)(k0 + k) * ld + c0 + c : base, ok);
+    }
+  }
+}
+
+template <bool BWD>
+__global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArgs a, int k_per,
+                                                                 int w_vec) {
+  extern __shared__ __align__(16) float smem[];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const long long r0 = (long long)blockIdx.y * TM;
+  const int c0 = blockIdx.x * TN;
+  const int k_lo = blockIdx.z * k_per, k_hi = min(a.K, k_lo + k_per);
+  const float* x = static_cast<const float*>(a.x);
+  const float* w = static_cast<const float*>(a.w);
+  auto stage = [&](int st, int k0) {
+    float* sa = smem + st * 2 * TK * PITCH;
+    float* sb = sa + TK * PITCH;
+    if (k0 < k_hi) {
+      stage_rows(sa, x, a.ldx, r0, a.T, k0, k_hi, tid);
+      if constexpr (BWD) stage_rows(sb, w, a.ldw, c0, a.N, k0, k_hi, tid);
+      else stage_cols(sb, w, a.ldw, c0, a.N, k0, k_hi, w_vec, tid);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  // rows ty * 4 + {0..3} and 64 + ty * 4 + {0..3}; columns alike from tx
+  F2 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f2(0.f);
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) stage(s, k_lo + s * TK);
+  int st = 0;
+  for (int k0 = k_lo; k0 < k_hi; k0 += TK) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+    __syncthreads();  // this stage has landed for all; the one before is free
+    stage(st == 0 ? STAGES - 1 : st - 1, k0 + (STAGES - 1) * TK);
+    const float* sa = smem + st * 2 * TK * PITCH + ty * 4;
+    const float* sb = smem + (st * 2 + 1) * TK * PITCH + tx * 4;
+#pragma unroll
+    for (int k = 0; k < TK; ++k) {
+      const float4 a0 = *reinterpret_cast<const float4*>(sa + k * PITCH);
+      const float4 a1 = *reinterpret_cast<const float4*>(sa + k * PITCH + 64);
+      const float4 b0 = *reinterpret_cast<const float4*>(sb + k * PITCH);
+      const float4 b1 = *reinterpret_cast<const float4*>(sb + k * PITCH + 64);
+      const float av[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+      const F2 bv[4] = {f2(b0.x, b0.y), f2(b0.z, b0.w), f2(b1.x, b1.y), f2(b1.z, b1.w)};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fma2(f2(av[i]), bv[j], acc[i][j]);
+    }
+    st = st + 1 == STAGES ? 0 : st + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  // planes have whole 32-column pieces (ldp a multiple of 32): only whole
+  // quads past ldp are left out
+  float* out = a.partial + (long long)blockIdx.z * a.T * a.ldp;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const long long r = r0 + (i < 4 ? 0 : 64) + ty * 4 + (i & 3);
+    if (r >= a.T) continue;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = c0 + 64 * h + tx * 4;
+      if (c < a.ldp)
+        *reinterpret_cast<float4*>(out + r * a.ldp + c) =
+            make_float4(acc[i][2 * h].x, acc[i][2 * h].y, acc[i][2 * h + 1].x,
+                        acc[i][2 * h + 1].y);
+    }
+  }
+}
+
+}  // namespace
+
+// K split over blocks until about two per SM run, each with at least 128 of K.
+int linear_f32_splits(long long T, int K, int N) {
+  const long long tiles = (T + TM - 1) / TM * ((N + TN - 1) / TN);
+  int s = (int)(304 / tiles);
+  if (s > 16) s = 16;
+  if (s > K / 128) s = K / 128;
+  if (s < 1) s = 1;
+  const int per = ((K + s - 1) / s + TK - 1) / TK * TK;
+  return (K + per - 1) / per;
+}
+
+mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st) {
+  const long long tm = (a.T + TM - 1) / TM;
+  if (tm > 65535) return MLP_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid((a.N + TN - 1) / TN, (unsigned)tm, a.splits);
+  const int per = ((a.K + a.splits - 1) / a.splits + TK - 1) / TK * TK;
+  const int w_vec = reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.ldw % 4 == 0;
+  auto kernel = bwd ? linear_f32_kernel<true> : linear_f32_kernel<false>;
+  static const cudaError_t configured[2] = {
+      cudaFuncSetAttribute(linear_f32_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem),
+      cudaFuncSetAttribute(linear_f32_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmem)};
+  if (configured[0] != cudaSuccess || configured[1] != cudaSuccess) return MLP_ERR_CUDA;
+  LaunchScope ls(bwd ? "linear_bwd_f32" : "linear_fwd_f32", st, a.T, a.N, a.K);
+  launch_k(kernel, grid, dim3(kThreads), kSmem, st, a, per, w_vec);
+  return launch_status();
+}
+
+}  // namespace mlp

@@ -259,6 +259,9 @@ constexpr int kPartRowsFew = 4;
 mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st);
 // Split count of that kernel (from the shape alone).
 int linear_tc_splits(long long T, int K, int N);
+// k_linear_f32.cu: raw fp32 sums into a.partial, K in linear_f32_splits parts.
+mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st);
+int linear_f32_splits(long long T, int K, int N);
 // k_linear_small.cu: a few rows, all types, one launch; in the backward it
 // writes the column sums to `dbias` itself.
 bool linear_takes_few(long long T, int K, int N, int dtype, bool bwd);
