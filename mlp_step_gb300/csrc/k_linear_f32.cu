@@ -4,9 +4,10 @@
 //
 // Bound: fp32 FMA issue (no tensor cores: their operands are 19 bits at most).
 // A block computes 128 x 128 outputs, a thread 8 x 8 of them: per step of K
-// four 16-byte shared-memory loads feed 64 FMAs, issued as 32 packed ones (the
-// 64 x 64 tiles of the general fp32 product, 4 x 4 per thread, load as much
-// for 16: 26,823 x 2,502 x 354 2,990 us there, 890 here).  Both operands lie in
+// four 16-byte shared-memory loads feed 64 FMAs, issued as 32 packed ones
+// (scalar FMAs: 1.12 times the time; the 64 x 64 tiles of the general fp32
+// product, 4 x 4 per thread, load half as much for 16: 26,823 x 2,502 x 354
+// 2,990 us there, 1,060 here = 45 TFLOP/s, 56 % of the FMA rate).  Both operands lie in
 // shared memory as [k][128 rows or columns]; matrices whose rows run along K
 // are transposed by the copies themselves (4-byte asynchronous copies, which
 // take any pitch), W [K][N] goes in 16-byte pieces where its rows allow.
@@ -40,19 +41,36 @@ __device__ __forceinline__ void copy(float* dst, const float* src, bool ok) {
                  : "memory");
 }
 
-// Rows [r0, r0 + 128) x columns [k0, k0 + 16) of a matrix whose rows run along
-// K, transposed into s[k][row].
-__device__ __forceinline__ void stage_rows(float* s, const float* base, long long ld, long long r0,
-                                           long long rows, int k0, int k_hi, int tid) {
-  const int k = tid & 15;
-  const bool k_ok = k0 + k < k_hi;
+// A thread's part of staging rows [r0, r0 + 128) x 16 columns of a matrix whose
+// rows run along K, transposed into s[k][row]: column tid % 16 of rows
+// tid / 16 + 16 i.  Addresses and the rows that exist are worked out once.
+struct RowStager {
+  const float* p;
+  long long step;  // 16 rows
+  unsigned rows;   // bit i: row i exists
+  __device__ __forceinline__ RowStager(const float* base, long long ld, long long r0,
+                                       long long n_rows, int k_lo, int tid) {
+    const long long r = r0 + (tid >> 4);
+    p = base + r * ld + k_lo + (tid & 15);
+    step = 16 * ld;
+    rows = 0;
 #pragma unroll
-  for (int i = 0; i < TM / 16; ++i) {
-    const int r = (tid >> 4) + 16 * i;
-    const bool ok = k_ok && r0 + r < rows;
-    copy<4>(s + k * PITCH + r, ok ? base + (r0 + r) * ld + k0 + k : base, ok);
+    for (int i = 0; i < TM / 16; ++i) rows |= (unsigned)(r + 16 * i < n_rows) << i;
   }
-}
+  // columns [k0, k0 + 16), of which `left` exist; then moves on
+  __device__ __forceinline__ void stage(float* s, int left, const float* any, int tid) {
+    float* d = s + (tid & 15) * PITCH + (tid >> 4);
+    const unsigned ok = (tid & 15) < left ? rows : 0u;
+    const float* q = p;
+#pragma unroll
+    for (int i = 0; i < TM / 16; ++i) {
+      const bool in = ok >> i & 1;
+      copy<4>(d + 16 * i, in ? q : any, in);
+      q += step;
+    }
+    p += TK;
+  }
+};
 
 // Rows [k0, k0 + 16) x columns [c0, c0 + 128) of a matrix [K][cols].
 __device__ __forceinline__ void stage_cols(float* s, const float* base, long long ld, int c0,
@@ -96,12 +114,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
   const int k_lo = blockIdx.z * k_per, k_hi = min(a.K, k_lo + k_per);
   const float* x = static_cast<const float*>(a.x);
   const float* w = static_cast<const float*>(a.w);
+  RowStager xs(x, a.ldx, r0, a.T, k_lo, tid);
+  RowStager wr(w, a.ldw, c0, BWD ? a.N : 0, k_lo, tid);
   auto stage = [&](int st, int k0) {
     float* sa = smem + st * 2 * TK * PITCH;
     float* sb = sa + TK * PITCH;
     if (k0 < k_hi) {
-      stage_rows(sa, x, a.ldx, r0, a.T, k0, k_hi, tid);
-      if constexpr (BWD) stage_rows(sb, w, a.ldw, c0, a.N, k0, k_hi, tid);
+      xs.stage(sa, k_hi - k0, x, tid);
+      if constexpr (BWD) wr.stage(sb, k_hi - k0, w, tid);
       else stage_cols(sb, w, a.ldw, c0, a.N, k0, k_hi, w_vec, tid);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -157,15 +177,25 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
 
 }  // namespace
 
-// K split over blocks until about two per SM run, each with at least 128 of K.
+// The split of K with the smallest estimated time (cycles): rounds of blocks
+// over 304 places (two per SM, 366 cycles per k at 70 % of the FMA rate), and
+// the raw sums' way through memory.
 int linear_f32_splits(long long T, int K, int N) {
   const long long tiles = (T + TM - 1) / TM * ((N + TN - 1) / TN);
-  int s = (int)(304 / tiles);
-  if (s > 16) s = 16;
-  if (s > K / 128) s = K / 128;
-  if (s < 1) s = 1;
-  const int per = ((K + s - 1) / s + TK - 1) / TK * TK;
-  return (K + per - 1) / per;
+  int best = 1;
+  double best_cycles = 1e300;
+  for (int s = 1; s <= 16; ++s) {
+    if (s > 1 && s > K / 64) break;
+    const int per = ((K + s - 1) / s + TK - 1) / TK * TK;
+    const int splits = (K + per - 1) / per;
+    const double cycles = (double)((tiles * splits + 303) / 304) * (per * 366. + 6000) +
+                          splits * (double)T * N * 8 / 3000;
+    if (cycles < best_cycles) {
+      best_cycles = cycles;
+      best = splits;
+    }
+  }
+  return best;
 }
 
 mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st) {
