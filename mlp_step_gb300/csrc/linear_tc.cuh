@@ -526,7 +526,7 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
             warp_copy<false>(qbox, 64, reinterpret_cast<uint8_t*>(a.q) + t.row0 * a.ldq + t.n0,
                              a.ldq, rows, cols, 1, lane);
         }
-#pragma unroll(WHOLE && BWD ? 2 : 1)
+#pragma unroll(BWD && FORM == kWhole64 ? 2 : 1)
         for (int h = 0; h < 2; ++h) {
           const int n0 = t.n0 + 32 * h;
           const int cols = WHOLE ? 32 : min(32, a.N - n0);
