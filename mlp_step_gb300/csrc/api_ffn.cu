@@ -285,7 +285,8 @@ mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int 
 
 size_t mlp_act_bwd_workspace_bytes(int T, int n) {
   if (T <= 0 || n <= 0) return 0;
-  return align256((size_t)(((long long)T + kPartRows - 1) / kPartRows) * ((n + 31) / 32 * 32) * 4);
+  const int rows = act_part_rows(T, n);
+  return align256((size_t)(((long long)T + rows - 1) / rows) * ((n + 31) / 32 * 32) * 4);
 }
 
 mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int act, float slope,
@@ -315,10 +316,11 @@ mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int ac
   a.q = const_cast<int8_t*>(u_q); a.ldq = ldq;
   a.scale = const_cast<uint8_t*>(u_scale); a.lds = lds;
   a.ldcp = (n + 31) / 32 * 32;
+  a.part_rows = act_part_rows(T, n);
   a.colpart = dbias ? static_cast<float*>(workspace) : nullptr;
   MLP_CHECK(launch_act_bwd(a, S(stream)));
   if (!dbias) return MLP_OK;
-  return launch_partial_sums(a.colpart, ((long long)T + kPartRows - 1) / kPartRows, n, a.ldcp,
+  return launch_partial_sums(a.colpart, ((long long)T + a.part_rows - 1) / a.part_rows, n, a.ldcp,
                              dbias, n, nullptr, S(stream));
 }
 

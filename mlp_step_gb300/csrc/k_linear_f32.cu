@@ -178,18 +178,20 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
 }  // namespace
 
 // The split of K with the smallest estimated time (cycles): rounds of blocks
-// over 304 places (two per SM, 366 cycles per k at 70 % of the FMA rate), and
-// the raw sums' way through memory.
+// over 304 places, each k taking an SM 260 cycles with one block on it and 380
+// with two (49 and 67 % of the FMA rate), and the raw sums' way through memory
+// and the pass that adds them, four planes at a time.
 int linear_f32_splits(long long T, int K, int N) {
   const long long tiles = (T + TM - 1) / TM * ((N + TN - 1) / TN);
   int best = 1;
   double best_cycles = 1e300;
-  for (int s = 1; s <= 16; ++s) {
+  for (int s = 1; s <= 32; ++s) {
     if (s > 1 && s > K / 64) break;
     const int per = ((K + s - 1) / s + TK - 1) / TK * TK;
     const int splits = (K + per - 1) / per;
-    const double cycles = (double)((tiles * splits + 303) / 304) * (per * 366. + 6000) +
-                          splits * (double)T * N * 8 / 3000;
+    const long long blocks = tiles * splits, waves = (blocks + 303) / 304;
+    const double cycles = (blocks <= 152 ? 260. : waves * 380.) * per + waves * 6000. + splits * (double)T * N * 8 / 3000 +
+                          (splits + 3) / 4 * 1500.;
     if (cycles < best_cycles) {
       best_cycles = cycles;
       best = splits;

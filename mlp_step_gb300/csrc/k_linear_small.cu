@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
   const long long rb = unit / groups;
   const int c = ((int)(unit - rb * groups) * 32 + lane) * V;
   const int n = a.N - c;  // this lane's columns that exist
-  const long long m0 = rb * kPartRows;
-  const int rows = (int)min((long long)kPartRows, a.T - m0);
+  const long long m0 = rb * a.part_rows;
+  const int rows = (int)min((long long)a.part_rows, a.T - m0);
   const bool has_u = CK || a.u_in != nullptr;
   // pitches are ints at the C boundary: products with a row number are one
   // widening multiplication
@@ -603,7 +603,7 @@ mlp_status finish_launch(const LinearArgs& a, cudaStream_t st) {
 template <typename T, int V, bool CK>
 mlp_status act_launch(const LinearArgs& a, cudaStream_t st) {
   const int groups = (a.N + 32 * V - 1) / (32 * V);
-  const long long units = (a.T + kPartRows - 1) / kPartRows * groups;
+  const long long units = (a.T + a.part_rows - 1) / a.part_rows * groups;
   const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
   if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
   LaunchScope ls("act_bwd", st, a.T, a.N, sizeof(T));

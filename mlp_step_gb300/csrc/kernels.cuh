@@ -254,6 +254,12 @@ struct LinearArgs {
 constexpr int kPartRows = 32;
 // ... where few rows would leave a pass over raw sums with few warps
 constexpr int kPartRowsFew = 4;
+// ... of the activation's gradient alone, whose warps walk that many rows: fewer
+// where 32 would leave an SM less than twelve warps of 128 columns (448 x 10,242
+// bf16 with its column sums: 23 us with 32, 15.5 with 8)
+inline int act_part_rows(long long T, int N) {
+  return (T + 31) / 32 * ((N + 127) / 128) >= 1824 ? 32 : 8;
+}
 // k_linear.cu: tcgen05 kernel of 16-bit operands.  splits > 1: raw partial
 // sums into a.partial, to be finished by launch_linear_finish.
 mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st);
