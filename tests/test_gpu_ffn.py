@@ -834,3 +834,102 @@ def test_offsets_past_32_bits():
     M.mlp_linear_fwd(x[last].contiguous(), w, z, act=M.MLP_ACT_RELU,
                      residual=out[last].contiguous())
     near(y[last], z, 2 * half(BF16) * z.double().abs() + 1e-6, "y")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,k,n", [(2001, 72, 1600), (3300, 1160, 1088), (4097, 512, 832)])
+def test_linear_whole_pieces(T, k, n, dtype):
+    """Outputs and saved values that rows of 16-byte pieces let TMA move, against
+    the same call at odd pitches (the general form: the same arithmetic, so the
+    same bits) and, for y and du, the formula; every combination of them."""
+    x, w, bias = rnd(130, T, k, dtype), rnd(131, k, n, dtype, std=k ** -0.5), vec(132, n)
+    wt = w.t().contiguous()
+    if k % 8:
+        wt = rnd(133, n, k, dtype)
+        wt.copy_(w.t())
+    r = rnd(134, T, n, dtype)
+    r_odd = rnd(135, T, n, dtype, pitch=n + 1)
+    r_odd.copy_(r)
+    raw = x.double() @ w.double()
+    eraw = (k + 8) * 2 * U24 * (x.double().abs() @ w.double().abs())
+    ru = raw + bias.double()
+    eu = eraw + U24 * (ru.abs() + bias.double().abs())
+    f, df, curve = act_ref(ru, "gelu_tanh")
+    ef = df.abs() * eu + curve * eu * eu + ACT_ERR * (1 + ru.abs()) * (1 + f.abs())
+    for res in (False, True):
+        for save in ("none", "u", "ckpt", "both"):
+            got = []
+            for pitch in (None, n + 1):
+                y, u = Guarded(T, n, dtype, pitch), Guarded(T, n, dtype, pitch)
+                q, s = new_ckpt(T, n, pitch)
+                M.mlp_linear_fwd(x, w, y.v, bias=bias, act=M.MLP_ACT_GELU_TANH,
+                                 residual=(r_odd if pitch else r) if res else None,
+                                 u=u.v if save in ("u", "both") else None,
+                                 ckpt=(q.v, s.v) if save in ("ckpt", "both") else None)
+                assert y.intact() and u.intact() and q.intact() and s.intact()
+                got.append((y.v, u.v, q.v, s.v))
+            assert all(torch.equal(a, b) for a, b in zip(*got)), (res, save)
+            ref = f + r.double() if res else f
+            near(got[0][0], ref, rounding(dtype, ref) + ef + 2 * U24 * (ref.abs() + f.abs()), "y")
+    u = rnd(136, T, n, dtype, std=1.5)
+    u_odd = rnd(137, T, n, dtype, pitch=n + 1)
+    u_odd.copy_(u)
+    ws = torch.empty(M.mlp_linear_bwd_workspace_bytes(T, n, k, dtype), dtype=torch.uint8,
+                     device="cuda")
+    for saved in ("none", "u", "ckpt"):
+        seen = u.double()
+        for again in (False, True):
+            if saved == "none" and again:
+                continue
+            got = []
+            for pitch in (None, n + 1):
+                kw = {"u": u_odd if pitch else u}
+                if saved == "ckpt":
+                    q, s = new_ckpt(T, n, pitch)
+                    M.mlp_ckpt8_encode(u, q.v, s.v)
+                    kw, seen = {"ckpt": (q.v, s.v)}, ckpt_values(q.v, s.v)
+                du, a = Guarded(T, n, dtype, pitch), Guarded(T, n, dtype, pitch)
+                db = torch.full((n,), math.nan, device="cuda")
+                M.mlp_linear_bwd(x, wt, du.v, dbias=db, a=a.v if again else None, workspace=ws,
+                                 **({"act": M.MLP_ACT_SILU, **kw} if saved != "none" else {}))
+                assert du.intact() and a.intact()
+                got.append((du.v, a.v, db))
+            assert all(torch.equal(a, b) for a, b in zip(*got)), (saved, again)
+            d = act_ref(seen, "silu")[1] if saved != "none" else torch.ones_like(raw)
+            ref = raw * d
+            e = eraw * d.abs() + 2 * U24 * ref.abs() + (raw.abs() + eraw) * ACT_ERR * (
+                1 + seen.abs()) * (saved != "none")
+            near(got[0][0], ref, rounding(dtype, ref) + e + 1e-30, "du")
+            near(got[0][2], ref.sum(0), e.sum(0) + (T + 8) * U24 * ref.abs().sum(0) + 1e-30,
+                 "dbias")
+
+
+@pytest.mark.parametrize("T,d", [(1, 8200), (9, 10477), (380, 8209), (2500, 8200)])
+def test_layernorm_backward_wide_rows(T, d):
+    """Rows wider than a block's registers: eight of them to a partial row."""
+    x, dy = rnd(140, T, d, F32, shift=0.3), rnd(141, T, d, F32, std=0.1)
+    _, mu, rho = ln_ref(x, None, None, 1e-5)
+    dx, dg, ds = torch.empty_like(x), torch.empty(d, device="cuda"), torch.empty(d, device="cuda")
+    ws = torch.empty(M.mlp_layernorm_workspace_bytes(T, d), dtype=torch.uint8, device="cuda")
+    M.mlp_layernorm_bwd(dy, mu.float(), rho.float(), dx, dg, ds, ws, x=x)
+    mu, rho = mu.float().double(), rho.float().double()
+    xh = (x.double() - mu[:, None]) * rho[:, None]
+    t = dy.double() * xh
+    # a term: the difference (half a step of |x - mu|, which is |xh| / rho), two
+    # products and the sum of T of them in any order
+    near(dg, t.sum(0), (T + 8) * U24 * t.abs().sum(0) + 1e-30, "dgain")
+    near(ds, dy.double().sum(0), (T + 8) * U24 * dy.double().abs().sum(0), "dshift")
+
+
+@pytest.mark.parametrize("T,n", [(1, 10242), (8, 130), (9, 1001), (448, 10242)])
+def test_act_backward_few_rows(T, n):
+    """Fewer rows to a warp where there are few: their column sums."""
+    dy, u = rnd(150, T, n, BF16), rnd(151, T, n, BF16, std=2.0)
+    du, a = Guarded(T, n, BF16), Guarded(T, n, BF16)
+    db = torch.full((n,), math.nan, device="cuda")
+    ws = torch.empty(M.mlp_act_bwd_workspace_bytes(T, n), dtype=torch.uint8, device="cuda")
+    M.mlp_act_bwd(dy, du.v, act=M.MLP_ACT_RELU, u=u, dbias=db, a=a.v, workspace=ws)
+    ref = dy.double() * (u > 0)
+    assert torch.equal(du.v.double(), ref) and torch.equal(a.v, u.clamp(min=0))
+    near(db, ref.sum(0), (T + 8) * U24 * ref.abs().sum(0) + 1e-30, "dbias")
+    assert du.intact() and a.intact()
