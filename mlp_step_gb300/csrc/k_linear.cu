@@ -16,11 +16,19 @@
 // (raw sums to a workspace, finished by launch_linear_finish).  Warps: TMA
 // producer, MMA issuer, four to sixteen epilogue warps (a tensor-memory lane
 // quarter and a share of the columns each); two accumulators, so that the
-// epilogue of one tile overlaps the MMAs of the next.  W is read as it is stored: [K][N] as an
-// N-major operand, [N][K] (backward) as a K-major one.
+// epilogue of one tile overlaps the MMAs of the next.  W is read as it is
+// stored: [K][N] as an N-major operand, [N][K] (backward) as a K-major one.
+// The kernel's body is in linear_tc.cuh; pairs whose pieces are all whole run
+// the form of k_linear_whole.cu, this file has the rest and the choice.
 //
-// Bound: the MMAs for long K; for K of a few hundred, the epilogue's
-// instruction issue (an activation is 10 to 20 instructions per output).
+// Bound: the MMAs for long K (16,384 x 8,192 -> 8,192 fp16, SiLU and residual:
+// 1,240 us = 1.77 PFLOP/s, 93 % of the library's rate; 65,536 x 1,536 -> 512
+// bf16 with residual: 75 us = 1.38 PFLOP/s).  For K of a few hundred, the
+// operands' way into shared memory (65,536 x 512 -> 1,536 bf16 without an
+// activation: 82 us, of which 64 are loads and MMAs) or the epilogue's issue
+// slots (GELU and 8-bit pre-activations: 105 us, backward with kept outputs
+// and column sums: 157 us = 28 and 30 instructions an output, at 55 % of the
+// issue rate with the sixteen warps that the registers hold).
 #include <cstring>
 
 #include "linear_tc.cuh"

@@ -71,7 +71,10 @@ __device__ __forceinline__ float epi_finish(const LinearArgs& a, long long m, in
 constexpr int kRowsAhead = 4;  // rows loaded before the first is finished
 
 // Warp unit: `unit_rows` rows of 32 columns; in the backward it adds their
-// column sums in row order into one row of colpart.
+// column sums in row order into one row of colpart.  Bound by reading the
+// planes (26,823 x 354 fp32, five planes, GELU: 88 us, the issue slots 75 %
+// taken), or by latency for the few rows that are split most (168 x 325, 15
+// planes: 10 us with cold caches).
 template <typename T, bool BWD>
 __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArgs a, int groups,
                                                                  int unit_rows,
@@ -130,7 +133,9 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
 // 32 rows of 32 V columns, V per lane: four where all rows keep them aligned
 // (8- and 16-byte accesses), else one (whole 32-value runs at any alignment).
 // Two batches of rows are in flight: the next one's loads are issued before
-// this one's arithmetic (one batch at a time, 10,007 x 1,001 fp32: 52 us).
+// this one's arithmetic (one batch at a time, 10,007 x 1,001 fp32: 52 us; two:
+// 28, 4.3 TB/s, the issue slots 77 % taken: rows at odd pitches go one value per
+// lane, and the fp32 derivative is some forty instructions).
 
 template <typename T, int V>
 __device__ __forceinline__ void load_cols(const T* p, bool in, int n, float (&v)[V]) {
@@ -273,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
 //   backward, W [N][K]: a warp keeps 8 of the 64 columns and its lanes walk
 //   along K.
 // All CTAs of a launch are resident at once: a second wave of a few would
-// double the time (8,192 x 8,192 bf16, one row: 70 us).
+// double the time (8,192 x 8,192 bf16, one row: 70 us; all resident 23 us =
+// 5.8 TB/s; 512 x 1,536 with cold caches 8 us).
 
 constexpr int kFewX = 4096;   // values of x staged at a time (all rows)
 constexpr int kFewRing = 8;   // pieces of a thread's ring
