@@ -109,9 +109,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  const long long r0 = (long long)blockIdx.y * TM;
-  const int c0 = blockIdx.x * TN;
-  const int k_lo = blockIdx.z * k_per, k_hi = min(a.K, k_lo + k_per);
+  const unsigned tiles_n = (a.N + TN - 1) / TN, tm = blockIdx.x / tiles_n;
+  const long long r0 = (long long)tm * TM;
+  const int c0 = (int)(blockIdx.x - tm * tiles_n) * TN;
+  const int k_lo = blockIdx.y * k_per, k_hi = min(a.K, k_lo + k_per);
   const float* x = static_cast<const float*>(a.x);
   const float* w = static_cast<const float*>(a.w);
   RowStager xs(x, a.ldx, r0, a.T, k_lo, tid);
@@ -159,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   // planes have whole 32-column pieces (ldp a multiple of 32): only whole
   // quads past ldp are left out
-  float* out = a.partial + (long long)blockIdx.z * a.T * a.ldp;
+  float* out = a.partial + (long long)blockIdx.y * a.T * a.ldp;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const long long r = r0 + (i < 4 ? 0 : 64) + ty * 4 + (i & 3);
@@ -201,9 +202,9 @@ int linear_f32_splits(long long T, int K, int N) {
 }
 
 mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st) {
-  const long long tm = (a.T + TM - 1) / TM;
-  if (tm > 65535) return MLP_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid((a.N + TN - 1) / TN, (unsigned)tm, a.splits);
+  const long long tiles = (a.T + TM - 1) / TM * ((a.N + TN - 1) / TN);
+  if (tiles > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid((unsigned)tiles, a.splits);
   const int per = ((a.K + a.splits - 1) / a.splits + TK - 1) / TK * TK;
   const int w_vec = reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.ldw % 4 == 0;
   auto kernel = bwd ? linear_f32_kernel<true> : linear_f32_kernel<false>;

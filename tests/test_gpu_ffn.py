@@ -933,3 +933,31 @@ def test_act_backward_few_rows(T, n):
     assert torch.equal(du.v.double(), ref) and torch.equal(a.v, u.clamp(min=0))
     near(db, ref.sum(0), (T + 8) * U24 * ref.abs().sum(0) + 1e-30, "dbias")
     assert du.intact() and a.intact()
+
+
+def test_linear_f32_many_rows():
+    """More row tiles than a grid's second dimension holds."""
+    T, k, n = 65535 * 128 + 5, 4, 3
+    x, w, bias = rnd(160, T, k, F32), rnd(161, k, n, F32), vec(162, n)
+    y = Guarded(T, n, F32, 3)
+    ws = torch.empty(M.mlp_linear_workspace_bytes(T, k, n, F32), dtype=torch.uint8, device="cuda")
+    M.mlp_linear_fwd(x, w, y.v, bias=bias, act=M.MLP_ACT_RELU, workspace=ws)
+    u = x.double() @ w.double() + bias.double()
+    # four products and four sums, each off by at most half a step of the sum
+    # of the terms' magnitudes
+    e = 8 * U24 * (x.double().abs() @ w.double().abs() + bias.double().abs())
+    near(y.v, u.clamp(min=0), e, "y")
+    assert y.intact()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_ckpt8_again_is_the_same(dtype):
+    """Encoding what was decoded gives the same bytes (q has at most 8 bits)."""
+    x = rnd(163, 300, 1001, dtype, std=3.0) * torch.logspace(-30, 30, 300, device="cuda")[:, None]
+    x = x.to(dtype)
+    q, s, q2, s2 = *new_ckpt(300, 1001), *new_ckpt(300, 1001)
+    out = torch.empty(300, 1001, dtype=dtype, device="cuda")
+    M.mlp_ckpt8_encode(x, q.v, s.v)
+    M.mlp_ckpt8_decode(q.v, s.v, out)
+    M.mlp_ckpt8_encode(out, q2.v, s2.v)
+    assert torch.equal(q.v, q2.v) and torch.equal(s.v, s2.v)
