@@ -9,9 +9,8 @@
 // with 64 bytes in flight per thread and full occupancy the loads cover the
 // latency without a staging pipeline.
 // Measured: 262,144 x 512 bf16 encoded in 62 us and decoded in 59 (6.6 and 6.9
-// TB/s, the copy rate); 10,007 x 1,001 fp32, whose rows start anywhere and move
-// value by value, in 16 and 18 (3.2 and 2.7 TB/s, bound by
-// instruction issue; 26 us both ways where L2 holds the matrix).
+// TB/s, the copy rate).  Rows that start anywhere: the kernels of a value per
+// lane below.
 #include "ckpt8.cuh"
 #include "kernels.cuh"
 #include "rowvec.cuh"
@@ -136,6 +135,83 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// Rows that start anywhere: a value per lane, so that a group is a warp (its
+// largest magnitude one reduction) and unaligned runs still leave as whole
+// lines.  A warp takes eight groups of a row, all loads first.  (10,007 x 1,001,
+// encoded and decoded: fp32 9.9 and 7.6 us, bf16 9.9 and 7.1; by pieces, whose
+// values then move one by one, 12.5 and 12.7, 14.3 and 28.4.)
+constexpr int kRowGroups = 8, kRowChunk = kRowGroups * kCkptGroup;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_encode_rows_kernel(const T* __restrict__ x, unsigned units, unsigned chunks, int cols,
+                             long long ldx, int8_t* __restrict__ q, long long ldq,
+                             uint8_t* __restrict__ scale, long long lds) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 31;
+  const unsigned row = unit / chunks;
+  const int g0 = (int)(unit - row * chunks) * kRowGroups, c = g0 * kCkptGroup + lane;
+  const T* px = x + row * ldx + c;
+  int8_t* pq = q + row * ldq + c;
+  float v[kRowGroups];
+#pragma unroll
+  for (int g = 0; g < kRowGroups; ++g)
+    v[g] = c + g * kCkptGroup < cols ? to_f32(px[g * kCkptGroup]) : 0.f;
+  uint32_t mine = 0;
+#pragma unroll
+  for (int g = 0; g < kRowGroups; ++g) {
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v[g]) & 0x7fffffffu);
+    const uint32_t b = ckpt8_byte(top);
+    if (ckpt8_must_hold(top)) v[g] = ckpt8_hold(v[g], ckpt8_step(b));
+    const uint32_t w = b == kCkptNanByte ? 0u : ckpt8_q(v[g], ckpt8_inv_step(b));
+    if (c + g * kCkptGroup < cols) pq[g * kCkptGroup] = (int8_t)w;
+    if (lane == g) mine = b;
+  }
+  if (lane < kRowGroups && (g0 + lane) * kCkptGroup < cols)
+    scale[row * lds + g0 + lane] = (uint8_t)mine;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    ckpt8_decode_rows_kernel(const int8_t* __restrict__ q, long long ldq,
+                             const uint8_t* __restrict__ scale, long long lds, unsigned units,
+                             unsigned chunks, int cols, T* __restrict__ out, long long ldo) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const unsigned unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 31;
+  const unsigned row = unit / chunks;
+  const int g0 = (int)(unit - row * chunks) * kRowGroups, c = g0 * kCkptGroup + lane;
+  const int8_t* pq = q + row * ldq + c;
+  T* po = out + row * ldo + c;
+  uint32_t b = 0;
+  if (lane < kRowGroups && (g0 + lane) * kCkptGroup < cols) b = scale[row * lds + g0 + lane];
+  int w[kRowGroups];
+#pragma unroll
+  for (int g = 0; g < kRowGroups; ++g)
+    w[g] = c + g * kCkptGroup < cols ? pq[g * kCkptGroup] : 0;
+  const float step = ckpt8_step(b);
+#pragma unroll
+  for (int g = 0; g < kRowGroups; ++g) {
+    const float s = __shfl_sync(0xffffffffu, step, g);
+    if (c + g * kCkptGroup < cols) from_f32((float)w[g] * s, po[g * kCkptGroup]);
+  }
+}
+
+// Units of those kernels; 0 where they are too many for their 32-bit numbers, or
+// rows so narrow that they leave a warp's chunk mostly empty (100,000 x 45 fp32:
+// encoded in 22 us by rows, 9 by pieces).
+unsigned row_units(long long rows, int cols, unsigned* chunks) {
+  *chunks = (cols + kRowChunk - 1) / kRowChunk;
+  if (cols < kRowChunk * 3 / 4) return 0u;
+  const long long units = rows * *chunks;
+  return units < 0x7fffffffll ? (unsigned)units : 0u;
+}
+
 // Rows of pitch ld (elements of size esz) keep pieces of `bytes` aligned?
 bool rows_aligned(const void* p, long long ld, int esz, int bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 && ld * esz % bytes == 0;
@@ -155,10 +231,18 @@ mlp_status encode_t(const T* x, long long rows, int cols, long long ldx, int8_t*
   if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
   LaunchScope ls("ckpt8_encode", st, rows, cols, sizeof(T));
   const bool flat = one_row(rows, cols, ldx, ldq, lds);
+  const int x_vec = rows_aligned(x, ldx, sizeof(T), 16), q_vec = rows_aligned(q, ldq, 1, RowVec<T>::N);
+  unsigned chunks;
+  const unsigned units = flat || (x_vec && q_vec) ? 0u : row_units(rows, cols, &chunks);
+  if (units) {
+    launch_k(ckpt8_encode_rows_kernel<T>, dim3((units + kThreads / 32 - 1) / (kThreads / 32)),
+             dim3(kThreads), 0, st, x, units, chunks, cols, ldx, q, ldq, scale, lds);
+    return launch_status();
+  }
   launch_k(flat ? ckpt8_encode_kernel<T, true> : ckpt8_encode_kernel<T, false>,
            dim3((unsigned)blocks), dim3(kThreads), 0, st, x, flat ? 1ll : rows,
            flat ? rows * cols : (long long)cols, ldx, q, ldq, scale, lds,
-           (int)rows_aligned(x, ldx, sizeof(T), 16), (int)rows_aligned(q, ldq, 1, RowVec<T>::N));
+           x_vec, q_vec);
   return launch_status();
 }
 
@@ -170,10 +254,18 @@ mlp_status decode_t(const int8_t* q, long long ldq, const uint8_t* scale, long l
   if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
   LaunchScope ls("ckpt8_decode", st, rows, cols, sizeof(T));
   const bool flat = one_row(rows, cols, ldo, ldq, lds);
+  const int q_vec = rows_aligned(q, ldq, 1, RowVec<T>::N), o_vec = rows_aligned(out, ldo, sizeof(T), 16);
+  unsigned chunks;
+  const unsigned units = flat || (q_vec && o_vec) ? 0u : row_units(rows, cols, &chunks);
+  if (units) {
+    launch_k(ckpt8_decode_rows_kernel<T>, dim3((units + kThreads / 32 - 1) / (kThreads / 32)),
+             dim3(kThreads), 0, st, q, ldq, scale, lds, units, chunks, cols, out, ldo);
+    return launch_status();
+  }
   launch_k(flat ? ckpt8_decode_kernel<T, true> : ckpt8_decode_kernel<T, false>,
            dim3((unsigned)blocks), dim3(kThreads), 0, st, q, ldq, scale, lds, flat ? 1ll : rows,
            flat ? rows * cols : (long long)cols, out, ldo,
-           (int)rows_aligned(q, ldq, 1, RowVec<T>::N), (int)rows_aligned(out, ldo, sizeof(T), 16));
+           q_vec, o_vec);
   return launch_status();
 }
 

@@ -961,3 +961,29 @@ def test_ckpt8_again_is_the_same(dtype):
     M.mlp_ckpt8_decode(q.v, s.v, out)
     M.mlp_ckpt8_encode(out, q2.v, s2.v)
     assert torch.equal(q.v, q2.v) and torch.equal(s.v, s2.v)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+def test_ckpt8_special_values_at_odd_pitches(dtype):
+    """Infinities, NaNs, zeros, tiny values and largest magnitudes that round to
+    128, in rows that start anywhere: the bytes of the same rows aligned."""
+    d = 1001
+    x = rnd(164, 40, d, dtype, std=2.0)
+    tiny = torch.finfo(dtype).smallest_normal
+    for i, v in enumerate((math.inf, -math.inf, math.nan, 0.0, tiny, -tiny / 4, 1.9999, -255 / 128,
+                           torch.finfo(dtype).max)):
+        x[4 * i, 31 * i::97] = v
+        x[4 * i + 1] = v
+        x[4 * i + 2, d - 1] = v
+    odd = rnd(165, 40, d, dtype, pitch=d)
+    odd.copy_(x)
+    q, s, q2, s2 = *new_ckpt(40, d), *new_ckpt(40, d, d)
+    M.mlp_ckpt8_encode(x, q.v, s.v)
+    M.mlp_ckpt8_encode(odd, q2.v, s2.v)
+    assert torch.equal(q.v, q2.v) and torch.equal(s.v, s2.v) and s2.intact()
+    a, b = Guarded(40, d, dtype), Guarded(40, d, dtype, d)
+    M.mlp_ckpt8_decode(q.v, s.v, a.v)
+    M.mlp_ckpt8_decode(q.v, s.v, b.v)
+    ra, rb = (t.v.contiguous().view(torch.int32 if dtype == F32 else torch.int16) for t in (a, b))
+    assert torch.equal(a.v.isnan(), b.v.isnan())
+    assert torch.equal(ra[~a.v.isnan()], rb[~b.v.isnan()]) and a.intact() and b.intact()
