@@ -6,6 +6,8 @@
 // In the first two a warp finishes 32 columns of a row at a time, one per
 // lane: memory is touched in whole rows of 32 values and a group of the 8-bit
 // form is one warp, its largest magnitude one warp reduction.
+#include <type_traits>
+
 #include "act.cuh"
 #include "ckpt8.cuh"
 #include "kernels.cuh"
@@ -130,58 +132,81 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
 // ------------------------------------------------------------ activation backward
 //
 // du = dy f'(u), a = f(u) and partial column sums: bound by HBM.  A warp takes
-// 32 rows of 32 V columns, V per lane: four where all rows keep them aligned
+// 32 (8) rows of 32 V columns, V per lane: four where all rows keep them aligned
 // (8- and 16-byte accesses), else one (whole 32-value runs at any alignment).
 // Two batches of rows are in flight: the next one's loads are issued before
-// this one's arithmetic (one batch at a time, 10,007 x 1,001 fp32: 52 us; two:
-// 28, 4.3 TB/s, the issue slots 77 % taken: rows at odd pitches go one value per
-// lane, and the fp32 derivative is some forty instructions).
+// this one's arithmetic.  Measured with GELU (tanh) and column sums: 65,536 x
+// 1,536 bf16 108 us (5.6 TB/s), fp32 188 (6.4 TB/s); 10,007 x 1,001 fp32, a
+// value per lane and some forty instructions each, 28 (4.3 TB/s, the issue
+// slots 78 % taken; with one batch at a time 52).
 
+// V neighbouring values as they lie in memory, in whole registers.
 template <typename T, int V>
-__device__ __forceinline__ void load_cols(const T* p, bool in, int n, float (&v)[V]) {
-  if constexpr (V == 1) {
-    v[0] = in && n > 0 ? to_f32(*p) : 0.f;
-  } else {
-    if (in && n >= V) {
-      union {
-        uint4 q4;
-        uint2 q2;
-        T t[V];
-      } u;
-      if constexpr (sizeof(T) == 4) u.q4 = *reinterpret_cast<const uint4*>(p);
-      else u.q2 = *reinterpret_cast<const uint2*>(p);
+union Cols {
+  static constexpr int BYTES = sizeof(T) * V, WORDS = (BYTES + 3) / 4;
+  uint32_t w[WORDS];
+  T t[V];
+  __device__ __forceinline__ Cols() {}
+  // Nothing computed from the words moves to before this point.  (The compiler
+  // converts 16-bit values where they are loaded, and so waits for the load.)
+  __device__ __forceinline__ void pin() {
 #pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = to_f32(u.t[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < V; ++j) v[j] = in && j < n ? to_f32(p[j]) : 0.f;
-    }
+    for (int i = 0; i < WORDS; ++i) asm volatile("" : "+r"(w[i]));
   }
-}
+};
 
+// ... of which the first n exist (none where the row does not); V > 1 only
+// where rows keep them aligned.
+template <typename T, int V>
+__device__ __forceinline__ Cols<T, V> load_cols(const T* p, bool in, int n) {
+  using C = Cols<T, V>;
+  C r;
+#pragma unroll
+  for (int i = 0; i < C::WORDS; ++i) r.w[i] = 0u;
+  if (in && n >= V) {
+    if constexpr (C::BYTES == 16) {
+      const uint4 q = *reinterpret_cast<const uint4*>(p);
+      r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+    } else if constexpr (C::BYTES == 8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      r.w[0] = q.x, r.w[1] = q.y;
+    } else if constexpr (C::BYTES == 4) {
+      r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (C::BYTES == 2) {
+      r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else {
+      r.w[0] = *reinterpret_cast<const uint8_t*>(p);
+    }
+  } else if (V > 1 && in) {
+#pragma unroll
+    for (int j = 0; j < V - 1; ++j)
+      if (j < n) r.t[j] = p[j];
+  }
+  return r;
+}
 template <typename T, int V>
 __device__ __forceinline__ void store_cols(T* p, int n, const float (&v)[V]) {
-  if (V > 1 && n >= V) {
-    union {
-      uint4 q4;
-      uint2 q2;
-      T t[V];
-    } u;
+  using C = Cols<T, V>;
+  C r;
 #pragma unroll
-    for (int j = 0; j < V; ++j) from_f32(v[j], u.t[j]);
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint4*>(p) = u.q4;
-    else *reinterpret_cast<uint2*>(p) = u.q2;
+  for (int j = 0; j < V; ++j) from_f32(v[j], r.t[j]);
+  if (n >= V) {
+    if constexpr (C::BYTES == 16)
+      *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else if constexpr (C::BYTES == 8) *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    else *p = r.t[0];
   } else {
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-      if (j < n) from_f32(v[j], p[j]);
+    for (int j = 0; j < V - 1; ++j)
+      if (j < n) p[j] = r.t[j];
   }
 }
 
 template <typename T, int V, bool CK>
 __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a, int groups,
                                                               long long units) {
-  constexpr int R = V == 1 ? 4 : 2;  // rows of a batch
+  constexpr bool ACC = sizeof(T) == 4;
+  constexpr int R = V > 1 && ACC ? 2 : 4;  // rows of a batch
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -203,56 +228,88 @@ __global__ void __launch_bounds__(kThreads, 3) act_bwd_kernel(const LinearArgs a
   const uint8_t* sc = a.scale + m0 * lds + c / kCkptGroup;
   T* du = static_cast<T*>(a.y) + m0 * ldy + c;
   T* ao = static_cast<T*>(a.u_out) + m0 * ldo + c;
-  float g[R][V], x[R][V];
-  float sum[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) sum[j] = 0.f;
+  // A batch as it lies in memory: whatever is computed from a load waits for
+  // it, so nothing is until the batch's turn (converted on arrival, 65,536 x
+  // 1,536 bf16 took 302 us instead of 108).
+  using S = typename std::conditional<CK, int8_t, T>::type;  // of the saved values
+  struct Batch {
+    Cols<T, V> g[R];
+    Cols<S, V> x[R];
+    uint32_t b[R];
+  };
   auto load = [&](int r0) {
+    Batch t;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const int r = r0 + k;
       const bool in = r < rows;
-      load_cols<T, V>(dy + (long long)r * ldx, in, n, g[k]);
+      t.g[k] = load_cols<T, V>(dy + (long long)r * ldx, in, n);
       if constexpr (CK) {
-        const float step = in && n > 0 ? ckpt8_step(sc[(long long)r * lds]) : 0.f;
-        const int8_t* p = q + (long long)r * ldq;
-        if (V == 4 && in && n >= V) {
-          const uint32_t w = ckpt8_flip(*reinterpret_cast<const uint32_t*>(p));
-#pragma unroll
-          for (int j = 0; j < V; ++j) x[k][j] = ckpt8_value(w, j, step);
-        } else {
-#pragma unroll
-          for (int j = 0; j < V; ++j) x[k][j] = in && j < n ? (float)p[j] * step : 0.f;
-        }
-      } else if (has_u) {
-        load_cols<T, V>(u + (long long)r * ldu, in, n, x[k]);
+        t.x[k] = load_cols<int8_t, V>(q + (long long)r * ldq, in, n);
+        t.b[k] = in && n > 0 ? sc[(long long)r * lds] : 0;
+      } else {
+        t.x[k] = load_cols<T, V>(u + (long long)r * ldu, in && has_u, n);
       }
     }
+    return t;
   };
-  load(0);
+  float sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[j] = 0.f;
+  Batch next = load(0);
   with_act(a.act, [&](auto tag) {
     constexpr int ACT = decltype(tag)::value;
+#pragma unroll 1
     for (int r0 = 0; r0 < rows; r0 += R) {
-      float gc[R][V], xc[R][V];
-#pragma unroll
-      for (int k = 0; k < R; ++k)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-          gc[k][j] = g[k][j];
-          xc[k][j] = has_u ? x[k][j] : 0.f;
-        }
-      if (r0 + R < rows) load(r0 + R);
+      Batch t = next;
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        if (r0 + k >= rows) break;  // warp-uniform
-        float f[V];
+        t.g[k].pin();
+        t.x[k].pin();
+      }
+      if (r0 + R < rows) next = load(r0 + R);
+      // two values at a time: neighbours, or a column of two rows
+      constexpr int KP = V == 1 ? 2 : 1;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          gc[k][j] *= act_grad_of<sizeof(T) == 4, ACT>(xc[k][j], a.slope, f[j]);
-          sum[j] += gc[k][j];
+      for (int k = 0; k < R; k += KP) {
+        float g[KP][V], x[KP][V], f[KP][V];
+#pragma unroll
+        for (int e = 0; e < KP; ++e) {
+          const Cols<T, V>& tg = t.g[k + e];
+          const Cols<S, V>& tx = t.x[k + e];
+          const float step = CK ? ckpt8_step(t.b[k + e]) : 0.f;
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            g[e][j] = to_f32(tg.t[j]);
+            if constexpr (CK) x[e][j] = (float)tx.t[j] * step;
+            else x[e][j] = to_f32(tx.t[j]);
+          }
         }
-        store_cols<T, V>(du + (long long)(r0 + k) * ldy, n, gc[k]);
-        if (a.u_out) store_cols<T, V>(ao + (long long)(r0 + k) * ldo, n, f);
+        float* gv = &g[0][0];
+        float* fv = &f[0][0];
+        const float* xv = &x[0][0];
+#pragma unroll
+        for (int i = 0; i < KP * V; i += 2) {
+          if constexpr (ACC) {
+            gv[i] *= act_grad_of<true, ACT>(xv[i], a.slope, fv[i]);
+            gv[i + 1] *= act_grad_of<true, ACT>(xv[i + 1], a.slope, fv[i + 1]);
+          } else {
+            F2 w;
+            const F2 d = mul2(f2(gv[i], gv[i + 1]), act_grad2<ACT>(f2(xv[i], xv[i + 1]), a.slope, w));
+            gv[i] = d.x;
+            gv[i + 1] = d.y;
+            fv[i] = w.x;
+            fv[i + 1] = w.y;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < KP; ++e) {
+          if (r0 + k + e >= rows) break;  // warp-uniform
+#pragma unroll
+          for (int j = 0; j < V; ++j) sum[j] += g[e][j];
+          store_cols<T, V>(du + (long long)(r0 + k + e) * ldy, n, g[e]);
+          if (a.u_out) store_cols<T, V>(ao + (long long)(r0 + k + e) * ldo, n, f[e]);
+        }
       }
     }
   });
