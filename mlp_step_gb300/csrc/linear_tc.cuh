@@ -96,6 +96,34 @@ __device__ __forceinline__ uint8_t* chunk_at(uint8_t* box, int row_bytes, int r,
   return box + r * row_bytes + ((c ^ swz) << 4);
 }
 
+// One value per lane and row; what is read from memory four rows at a time, so
+// that their latencies overlap (backward of 43,599 x 144 -> 1,241 fp16 from u
+// kept at an odd pitch: 480 us one by one, 261 this way).
+template <bool OUT, typename V>
+__device__ __forceinline__ void warp_copy_values(uint8_t* box, int row_bytes, uint8_t* mem,
+                                                 long long ld, int rows, int n, int lane) {
+  constexpr int B = OUT ? 1 : 4;  // rows at a time (more spill)
+#pragma unroll 1
+  for (int j = lane; j < n; j += 32) {
+    const int o = j * (int)sizeof(V);
+#pragma unroll 1
+    for (int r = 0; r < rows; r += B) {
+      V v[B];
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        const uint8_t* bp = chunk_at(box, row_bytes, r + k, o >> 4) + (o & 15);
+        if (r + k < rows)
+          v[k] = *reinterpret_cast<const V*>(OUT ? bp : mem + (r + k) * ld + o);
+      }
+#pragma unroll
+      for (int k = 0; k < B; ++k) {
+        uint8_t* bp = chunk_at(box, row_bytes, r + k, o >> 4) + (o & 15);
+        if (r + k < rows) *reinterpret_cast<V*>(OUT ? mem + (r + k) * ld + o : bp) = v[k];
+      }
+    }
+  }
+}
+
 // The warp's own copy between a box and a matrix: `rows` rows of `bytes` bytes,
 // `esz` per value, at mem with a pitch of ld bytes.  16-byte pieces where rows
 // and widths allow, else one value per lane (runs of 32 values either way).
@@ -113,26 +141,12 @@ __device__ __forceinline__ void warp_copy(uint8_t* box, int row_bytes, uint8_t* 
       if (OUT) *m = *b;
       else *b = *m;
     }
+  } else if (esz == 1) {
+    warp_copy_values<OUT, uint8_t>(box, row_bytes, mem, ld, rows, bytes, lane);
+  } else if (esz == 2) {
+    warp_copy_values<OUT, uint16_t>(box, row_bytes, mem, ld, rows, bytes >> 1, lane);
   } else {
-    const int n = bytes / esz;
-#pragma unroll 1
-    for (int r = 0; r < rows; ++r)
-#pragma unroll 1
-      for (int j = lane; j < n; j += 32) {
-        const int o = j * esz;
-        uint8_t* b = chunk_at(box, row_bytes, r, o >> 4) + (o & 15);
-        uint8_t* m = mem + r * ld + o;
-        if (esz == 1) {
-          if (OUT) *m = *b;
-          else *b = *m;
-        } else if (esz == 2) {
-          if (OUT) *reinterpret_cast<uint16_t*>(m) = *reinterpret_cast<uint16_t*>(b);
-          else *reinterpret_cast<uint16_t*>(b) = *reinterpret_cast<uint16_t*>(m);
-        } else {
-          if (OUT) *reinterpret_cast<uint32_t*>(m) = *reinterpret_cast<uint32_t*>(b);
-          else *reinterpret_cast<uint32_t*>(b) = *reinterpret_cast<uint32_t*>(m);
-        }
-      }
+    warp_copy_values<OUT, uint32_t>(box, row_bytes, mem, ld, rows, bytes >> 2, lane);
   }
   __syncwarp();
 }
