@@ -408,7 +408,9 @@ mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float ep
  *     same in every run; MLP_ORDER_LINEAR does not apply here;
  *   - calls that take a workspace write it before they read it; calls that may
  *     overlap on the GPU (other streams, graphs in flight together) need
- *     workspaces of their own.
+ *     workspaces of their own.  Fewer rows may need more of it (work is split
+ *     further where rows are few): a buffer for several row counts is as large
+ *     as the largest of their sizes, and one too small is refused.
  */
 
 /* ---------------------------------------------------------------- 8-bit checkpoints

@@ -634,7 +634,8 @@ def mlp_layernorm_bwd(dy, mean, rstd, dx, dgain, dshift, workspace, x=None, ckpt
 
 
 def mlp_linear_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
-    """Workspace of mlp_linear_fwd (0 for most shapes); dtype: the operands' torch dtype."""
+    """Workspace of mlp_linear_fwd (0 for most shapes; fewer rows may need more);
+    dtype: the operands' torch dtype."""
     return load().mlp_linear_workspace_bytes(T, d_in, d_out, _code_of(dtype))
 
 
@@ -659,7 +660,8 @@ def mlp_linear_fwd(x, w, y, bias=None, act=MLP_ACT_NONE, slope=0.5, residual=Non
 
 
 def mlp_linear_bwd_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
-    """Workspace of mlp_linear_bwd for w [d_in, d_out] and dy [T, d_out]."""
+    """Workspace of mlp_linear_bwd for w [d_in, d_out] and dy [T, d_out] (fewer
+    rows may need more)."""
     return load().mlp_linear_bwd_workspace_bytes(T, d_in, d_out, _code_of(dtype))
 
 
@@ -685,6 +687,7 @@ def mlp_linear_bwd(dy, w, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, db
 
 
 def mlp_act_bwd_workspace_bytes(T: int, n: int) -> int:
+    """Workspace of mlp_act_bwd with dbias (fewer rows may need more)."""
     return load().mlp_act_bwd_workspace_bytes(T, n)
 
 

@@ -191,8 +191,8 @@ int linear_f32_splits(long long T, int K, int N) {
     const int per = ((K + s - 1) / s + TK - 1) / TK * TK;
     const int splits = (K + per - 1) / per;
     const long long blocks = tiles * splits, waves = (blocks + 303) / 304;
-    const double cycles = (blocks <= 152 ? 260. : waves * 380.) * per + waves * 6000. + splits * (double)T * N * 8 / 3000 +
-                          (splits + 3) / 4 * 1500.;
+    const double cycles = (blocks <= 152 ? 260. : waves * 380.) * per + waves * 6000. +
+                          splits * (double)T * N * 8 / 3000 + (splits + 3) / 4 * 1500.;
     if (cycles < best_cycles) {
       best_cycles = cycles;
       best = splits;

@@ -245,7 +245,7 @@ struct LinearArgs {
   uint8_t* scale;
   long long lds;
   float* colpart;    // backward: fp32 [ceil(T / part_rows)][ldcp] partial column sums (nullable)
-  int part_rows;     // rows of du to a row of colpart: 32 but in launch_linear_finish
+  int part_rows;     // rows of du to a row of colpart: 32 in the tensor-core tiles
   long long ldcp;
   float* partial;    // fp32 [splits][T][ldp] raw sums
   long long ldp;

@@ -987,3 +987,23 @@ def test_ckpt8_special_values_at_odd_pitches(dtype):
     ra, rb = (t.v.contiguous().view(torch.int32 if dtype == F32 else torch.int16) for t in (a, b))
     assert torch.equal(a.v.isnan(), b.v.isnan())
     assert torch.equal(ra[~a.v.isnan()], rb[~b.v.isnan()]) and a.intact() and b.intact()
+
+
+def test_act_backward_workspace_of_fewer_rows():
+    """Fewer rows may need a larger workspace: one too small for them is refused,
+    the largest of the sizes serves all."""
+    n, counts = 128, (58_400, 58_300, 700)
+    sizes = [M.mlp_act_bwd_workspace_bytes(T, n) for T in counts]
+    assert sizes[1] > sizes[0]
+    dy, u = rnd(170, counts[0], n, BF16), rnd(171, counts[0], n, BF16)
+    du, db = torch.empty_like(dy), torch.empty(n, device="cuda")
+    small = torch.empty(sizes[0], dtype=torch.uint8, device="cuda")
+    with pytest.raises(M.MlpError):
+        M.mlp_act_bwd(dy[:counts[1]], du[:counts[1]], u=u[:counts[1]], act=M.MLP_ACT_RELU,
+                      dbias=db, workspace=small)
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device="cuda")
+    for T in counts:
+        M.mlp_act_bwd(dy[:T], du[:T], u=u[:T], act=M.MLP_ACT_RELU, dbias=db, workspace=ws)
+        ref = dy[:T].double() * (u[:T] > 0)
+        assert torch.equal(du[:T].double(), ref)
+        near(db, ref.sum(0), (T + 8) * U24 * ref.abs().sum(0), "dbias")
