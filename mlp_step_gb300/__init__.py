@@ -450,13 +450,14 @@ def mlp_stack_train_step(n_blocks, T, d, hidden, x0, target, params, velocity, g
 
 
 def mlp_stack_ckpt8_workspace_bytes(n_blocks: int, T: int, d: int, hidden: int) -> int:
-    return load().mlp_stack_ckpt8_workspace_bytes(n_blocks, T, d, hidden)
+    return load().mlp_stack_ckpt8_workspace_bytes(*_sizes(n_blocks, T, d, hidden))
 
 
 def mlp_stack_train_step_ckpt8(n_blocks, T, d, hidden, x0, target, params, velocity, grads,
                                params_bf16, lr, momentum, loss_out, workspace, eps=1e-6,
                                slope=0.5, stream=None):
     """mlp_stack_train_step with the kept block outputs in 8 bits."""
+    _sizes(n_blocks, T, d, hidden)
     wsb = workspace.numel() * workspace.element_size()
     _check(load().mlp_stack_train_step_ckpt8(n_blocks, T, d, hidden, eps, slope, _ptr(x0),
                                              _ptr(target), _ptr(params), _ptr(velocity),
@@ -504,6 +505,18 @@ def _device(t, what):
     return dev
 
 
+# The C entry points take sizes and pitches as 32-bit ints, and ctypes would
+# pass a larger one on by its low 32 bits.
+_INT_MAX = 0x7fffffff
+
+
+def _sizes(*n):
+    """The sizes as they are, if each fits a 32-bit int."""
+    if max(n) > _INT_MAX or min(n) < -_INT_MAX:
+        raise ValueError("sizes and row pitches must be at most %d (got %s)" % (_INT_MAX, n))
+    return n
+
+
 def _mat(t, what, rows, cols, dev, dtype=None):
     """(address, row pitch) of a [rows, cols] matrix on device dev; (None, 0) for None."""
     if t is None:
@@ -518,9 +531,13 @@ def _mat(t, what, rows, cols, dev, dtype=None):
     if step != 1 and cols > 1:
         raise ValueError("%s: the values of a row must be adjacent (strides %s)"
                          % (what, (pitch, step)))
-    # the pitch of a single row is never used; a whole number of 16-byte
-    # pieces keeps it acceptable for any width
-    return t.data_ptr(), pitch if rows > 1 else (cols + 15) // 16 * 16
+    if rows <= 1:
+        # the pitch of a single row is never used; a whole number of 16-byte
+        # pieces keeps it acceptable for any width
+        pitch = (cols + 15) // 16 * 16
+    if (rows | cols | pitch) > _INT_MAX:  # none is negative
+        _sizes(rows, cols, pitch)
+    return t.data_ptr(), pitch
 
 
 def _vec(t, what, n, dev):
@@ -572,7 +589,7 @@ def _stream_of(stream, dev):
 
 def mlp_ckpt8_scale_cols(cols: int) -> int:
     """Scale bytes per row of an 8-bit checkpoint of `cols` columns."""
-    return load().mlp_ckpt8_scale_cols(cols)
+    return load().mlp_ckpt8_scale_cols(*_sizes(cols))
 
 
 def mlp_ckpt8_encode(x, q, scale, stream=None):
@@ -611,7 +628,7 @@ def mlp_layernorm_fwd(x, y, gain=None, shift=None, mean=None, rstd=None, ckpt=No
 
 
 def mlp_layernorm_workspace_bytes(T: int, d: int) -> int:
-    return load().mlp_layernorm_workspace_bytes(T, d)
+    return load().mlp_layernorm_workspace_bytes(*_sizes(T, d))
 
 
 def mlp_layernorm_bwd(dy, mean, rstd, dx, dgain, dshift, workspace, x=None, ckpt=None, gain=None,
@@ -636,7 +653,7 @@ def mlp_layernorm_bwd(dy, mean, rstd, dx, dgain, dshift, workspace, x=None, ckpt
 def mlp_linear_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
     """Workspace of mlp_linear_fwd (0 for most shapes; fewer rows may need more);
     dtype: the operands' torch dtype."""
-    return load().mlp_linear_workspace_bytes(T, d_in, d_out, _code_of(dtype))
+    return load().mlp_linear_workspace_bytes(*_sizes(T, d_in, d_out), _code_of(dtype))
 
 
 def mlp_linear_fwd(x, w, y, bias=None, act=MLP_ACT_NONE, slope=0.5, residual=None, u=None,
@@ -662,7 +679,7 @@ def mlp_linear_fwd(x, w, y, bias=None, act=MLP_ACT_NONE, slope=0.5, residual=Non
 def mlp_linear_bwd_workspace_bytes(T: int, d_in: int, d_out: int, dtype) -> int:
     """Workspace of mlp_linear_bwd for w [d_in, d_out] and dy [T, d_out] (fewer
     rows may need more)."""
-    return load().mlp_linear_bwd_workspace_bytes(T, d_in, d_out, _code_of(dtype))
+    return load().mlp_linear_bwd_workspace_bytes(*_sizes(T, d_in, d_out), _code_of(dtype))
 
 
 def mlp_linear_bwd(dy, w, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, dbias=None, a=None,
@@ -688,7 +705,7 @@ def mlp_linear_bwd(dy, w, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, db
 
 def mlp_act_bwd_workspace_bytes(T: int, n: int) -> int:
     """Workspace of mlp_act_bwd with dbias (fewer rows may need more)."""
-    return load().mlp_act_bwd_workspace_bytes(T, n)
+    return load().mlp_act_bwd_workspace_bytes(*_sizes(T, n))
 
 
 def mlp_act_bwd(dy, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, dbias=None, a=None,

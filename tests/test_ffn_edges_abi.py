@@ -1,0 +1,35 @@
+"""Sizes at the edge of what the feed-forward operators' C interface can say, on
+the CPU: no call here launches a kernel."""
+import pytest
+import torch
+
+import mlp_step_gb300 as M
+from mlp_step_gb300 import build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return M.load()
+
+
+def test_binding_refuses_sizes_past_32_bits(lib):
+    """Pitches and row counts that a 32-bit int cannot hold are refused: passed
+    on by their low bits, 2^32 + 8 would be read as rows 8 values apart."""
+    e = lambda *a: torch.empty_strided(*a, dtype=torch.bfloat16, device="meta")  # noqa: E731
+    for pitch in (1 << 31, (1 << 32) + 8):
+        with pytest.raises(ValueError, match="pitches"):
+            M._mat(e((2, 8), (pitch, 1)), "x", 2, 8, -1)
+    with pytest.raises(ValueError, match="pitches"):
+        M._mat(e(((1 << 32) + 5, 1), (1, 1)), "x", (1 << 32) + 5, 1, -1)
+    assert M._mat(e((2, 8), ((1 << 31) - 1, 1)), "x", 2, 8, -1)[1] == (1 << 31) - 1
+    # a single row's pitch is never used
+    assert M._mat(e((1, 8), (1 << 33, 1)), "x", 1, 8, -1)[1] == 16
+    big = (1 << 32) + 32
+    for f in (lambda: M.mlp_ckpt8_scale_cols(big), lambda: M.mlp_layernorm_workspace_bytes(big, 64),
+              lambda: M.mlp_linear_workspace_bytes(64, big, 64, torch.float32),
+              lambda: M.mlp_linear_bwd_workspace_bytes(64, 64, big, torch.float32),
+              lambda: M.mlp_act_bwd_workspace_bytes(big, 64),
+              lambda: M.mlp_stack_ckpt8_workspace_bytes(2, big, 512, 512)):
+        with pytest.raises(ValueError, match="at most"):
+            f()
