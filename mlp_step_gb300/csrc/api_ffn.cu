@@ -21,7 +21,12 @@ bool known_act(int act) { return act >= MLP_ACT_NONE && act <= MLP_ACT_SILU; }
 constexpr int kMaxWidth = 65536;    // layer-norm rows
 constexpr int kMaxLinear = 1 << 24; // widths of linear layers
 
-int scale_cols(int cols) { return (cols + kCkptGroup - 1) / kCkptGroup; }
+int scale_cols(int cols) { return (cols - 1) / kCkptGroup + 1; }  // cols >= 1
+
+// Widths that the entry points take; a size query for others is 0.
+bool linear_widths(int d_in, int d_out) {
+  return d_in > 0 && d_in <= kMaxLinear && d_out > 0 && d_out <= kMaxLinear;
+}
 
 // A checkpoint argument pair: both given with pitches that hold `cols`
 // columns, or neither.
@@ -209,7 +214,7 @@ mlp_status check_linear(int T, int d_in, int d_out, int dtype, int out_dtype, in
 extern "C" {
 
 size_t mlp_linear_workspace_bytes(int T, int d_in, int d_out, int dtype) {
-  if (T <= 0 || d_in <= 0 || d_out <= 0 || !float_dtype(dtype)) return 0;
+  if (T <= 0 || !linear_widths(d_in, d_out) || !float_dtype(dtype)) return 0;
   return linear_path(T, d_in, d_out, dtype, false).sums;
 }
 
@@ -245,7 +250,7 @@ mlp_status mlp_linear_fwd(const void* x, int ldx, const void* w, int ldw, int T,
 }
 
 size_t mlp_linear_bwd_workspace_bytes(int T, int d_in, int d_out, int dtype) {
-  if (T <= 0 || d_in <= 0 || d_out <= 0 || !float_dtype(dtype)) return 0;
+  if (T <= 0 || !linear_widths(d_in, d_out) || !float_dtype(dtype)) return 0;
   const LinearPath lp = linear_path(T, d_out, d_in, dtype, true);
   return lp.sums + lp.part;
 }
@@ -284,7 +289,7 @@ mlp_status mlp_linear_bwd(const void* dy, int lddy, const void* w, int ldw, int 
 }
 
 size_t mlp_act_bwd_workspace_bytes(int T, int n) {
-  if (T <= 0 || n <= 0) return 0;
+  if (T <= 0 || !linear_widths(n, n)) return 0;
   const int rows = act_part_rows(T, n);
   return align256((size_t)(((long long)T + rows - 1) / rows) * ((n + 31) / 32 * 32) * 4);
 }

@@ -33,3 +33,23 @@ def test_binding_refuses_sizes_past_32_bits(lib):
               lambda: M.mlp_stack_ckpt8_workspace_bytes(2, big, 512, 512)):
         with pytest.raises(ValueError, match="at most"):
             f()
+
+
+def test_size_queries_beyond_the_widths(lib):
+    """No arithmetic of a size query overflows: widths that the calls refuse need
+    no workspace, and an INT_MAX columns' scale bytes are counted."""
+    most, wide = (1 << 31) - 1, (1 << 24) + 1
+    assert M.mlp_ckpt8_scale_cols(most) == 1 << 26
+    assert M.mlp_ckpt8_scale_cols(most - 31) == (1 << 26) - 1
+    for n in (wide, most):
+        for dt in (torch.bfloat16, torch.float32):
+            assert M.mlp_linear_workspace_bytes(64, n, 64, dt) == 0
+            assert M.mlp_linear_workspace_bytes(64, 64, n, dt) == 0
+            assert M.mlp_linear_bwd_workspace_bytes(64, n, 64, dt) == 0
+            assert M.mlp_linear_bwd_workspace_bytes(64, 64, n, dt) == 0
+        assert M.mlp_act_bwd_workspace_bytes(64, n) == 0
+    # the widest that are taken
+    w = 1 << 24
+    assert M.mlp_act_bwd_workspace_bytes(64, w) == 2 * w * 4
+    assert M.mlp_linear_workspace_bytes(64, 64, w, torch.float32) == 64 * w * 4
+    assert M.mlp_linear_bwd_workspace_bytes(most, w, 64, torch.float32) > most * w * 4
