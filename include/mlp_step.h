@@ -68,7 +68,8 @@ typedef int mlp_status;
                                         linear layers' activations (mlp_gemm and
                                         mlp_create take NONE and RELU)               */
 #define MLP_ACT_GELU_TANH 4          /* u (1 + tanh(sqrt(2/pi)(u + 0.044715 u^3)))/2  */
-#define MLP_ACT_SILU 5               /* u / (1 + exp(-u))                            */
+#define MLP_ACT_SILU 5               /* u / (1 + exp(-u)); of an infinite u, all of
+                                        them and their derivatives give their limits */
 
 #define MLP_PREC_FP32 0              /* fp32 operands, fp32 SIMT kernels             */
 #define MLP_PREC_BF16 1              /* bf16 operands, fp32 accumulation in tensor

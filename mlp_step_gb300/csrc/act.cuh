@@ -44,7 +44,7 @@ __device__ __forceinline__ F2 sigmoid2(F2 z) {
   return f2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
-// Of c = min(|u|, 14): Phi(-c) and the Gaussian e^(-c^2 / 2).
+// Of c = min(|u|, 15): Phi(-c) and the Gaussian e^(-c^2 / 2).
 __device__ __forceinline__ F2 normal_tail2(F2 c, F2& gauss) {
   const F2 e = mul2(mul2(c, c), f2(-0.72134752044448170f));  // log2(e) / 2
   gauss = f2(ex2_fast(e.x), ex2_fast(e.y));
@@ -60,10 +60,16 @@ __device__ __forceinline__ F2 normal_tail2(F2 c, F2& gauss) {
 
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
-// Arguments beyond which the bell-shaped parts are below the smallest fp32:
-// they are evaluated there instead, so that an infinite u gives the limits 0
-// and 1 rather than 0 times infinity.
-constexpr float kGaussEnd = 14.f, kLogisticEnd = 104.f;
+// Arguments beyond which the bell-shaped parts, Phi(-|u|) and the logistic
+// function of -|u| are 0 in fp32: they are evaluated there instead, and the
+// factor u that multiplies them is held there from below, so that an infinite u
+// gives f and f' their limits rather than 0 times infinity.
+constexpr float kGaussEnd = 15.f, kLogisticEnd = 104.f;
+
+// max(u, -limit) of two values; what multiplies it is NaN where u is
+__device__ __forceinline__ F2 above2(F2 u, float limit) {
+  return f2(fmaxf(u.x, -limit), fmaxf(u.y, -limit));
+}
 
 // f(u) of activation ACT for two values.
 template <int ACT>
@@ -82,9 +88,9 @@ __device__ __forceinline__ F2 act_value2(F2 u, float slope) {
     return f2(fmaf(-c.x, tail.x, fmaxf(u.x, 0.f)), fmaf(-c.y, tail.y, fmaxf(u.y, 0.f)));
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
     const F2 k = fma2(mul2(u, u), f2(kTanhScale * kTanhCubic), f2(kTanhScale));
-    return mul2(u, sigmoid2(mul2(u, k)));
+    return mul2(above2(u, kGaussEnd), sigmoid2(mul2(u, k)));
   } else if constexpr (ACT == MLP_ACT_SILU) {
-    return mul2(u, sigmoid2(u));
+    return mul2(above2(u, kLogisticEnd), sigmoid2(u));
   } else {
     return u;
   }
@@ -115,7 +121,7 @@ __device__ __forceinline__ F2 act_grad2(F2 u, float slope, F2& value) {
                     copysignf(abs_upto(u.y, kGaussEnd), u.y));
     const F2 c2 = mul2(mul2(c, c), f2(kTanhCubic));
     const F2 s = sigmoid2(mul2(mul2(c, f2(kTanhScale)), add2(c2, f2(1.f))));
-    value = mul2(u, s);
+    value = mul2(above2(u, kGaussEnd), s);
     const F2 w = fma2(c2, f2(3.f * kTanhScale), f2(kTanhScale));
     const F2 b = mul2(mul2(c, s), fma2(s, f2(-1.f), f2(1.f)));
     return fma2(b, w, s);
@@ -123,7 +129,7 @@ __device__ __forceinline__ F2 act_grad2(F2 u, float slope, F2& value) {
     const F2 c = f2(copysignf(abs_upto(u.x, kLogisticEnd), u.x),
                     copysignf(abs_upto(u.y, kLogisticEnd), u.y));
     const F2 s = sigmoid2(c);
-    value = mul2(u, s);
+    value = mul2(above2(u, kLogisticEnd), s);
     return fma2(mul2(c, s), fma2(s, f2(-1.f), f2(1.f)), s);
   } else {
     value = u;
@@ -139,11 +145,12 @@ __device__ __forceinline__ float act_value_of(float u, float slope) {
   if constexpr (!ACC || ACT <= MLP_ACT_LEAKY_RELU_SQ) {
     return act_value2<ACT>(f2(u), slope).x;
   } else if constexpr (ACT == MLP_ACT_GELU) {
-    return u * 0.5f * erfcf(-0.70710678118654752f * u);
+    return fmaxf(u, -kGaussEnd) * 0.5f * erfcf(-0.70710678118654752f * u);
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
-    return __fdividef(u, 1.f + expf(-kTanhScale * fmaf(kTanhCubic * u * u, u, u)));
+    return __fdividef(fmaxf(u, -kGaussEnd),
+                      1.f + expf(-kTanhScale * fmaf(kTanhCubic * u * u, u, u)));
   } else {
-    return __fdividef(u, 1.f + expf(-u));
+    return __fdividef(fmaxf(u, -kLogisticEnd), 1.f + expf(-u));
   }
 }
 
@@ -158,18 +165,18 @@ __device__ __forceinline__ float act_grad_of(float u, float slope, float& value)
   } else if constexpr (ACT == MLP_ACT_GELU) {
     const float c = copysignf(abs_upto(u, kGaussEnd), u);
     const float phi = 0.5f * erfcf(-0.70710678118654752f * c);
-    value = u * phi;
+    value = fmaxf(u, -kGaussEnd) * phi;
     return fmaf(0.3989422804014327f * c, expf(-0.5f * c * c), phi);
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
     const float c = copysignf(abs_upto(u, kGaussEnd), u);
     const float c2 = kTanhCubic * c * c;
     const float s = __fdividef(1.f, 1.f + expf(-kTanhScale * fmaf(c2, c, c)));
-    value = u * s;
+    value = fmaxf(u, -kGaussEnd) * s;
     return fmaf(c * s * (1.f - s), kTanhScale * fmaf(3.f, c2, 1.f), s);
   } else {
     const float c = copysignf(abs_upto(u, kLogisticEnd), u);
     const float s = __fdividef(1.f, 1.f + expf(-c));
-    value = u * s;
+    value = fmaxf(u, -kLogisticEnd) * s;
     return fmaf(c * s, 1.f - s, s);
   }
 }
