@@ -5,14 +5,20 @@
 //   MLP_ACT_GELU_TANH       u (1 + tanh z) / 2 = u / (1 + e^(-2z)),
 //                           z = sqrt(2 / pi) (u + 0.044715 u^3)
 //   MLP_ACT_SILU            u / (1 + e^(-u))
-// ACC = true (fp32 layers) uses the CUDA library's functions (and its two-ulp
-// division).  ACC = false
-// (16-bit layers, where the activation's instructions bound the epilogue of
-// short-K products) works on two values at a time with the packed fp32
-// instructions, the hardware exponential and reciprocal (a few 2^-23
-// relative) and, for Phi, the rational approximation 7.1.26 of Abramowitz and
-// Stegun, "Handbook of Mathematical Functions" (absolute error 1.5e-7 of
-// erfc): all below the rounding of 16-bit outputs.
+// ACC = true (fp32 layers) uses the CUDA library's functions and its two-ulp
+// division (whose quotients read as 0 below about 2^-118).  ACC = false (16-bit
+// layers, where the activation's instructions bound the epilogue of short-K
+// products) works on two values at a time with the packed fp32 instructions,
+// the hardware exponential and reciprocal and, for Phi, a polynomial.
+//
+// Error of the ACC = false forms, relative to the value itself for f and to the
+// sum of magnitudes of its two terms for f' (Phi and u phi; s and u s (1 - s)
+// z'): for GELU below 0, 4e-6 + u^2 2^-24; for the logistic ones (4 |z| + 16)
+// 2^-23, z the exponential's argument: 5e-5 at most, near 1e-36, and 5e-6 at
+// 1e-4.  Above 0, where values are of the order of 1 and u, 3e-7 of 1 + |u|
+// (f' of the tanh form up to 5e-6: 1 - s, good to 2^-23, times u z').  Half a
+// step of a 16-bit output is 2e-4 (fp16) or more; an fp32 output of a 16-bit
+// layer carries these errors.  Values below 2^-120 may read as 0.
 #pragma once
 
 #include "f32x2.cuh"
@@ -44,17 +50,27 @@ __device__ __forceinline__ F2 sigmoid2(F2 z) {
   return f2(rcp_fast(d.x), rcp_fast(d.y));
 }
 
-// Of c = min(|u|, 15): Phi(-c) and the Gaussian e^(-c^2 / 2).
+// Of c = min(|u|, 15): -Phi(-c) and the Gaussian g = e^(-c^2 / 2).  Phi(-c) / g
+// falls smoothly from 1/2 to 0.028 at c = 14 (g is 0 from 13.3 on); it is a
+// polynomial of degree 7 in t = 1 / (1 + 0.35 c) without a constant term: a
+// minimax fit, by linear programming, of its error relative to the ratio,
+// weighted so that Phi(-c) is also within 4.2e-8 (2.7e-6 of the ratio, 8.4e-8
+// near c = 0), coefficients rounded to fp32.  With the sign turned, u Phi(u) =
+// max(u, 0) + c (-Phi(-c)) is one packed instruction.  (Approximation 7.1.26 of
+// Abramowitz and Stegun, two terms shorter, bounds the absolute error only: f'
+// was 68 % off at u = -6 and f 1 % at -8, in 159 instead of 163 us for the
+// backward of 65,536 x 512 -> 1,536 from 8-bit pre-activations.)
 __device__ __forceinline__ F2 normal_tail2(F2 c, F2& gauss) {
   const F2 e = mul2(mul2(c, c), f2(-0.72134752044448170f));  // log2(e) / 2
   gauss = f2(ex2_fast(e.x), ex2_fast(e.y));
-  const F2 d = fma2(c, f2(0.23164188827f), f2(1.f));  // 0.3275911 / sqrt 2
+  const F2 d = fma2(c, f2(0.35f), f2(1.f));
   const F2 t = f2(rcp_fast(d.x), rcp_fast(d.y));
-  // half of a5 .. a1
-  F2 p = fma2(f2(0.5307027145f), t, f2(-0.7265760135f));
-  p = fma2(p, t, f2(0.7107068705f));
-  p = fma2(p, t, f2(-0.142248368f));
-  p = fma2(p, t, f2(0.127414796f));
+  F2 p = fma2(f2(-0.0449843592941761f), t, f2(0.18593889474868774f));
+  p = fma2(p, t, f2(-0.21355803310871124f));
+  p = fma2(p, t, f2(-0.0068651409819722176f));
+  p = fma2(p, t, f2(-0.1440645009279251f));
+  p = fma2(p, t, f2(-0.1366742104291916f));
+  p = fma2(p, t, f2(-0.13979268074035645f));
   return mul2(mul2(p, t), gauss);
 }
 
@@ -85,7 +101,7 @@ __device__ __forceinline__ F2 act_value2(F2 u, float slope) {
     const F2 c = f2(abs_upto(u.x, kGaussEnd), abs_upto(u.y, kGaussEnd));
     F2 g;
     const F2 tail = normal_tail2(c, g);
-    return f2(fmaf(-c.x, tail.x, fmaxf(u.x, 0.f)), fmaf(-c.y, tail.y, fmaxf(u.y, 0.f)));
+    return fma2(c, tail, f2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
     const F2 k = fma2(mul2(u, u), f2(kTanhScale * kTanhCubic), f2(kTanhScale));
     return mul2(above2(u, kGaussEnd), sigmoid2(mul2(u, k)));
@@ -111,11 +127,12 @@ __device__ __forceinline__ F2 act_grad2(F2 u, float slope, F2& value) {
     const F2 c = f2(abs_upto(u.x, kGaussEnd), abs_upto(u.y, kGaussEnd));
     F2 g;
     const F2 tail = normal_tail2(c, g);
-    value = f2(fmaf(-c.x, tail.x, fmaxf(u.x, 0.f)), fmaf(-c.y, tail.y, fmaxf(u.y, 0.f)));
-    // f' = Phi(u) + u phi(u); for u < 0 it is 1 - f'(-u), and with
-    // s = 1/2 - (Phi(-c) - c phi(c)) it is 1/2 +- s
-    const F2 q = fma2(mul2(c, f2(0.3989422804014327f)), g, f2(0.5f));
-    return f2(0.5f + copysignf(q.x - tail.x, u.x), 0.5f + copysignf(q.y - tail.y, u.y));
+    value = fma2(c, tail, f2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
+    // f' = Phi(u) + u phi(u): below 0 that is Phi(-c) - c phi(c), here -d, as it
+    // is (no detour over 1, which would leave steps of 2^-24), above it 1 + d
+    const F2 d = fma2(mul2(c, f2(0.3989422804014327f)), g, tail);
+    const F2 r = add2(d, f2(1.f));
+    return f2(u.x < 0.f ? -d.x : r.x, u.y < 0.f ? -d.y : r.y);
   } else if constexpr (ACT == MLP_ACT_GELU_TANH) {
     const F2 c = f2(copysignf(abs_upto(u.x, kGaussEnd), u.x),
                     copysignf(abs_upto(u.y, kGaussEnd), u.y));

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import mlp_step_gb300 as M
-from test_gpu_ffn import ACTS, BF16, F16, F32, SLOPE, Guarded, rnd
+from test_gpu_ffn import ACTS, BF16, F16, F32, SLOPE, Guarded, near, rnd, rounding
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +86,104 @@ def test_activation_values_at_their_limits(act, dtype):
         ws = bytes_for(M.mlp_linear_bwd_workspace_bytes(T, n, k, dtype))
         M.mlp_linear_bwd(dy[:, :k], wt[:, :k], du.v, act=ACTS[act], slope=SLOPE, u=us, a=a.v, workspace=ws)
         check_limits(a.v, u, act, ("a", T))
+
+
+def act_terms(u, act):
+    """f(u), its derivative, the sum of magnitudes of the derivative's two terms,
+    and the argument of the exponential in it, in 64 bits."""
+    if act == "gelu":
+        p = torch.special.erfc(-u / math.sqrt(2)) / 2
+        b = u * torch.exp(-u * u / 2) / math.sqrt(2 * math.pi)
+        return u * p, p + b, p + b.abs(), u * u / 2
+    if act == "gelu_tanh":
+        c = 2 * math.sqrt(2 / math.pi)
+        z, dz = c * (u + 0.044715 * u ** 3), c * (1 + 3 * 0.044715 * u * u)
+    else:
+        z, dz = u, torch.ones_like(u)
+    s = 1 / (1 + torch.exp(-z))
+    b = u * s / (1 + torch.exp(z)) * dz
+    return u * s, s + b, s + b.abs(), z
+
+
+def act_error(u, act, fp32):
+    """Relative error of f(u), and of f'(u) against its two terms."""
+    z = act_terms(u, act)[3].abs()
+    if fp32:
+        # the argument is off by two roundings (four for the cubic), which the
+        # exponential turns into |z| times as much (erfc of u / sqrt 2 into
+        # u^2 = 2 z); the functions are good to 4 ulp, the division to 2, and
+        # some roundings of products and sums
+        return (8 * z + 20) * 2.0 ** -24
+    if act == "gelu":
+        # the polynomial's 2.7e-6 with the functions' few 2^-23, and the
+        # exponent u^2 / 2 after two roundings
+        return 4e-6 + u * u * 2.0 ** -24
+    # the exponent's four roundings, the hardware functions' few 2^-23
+    return (4 * z + 16) * 2.0 ** -23
+
+
+# what reads as 0: the fast division's quotients by more than 2^126 (times |u|),
+# subnormal results of the hardware exponential
+LOST = 2.0 ** -118
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_activation_tails(act, dtype):
+    """f and f' of negative pre-activations are as exact relative to their own
+    (small) values as they are near 0: in outputs of the operand type, and in fp32 ones
+    of a 16-bit layer."""
+    n = 2048
+    u = torch.linspace(-1, 0, n, device="cuda") * (40 if act == "silu" else 12)
+    u = torch.stack([u, u.flip(0) * 0.37]).to(dtype)
+    ud = u.double()
+    f, df, terms, _ = act_terms(ud, act)
+    e = act_error(ud, act, dtype == F32)
+    du, a = torch.empty_like(u), torch.empty_like(u)
+    M.mlp_act_bwd(torch.ones_like(u), du, act=ACTS[act], u=u, a=a)
+    # (the error comes before the rounding: both, and the error's own rounding)
+    r = lambda ref, err, t: rounding(t, ref) * (1 + 1e-3) + err + LOST  # noqa: E731
+    near(a, f, r(f, e * f.abs(), dtype), "f")
+    near(du, df, r(df, e * terms, dtype), "f'")
+    # a product that gives u (forward) or 1 (backward) exactly, fp32 outputs:
+    # few rows, single tiles, pairs
+    for T in (2, 200, 4100):
+        x = torch.zeros(T, 8, dtype=dtype, device="cuda")
+        x[::2, 0], x[1::2, 1] = 1, 1
+        w = torch.zeros(8, n, dtype=dtype, device="cuda")
+        w[:2] = u
+        rows = torch.arange(T, device="cuda") % 2
+        ws = bytes_for(M.mlp_linear_workspace_bytes(T, 8, n, dtype))
+        for odt in {F32, dtype}:
+            y = torch.empty(T, n, dtype=odt, device="cuda")
+            M.mlp_linear_fwd(x, w, y, act=ACTS[act], workspace=ws)
+            near(y, f[rows], r(f, e * f.abs(), odt)[rows], ("y", T, odt))
+        one = torch.ones(n, 8, dtype=dtype, device="cuda")
+        us = u[rows].contiguous()
+        ws = bytes_for(M.mlp_linear_bwd_workspace_bytes(T, n, 8, dtype))
+        for odt in {F32, dtype}:
+            g = torch.empty(T, n, dtype=odt, device="cuda")
+            a = torch.empty(T, n, dtype=dtype, device="cuda")
+            M.mlp_linear_bwd(x, one, g, act=ACTS[act], u=us, a=a, workspace=ws)
+            near(g, df[rows], r(df, e * terms, odt)[rows], ("du", T, odt))
+            near(a, f[rows], r(f, e * f.abs(), dtype)[rows], ("a", T, odt))
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_activations_above_zero(act, dtype):
+    """Beside 0 and above it errors are absolute: 3e-7 of 1 + |u|.  (The tanh
+    form's f' = s + u s (1 - s) z' has u z' of up to 38 beside 1 - s, which is
+    off by the 2 ulp of s, 2^-23, until s is 1 for z above 24 ln 2 = 16.7.)"""
+    u = torch.linspace(-1, 30, 4096, device="cuda").view(1, -1).to(dtype)
+    f, df, _, _ = act_terms(u.double(), act)
+    du, a = torch.empty_like(u), torch.empty_like(u)
+    M.mlp_act_bwd(torch.ones_like(u), du, act=ACTS[act], u=u, a=a)
+    e = 3e-7 * (1 + u.double().abs())
+    near(a, f, rounding(dtype, f) * (1 + 1e-3) + e, "f")
+    if act == "gelu_tanh":
+        ud = u.double()
+        dz = 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * ud * ud)
+        z = act_terms(ud, act)[3]
+        e = e + ud.abs() * dz * torch.where(z < 18, 2.0 ** -23, torch.exp(-z))
+    near(du, df, rounding(dtype, df) * (1 + 1e-3) + e, "f'")
