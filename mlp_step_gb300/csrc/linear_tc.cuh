@@ -459,6 +459,10 @@ __device__ __forceinline__ void linear_body(const LinMaps& maps, const LinParams
         }
       }
       if (tma_in) {
+        // A unit that left by the warp's own copy wrote the box with ordinary
+        // stores; each lane orders its own before the copy's writes.  (Whole
+        // pieces always leave by TMA, behind the fence before that store.)
+        if (!WHOLE) ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
           ptx::mbar_arrive_expect_tx(&in_full[ew], kBox);

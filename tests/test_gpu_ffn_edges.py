@@ -187,3 +187,41 @@ def test_activations_above_zero(act, dtype):
         z = act_terms(ud, act)[3]
         e = e + ud.abs() * dz * torch.where(z < 18, 2.0 ** -23, torch.exp(-z))
     near(du, df, rounding(dtype, df) * (1 + 1e-3) + e, "f'")
+
+
+# ------------------------------------------------------------ mixed pitches
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,k,n", [(200, 520, 200), (1500, 520, 1001), (2000, 72, 2000),
+                                   (4100, 200, 776), (3300, 1160, 1088)])
+def test_linear_input_by_tma_output_by_copies(T, k, n, dtype):
+    """A residual (u) that TMA brings into the box of a unit whose output leaves
+    by the warp's own copies, its rows at an odd pitch or its last columns ragged:
+    the same bits as where all of them are moved value by value."""
+    x, w, bias = rnd(4, T, k, dtype), rnd(5, k, n, dtype, std=k ** -0.5), torch.randn(n, device="cuda")
+    wt = rnd(6, n, k, dtype)
+    wt.copy_(w.t())
+    r, u = rnd(7, T, n, dtype), rnd(8, T, n, dtype, std=1.5)
+    odd = [rnd(9, T, n, dtype, pitch=n + 1) for _ in range(2)]
+    odd[0].copy_(r)
+    odd[1].copy_(u)
+    ws = bytes_for(max(M.mlp_linear_workspace_bytes(T, k, n, dtype),
+                       M.mlp_linear_bwd_workspace_bytes(T, n, k, dtype)))
+    got = []
+    for res, saved, pitch in ((odd[0], odd[1], n + 1), (r, u, n + 1), (r, u, None)):
+        y, du = Guarded(T, n, dtype, pitch), Guarded(T, n, dtype, pitch)
+        db = torch.empty(n, device="cuda")
+        for _ in range(3):  # the same again, over itself
+            M.mlp_linear_fwd(x, w, y.v, bias=bias, act=M.MLP_ACT_RELU, residual=res, workspace=ws)
+            M.mlp_linear_bwd(x, wt, du.v, act=M.MLP_ACT_RELU, u=saved, dbias=db, workspace=ws)
+        assert y.intact() and du.intact()
+        got.append((y.v, du.v, db))
+    for a in got[1:]:
+        assert all(torch.equal(p, q) for p, q in zip(got[0], a))
+    # and of the formula: a term's rounding in fp32 each, then one to 16 bits
+    ru = x.double() @ w.double()
+    e = (k + 8) * 2.0 ** -23 * (x.double().abs() @ w.double().abs())
+    ref = (ru + bias.double()).clamp(min=0) + r.double()
+    near(got[0][0], ref, rounding(dtype, ref) + e + 2.0 ** -22 * (ref.abs() + bias.double().abs()), "y")
+    ref = ru * (u.double() > 0)
+    near(got[0][1], ref, rounding(dtype, ref) + e + 1e-30, "du")
