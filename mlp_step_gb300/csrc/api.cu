@@ -41,12 +41,11 @@ int* device_error_word() {
 // Programmatic dependent launch is on unless MLP_STEP_PDL=0 is set in the
 // environment (read once).
 bool pdl_enabled() {
-  static int on = -1;
-  if (on < 0) {
+  static const bool on = [] {
     const char* e = getenv("MLP_STEP_PDL");
-    on = (e && e[0] == '0') ? 0 : 1;
-  }
-  return on == 1;
+    return !(e && e[0] == '0');
+  }();
+  return on;
 }
 
 // ------------------------------------------------------------ bounded waits

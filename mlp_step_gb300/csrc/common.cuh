@@ -10,6 +10,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/mlp_step.h"
+#include "per_device.cuh"
 
 namespace mlp {
 
@@ -117,15 +118,53 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+inline int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
 inline int num_sms() {
-  static int n = 0;
-  if (n == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
+  static PerDevice sms;
+  const int dev = current_device();
+  return sms.get(dev, [dev] {
+    int n = 0;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    if (n <= 0) n = 1;
-  }
-  return n;
+    return n > 0 ? n : 1;
+  });
+}
+
+// Lets a kernel use `smem` bytes of dynamic shared memory on the current
+// device; `done` is the launcher's.
+template <typename K>
+inline bool allow_smem(PerDevice& done, K* kernel, int smem) {
+  return done.get(current_device(), [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+                   cudaSuccess
+               ? 1
+               : 0;
+  }) > 0;
+}
+
+// The same for a kernel of CTA pairs, and the pairs that fit at once (a GPC
+// with an odd number of free SMs leaves one over); 0 where the attribute is
+// refused.
+template <typename K>
+inline int resident_pairs(PerDevice& done, K* kernel, int threads, int smem) {
+  return done.get(current_device(), [&] {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+        cudaSuccess)
+      return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (num_sms() / 2));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = num_sms() / 2;
+    }
+    return n;
+  });
 }
 
 // Translate the last launch error into a status.

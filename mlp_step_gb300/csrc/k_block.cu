@@ -887,24 +887,9 @@ __global__ void __launch_bounds__(256) rmsnorm_bwd_kernel(const __nv_bfloat16* _
 
 mlp_status launch_block_fwd(const void* x, const void* wg, const void* wd, int T, int hidden,
                             float eps, float slope, void* y, float* rstd, cudaStream_t st) {
-  static bool configured = false;
-  static int max_clusters = 0;
-  if (!configured) {
-    if (cudaFuncSetAttribute(block_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             F2_SMEM) != cudaSuccess)
-      return MLP_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(F2_THREADS);
-    cfg.dynamicSmemBytes = F2_SMEM;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, block_fwd_kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = num_sms() / 2;
-    }
-    max_clusters = n;
-    configured = true;
-  }
+  static PerDevice resident;
+  const int max_clusters = resident_pairs(resident, block_fwd_kernel, F2_THREADS, F2_SMEM);
+  if (max_clusters < 1) return MLP_ERR_CUDA;
   CUtensorMap tx, tg, td;
   if (!encode_tmap_bf16_2d(&tx, x, DM, T, DM * 2, 64, F2_TOK)) return MLP_ERR_CUDA;
   if (!encode_tmap_bf16_2d(&tg, wg, hidden, DM, (unsigned long long)hidden * 2, 64, 128))
@@ -933,24 +918,9 @@ mlp_status launch_block_fwd(const void* x, const void* wg, const void* wd, int T
 mlp_status launch_block_bwd_act(const void* x, const void* wg, const void* wd, const void* dy,
                                 const float* rstd, int T, int hidden, float slope, void* a_out,
                                 void* du_out, cudaStream_t st) {
-  static bool configured = false;
-  static int max_pairs = 0;
-  if (!configured) {
-    if (cudaFuncSetAttribute(block_bwd_act_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             B_SMEM) != cudaSuccess)
-      return MLP_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(B_THREADS);
-    cfg.dynamicSmemBytes = B_SMEM;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, block_bwd_act_kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = num_sms() / 2;
-    }
-    max_pairs = n;
-    configured = true;
-  }
+  static PerDevice resident;
+  const int max_pairs = resident_pairs(resident, block_bwd_act_kernel, B_THREADS, B_SMEM);
+  if (max_pairs < 1) return MLP_ERR_CUDA;
   CUtensorMap tx, tg, tdy, twd, ta, tdu;
   if (!encode_tmap_bf16_2d(&tx, x, DM, T, DM * 2, 64, TM)) return MLP_ERR_CUDA;
   if (!encode_tmap_bf16_2d(&tg, wg, hidden, DM, (unsigned long long)hidden * 2, 64, 64))

@@ -739,15 +739,10 @@ mlp_status launch_xent(const float* logits, int ldl, const int* labels, int B, i
   if (vec && blocks > num_sms() * 2) blocks = num_sms() * 2;
   {
   LaunchScope ls("xent", st, B, C);
-  static bool configured = false;
-  if (vec && !configured) {
-    if (cudaFuncSetAttribute(xent_rows_regs_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)xent_rows_smem<2>()) != cudaSuccess ||
-        cudaFuncSetAttribute(xent_rows_regs_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)xent_rows_smem<8>()) != cudaSuccess)
-      return MLP_ERR_CUDA;
-    configured = true;
-  }
+  static PerDevice configured[2];
+  if (vec && (!allow_smem(configured[0], xent_rows_regs_kernel<2>, (int)xent_rows_smem<2>()) ||
+              !allow_smem(configured[1], xent_rows_regs_kernel<8>, (int)xent_rows_smem<8>())))
+    return MLP_ERR_CUDA;
   const unsigned long long wait_ns = wait_limit_ns();
   if (vec && C <= 256)
     launch_k(xent_rows_regs_kernel<2>, dim3(blocks), dim3(256), xent_rows_smem<2>(), st, logits,

@@ -1793,13 +1793,8 @@ template <int BN, int STAGES, int H16>
 mlp_status launch_bn(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                      const TcParams& p, cudaStream_t st) {
   using L = Layout<BN, STAGES>;
-  static bool configured = false;
-  if (!configured) {
-    if (cudaFuncSetAttribute(tc_gemm_kernel<BN, STAGES, H16>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-      return MLP_ERR_CUDA;
-    configured = true;
-  }
+  static PerDevice configured;
+  if (!allow_smem(configured, tc_gemm_kernel<BN, STAGES, H16>, L::SMEM)) return MLP_ERR_CUDA;
   const int units = p.num_tiles * p.splits;
   int grid = units < num_sms() ? units : num_sms();
   {
@@ -1828,27 +1823,10 @@ mlp_status launch_pair(const CUtensorMap& ta, const CUtensorMap& tb, const CUten
                        const TcParams& p, cudaStream_t st, const AttnEpi& ae = AttnEpi{}) {
   using L = PairLayout<STAGES, EPI, BRES>;
   static_assert(L::SMEM <= 232448, "pair kernel shared memory");
-  static bool configured = false;
-  static int max_pairs = 0;
-  if (!configured) {
-    if (cudaFuncSetAttribute(tc_gemm_pair_kernel<STAGES, H16, EPI, BRES>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
-      return MLP_ERR_CUDA;
-    // pairs that fit at once (a GPC with an odd number of free SMs leaves one over)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(kPairThreads);
-    cfg.dynamicSmemBytes = L::SMEM;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, tc_gemm_pair_kernel<STAGES, H16, EPI, BRES>, &cfg) !=
-            cudaSuccess ||
-        n < 1) {
-      cudaGetLastError();
-      n = num_sms() / 2;
-    }
-    max_pairs = n;
-    configured = true;
-  }
+  static PerDevice resident;
+  const int max_pairs = resident_pairs(resident, tc_gemm_pair_kernel<STAGES, H16, EPI, BRES>,
+                                       kPairThreads, L::SMEM);
+  if (max_pairs < 1) return MLP_ERR_CUDA;
   const int units = p.num_tiles * p.splits;
   const int pairs = units < max_pairs ? units : max_pairs;
   {
@@ -1994,16 +1972,13 @@ bool step_gemm_supported(const GemmArgs& g) {
 mlp_status launch_step_program(const StepSpec& s, unsigned* bar_words, unsigned long long wait_ns,
                                cudaStream_t st) {
   using L = Layout<STEP_BN, STEP_STAGES>;
-  static bool configured[2] = {false, false};
+  static PerDevice configured[2];
   const int h16 = s.f16 ? 1 : 0;
-  if (!configured[h16]) {
-    if (cudaFuncSetAttribute(h16 ? tc_step_kernel<STEP_BN, STEP_STAGES, 1>
-                                 : tc_step_kernel<STEP_BN, STEP_STAGES, 0>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             L::SMEM + STEP_SGD_BYTES) != cudaSuccess)
-      return MLP_ERR_CUDA;
-    configured[h16] = true;
-  }
+  if (!allow_smem(configured[h16],
+                  h16 ? tc_step_kernel<STEP_BN, STEP_STAGES, 1>
+                      : tc_step_kernel<STEP_BN, STEP_STAGES, 0>,
+                  L::SMEM + STEP_SGD_BYTES))
+    return MLP_ERR_CUDA;
   if (s.n_gemm < 0 || s.n_gemm > kStepMaxGemms || !bar_words) return MLP_ERR_INVALID_ARG;
   StepProgram prog;  // ~12 KiB of kernel parameters
   memset(&prog, 0, sizeof(prog));

@@ -537,25 +537,25 @@ bool row_vec(const void* p, long long ld, int esz, int bytes) {
 // Blocks of a row-walking launch: as many as are resident at once (more would
 // run as a second, ragged wave), at most one per row set.
 template <typename K>
-int walk_blocks(K kernel, int threads, int* per_sm, long long T, int rows_per_block) {
-  if (*per_sm == 0) {
+int walk_blocks(K kernel, int threads, PerDevice& resident, long long T, int rows_per_block) {
+  const int per_sm = resident.get(current_device(), [&] {
     int n = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess) {
       cudaGetLastError();
       n = 1;
     }
-    *per_sm = n > 0 ? n : 1;
-  }
+    return n > 0 ? n : 1;
+  });
   const long long need = (T + rows_per_block - 1) / rows_per_block;
-  const long long most = (long long)num_sms() * *per_sm;
+  const long long most = (long long)num_sms() * per_sm;
   return (int)(need < most ? need : most);
 }
 
 template <typename T, int WPR, bool FULL>
 mlp_status fwd_held_of(const LayerNormFwd& p, cudaStream_t st) {
   using B = HeldBlock<WPR>;
-  static int per_sm = 0;
-  const int blocks = walk_blocks(ln_fwd_kernel<T, WPR, FULL>, B::THREADS, &per_sm, p.T, B::ROWS);
+  static PerDevice per_sm;
+  const int blocks = walk_blocks(ln_fwd_kernel<T, WPR, FULL>, B::THREADS, per_sm, p.T, B::ROWS);
   launch_k(ln_fwd_kernel<T, WPR, FULL>, dim3(blocks), dim3(B::THREADS), 0, st, p);
   return launch_status();
 }
@@ -578,8 +578,8 @@ mlp_status fwd_t(LayerNormFwd p, cudaStream_t st) {
   if (p.d <= 2048) return fwd_held<T, 4>(p, st);
   if (p.d <= 4096) return fwd_held<T, 8>(p, st);
   if (p.d <= kHeldWidth) return fwd_held<T, 16>(p, st);
-  static int per_sm = 0;
-  const int blocks = walk_blocks(ln_fwd_wide_kernel<T>, kLoopThreads, &per_sm, p.T, 1);
+  static PerDevice per_sm;
+  const int blocks = walk_blocks(ln_fwd_wide_kernel<T>, kLoopThreads, per_sm, p.T, 1);
   launch_k(ln_fwd_wide_kernel<T>, dim3(blocks), dim3(kLoopThreads), 0, st, p);
   return launch_status();
 }
@@ -600,9 +600,9 @@ int bwd_blocks(long long T, int d) {
 template <typename T, int WPR, bool CK, bool FULL>
 mlp_status bwd_held_of(const LayerNormBwd& p, int* blocks, cudaStream_t st) {
   using B = HeldBlock<WPR>;
-  static int per_sm = 0;
+  static PerDevice per_sm;
   const int resident =
-      walk_blocks(ln_bwd_kernel<T, WPR, CK, FULL>, B::THREADS, &per_sm, p.T, B::ROWS);
+      walk_blocks(ln_bwd_kernel<T, WPR, CK, FULL>, B::THREADS, per_sm, p.T, B::ROWS);
   if (resident < *blocks) *blocks = resident;
   const size_t smem = B::ROWS > 1 ? (size_t)32 * WPR * kPerThread * 4 : 0;
   LaunchScope ls("layernorm_bwd", st, p.T, p.d, sizeof(T));
@@ -635,9 +635,9 @@ mlp_status bwd_t(LayerNormBwd p, cudaStream_t st) {
   else {
     {
       LaunchScope ls("layernorm_bwd_wide", st, p.T, p.d, sizeof(T));
-      static int per_sm = 0;
+      static PerDevice per_sm;
       launch_k(ln_bwd_wide_kernel<T, CK>,
-               dim3(walk_blocks(ln_bwd_wide_kernel<T, CK>, kLoopThreads, &per_sm, p.T, 1)),
+               dim3(walk_blocks(ln_bwd_wide_kernel<T, CK>, kLoopThreads, per_sm, p.T, 1)),
                dim3(kLoopThreads), 0, st, p);
       MLP_CHECK(launch_status());
     }

@@ -93,9 +93,8 @@ template <int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
 mlp_status launch_single(const LinMaps& maps, const LinParams& p, cudaStream_t st) {
   using L = LinLayout<0, BN, STAGES, EW, AROWS>;
   auto kernel = linear_kernel<BN, STAGES, EW, AROWS, H16, MODE>;
-  static const cudaError_t configured =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
-  if (configured != cudaSuccess) return MLP_ERR_CUDA;
+  static PerDevice configured;
+  if (!allow_smem(configured, kernel, L::SMEM)) return MLP_ERR_CUDA;
   const int grid = p.units < num_sms() ? p.units : num_sms();
   LaunchScope ls(MODE != kFwd ? "linear_bwd" : "linear_fwd", st, p.a.T, p.a.N, p.a.K);
   launch_k(kernel, dim3(grid), dim3(L::THREADS), L::SMEM, st, maps, p);

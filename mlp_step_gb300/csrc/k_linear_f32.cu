@@ -208,12 +208,8 @@ mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st) {
   const int per = ((a.K + a.splits - 1) / a.splits + TK - 1) / TK * TK;
   const int w_vec = reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.ldw % 4 == 0;
   auto kernel = bwd ? linear_f32_kernel<true> : linear_f32_kernel<false>;
-  static const cudaError_t configured[2] = {
-      cudaFuncSetAttribute(linear_f32_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem),
-      cudaFuncSetAttribute(linear_f32_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmem)};
-  if (configured[0] != cudaSuccess || configured[1] != cudaSuccess) return MLP_ERR_CUDA;
+  static PerDevice configured[2];
+  if (!allow_smem(configured[bwd], kernel, kSmem)) return MLP_ERR_CUDA;
   LaunchScope ls(bwd ? "linear_bwd_f32" : "linear_fwd_f32", st, a.T, a.N, a.K);
   launch_k(kernel, grid, dim3(kThreads), kSmem, st, a, per, w_vec);
   return launch_status();

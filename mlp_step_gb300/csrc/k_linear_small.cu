@@ -600,10 +600,9 @@ __global__ void __launch_bounds__(kThreads, FewShape<MT, BWD, COLS>::kPerSm)
 template <typename T, int MT, bool BWD, int COLS>
 mlp_status few_launch(const LinearArgs& a, float* dbias, cudaStream_t st) {
   using Shape = FewShape<MT, BWD, COLS>;
-  static const cudaError_t configured =
-      cudaFuncSetAttribute(linear_few_kernel<T, MT, BWD, COLS>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
-  if (configured != cudaSuccess) return MLP_ERR_CUDA;
+  static PerDevice configured;
+  if (!allow_smem(configured, linear_few_kernel<T, MT, BWD, COLS>, Shape::kSmem))
+    return MLP_ERR_CUDA;
   // the widest cluster with which all CTAs are resident (on 152 SMs) and each
   // still has 128 of K
   const long long tiles = (a.N + COLS - 1) / COLS;

@@ -827,22 +827,8 @@ template <int STAGES, int EW, int H16, int MODE, int FORM>
 mlp_status launch_pair(const LinMaps& maps, const LinParams& p, cudaStream_t st) {
   using L = LinLayout<1, 256, STAGES, EW>;
   auto kernel = linear_pair_kernel<STAGES, EW, H16, MODE, FORM>;
-  // pairs that fit at once (a GPC with an odd number of free SMs leaves one over)
-  static const int max_pairs = [&] {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) !=
-        cudaSuccess)
-      return 0;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (num_sms() / 2));
-    cfg.blockDim = dim3(L::THREADS);
-    cfg.dynamicSmemBytes = L::SMEM;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = num_sms() / 2;
-    }
-    return n;
-  }();
+  static PerDevice resident;
+  const int max_pairs = resident_pairs(resident, kernel, L::THREADS, L::SMEM);
   if (max_pairs < 1) return MLP_ERR_CUDA;
   const int pairs = p.units < max_pairs ? p.units : max_pairs;
   LaunchScope ls(MODE != kFwd ? "linear_bwd_pair" : "linear_fwd_pair", st, p.a.T, p.a.N, p.a.K);
