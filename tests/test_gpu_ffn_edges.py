@@ -1,5 +1,6 @@
 """The feed-forward operators where values, pitches and callers are unusual."""
 import math
+import threading
 
 import pytest
 import torch
@@ -225,3 +226,75 @@ def test_linear_input_by_tma_output_by_copies(T, k, n, dtype):
     near(got[0][0], ref, rounding(dtype, ref) + e + 2.0 ** -22 * (ref.abs() + bias.double().abs()), "y")
     ref = ru * (u.double() > 0)
     near(got[0][1], ref, rounding(dtype, ref) + e + 1e-30, "du")
+
+
+# ------------------------------------------------------------ callers
+
+def test_host_threads_at_once():
+    """Calls from several host threads, each on a stream and a workspace of its
+    own: the bits of the same calls one after another."""
+    T, k, n = 96, 1040, 784
+    jobs = []
+    for i, dtype in enumerate((BF16, F16, F32, BF16, F16, F32)):
+        x, w = rnd(20 + i, T, k, dtype), rnd(30 + i, k, n, dtype, std=k ** -0.5)
+        o = [torch.empty(T, n, dtype=dtype, device="cuda") for _ in range(4)]
+        f = [torch.empty(z, device="cuda") for z in (T, T, n, n, n)]
+        ws = bytes_for(max(M.mlp_linear_workspace_bytes(T, k, n, dtype),
+                           M.mlp_layernorm_workspace_bytes(T, n),
+                           M.mlp_act_bwd_workspace_bytes(T, n)))
+        jobs.append((x, w, o, f, ws, torch.cuda.Stream()))
+
+    def one(x, w, o, f, ws, stream):
+        M.mlp_linear_fwd(x, w, o[0], act=M.MLP_ACT_GELU, workspace=ws, stream=stream)
+        M.mlp_layernorm_fwd(o[0], o[1], mean=f[0], rstd=f[1], stream=stream)
+        M.mlp_layernorm_bwd(o[1], f[0], f[1], o[2], f[2], f[3], ws, x=o[0], stream=stream)
+        M.mlp_act_bwd(o[2], o[3], act=M.MLP_ACT_SILU, u=o[0], dbias=f[4], workspace=ws,
+                      stream=stream)
+
+    def run(job):
+        with torch.cuda.device(0):
+            for _ in range(25):
+                one(*job)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=run, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    got = [[t.clone() for t in j[2] + j[3]] for j in jobs]
+    for j, g in zip(jobs, got):
+        for t in j[2] + j[3]:
+            t.fill_(math.nan)
+        torch.cuda.synchronize()
+        one(*j)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(j[2] + j[3], g))
+
+
+def test_host_thread_without_a_context():
+    """The first CUDA call of a host thread may be one of ours: products whose
+    tensor maps a driver call encodes work in it."""
+    T, k, n = 96, 1040, 784
+    x, w, c = rnd(40, T, k, BF16), rnd(41, k, n, BF16, std=k ** -0.5), torch.empty(T, n, device="cuda")
+    y = torch.empty(T, n, dtype=BF16, device="cuda")
+    ws = bytes_for(M.mlp_linear_workspace_bytes(T, k, n, BF16))
+    calls = [lambda: M.mlp_linear_fwd(x, w, y, workspace=ws), lambda: M.mlp_gemm(x, w, c, T, n, k)]
+    for call, out in zip(calls, (y, c)):
+        call()  # here first, so that nothing is left to set up
+        torch.cuda.synchronize()
+        want, raised = out.clone(), []
+        out.fill_(math.nan)
+        torch.cuda.synchronize()
+
+        def run():
+            try:
+                call()
+            except M.MlpError as e:
+                raised.append(e)
+        t = threading.Thread(target=run)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not raised and torch.equal(out, want)
