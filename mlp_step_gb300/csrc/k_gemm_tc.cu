@@ -68,7 +68,8 @@ struct TcParams {
   float sgd_lr, sgd_mom;
   __nv_bfloat16* sgd_shadow;
   int sgd_ld_shadow, sgd_shadow_rows;
-  int tma_store;  // epilogue writes C through the tmC tensor map
+  int tma_store;  // epilogue writes C through the tmC tensor map ...
+  int tma_cols;   // ... its 32-column boxes that start in [0, tma_cols) (0 without the map)
   int a_alt;      // step programs: odd steps read A through the alternate tensor map
 };
 
@@ -771,13 +772,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           } else if (p.xent_labels) {
             row_loss = xent_epilogue_row<H16>(p, m, r, p.xent_labels, p.xent_argmax);
-          } else if (!p.tma_store) {
+          } else if (n0 >= p.tma_cols) {
             float v[32];
             epilogue_values(p, m, n0, r, sb, mp, v);
             epilogue_store_regs<H16>(p, m, n0, v);
           }
         }
-        if (p.tma_store) {
+        if (n0 < p.tma_cols) {
           // all lanes take part: rows past M are staged too and clipped by TMA
           float v[32];
           epilogue_values(p, m, n0, r, sb, mp, v);
@@ -1603,7 +1604,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                   if (n0 + j < p.N) prow[j] = __uint_as_float(r[j]);
               }
             }
-          } else if (!p.tma_store) {
+          } else if (n0 >= p.tma_cols) {
             if (m < p.M) {
               float v[32];
               epilogue_values(p, m, n0, r, sb, mp, v);
@@ -1937,7 +1938,7 @@ mlp_status prepare_tc(const GemmArgs& g, int tiles_m, int BN, int splits, int kb
   p.sgd_shadow = g.sgd_shadow;
   p.sgd_ld_shadow = g.sgd_ld_shadow;
   p.sgd_shadow_rows = g.sgd_shadow_rows;
-  p.tma_store = 0;
+  p.tma_store = p.tma_cols = 0;
   if (p.xent_labels && (p.num_tiles != 1 || g.N > 32 || !p.xent_dlog || !p.xent_loss))
     return MLP_ERR_UNSUPPORTED_SHAPE;
   if ((p.xent_labels || p.sgd_w) && splits > 1) return MLP_ERR_UNSUPPORTED_SHAPE;
@@ -2130,7 +2131,10 @@ mlp_status launch_gemm_tc(const GemmArgs& g, unsigned long long wait_ns, cudaStr
 
   // Output through TMA stores when the output is large (for small outputs the
   // staging round trip costs more latency than it saves), rows are 16-byte
-  // aligned and no fused epilogue writes extra tensors.
+  // aligned and no fused epilogue writes extra tensors.  The stores write whole
+  // 16-byte pieces: where rows do not end on one, the last 32-column box goes
+  // from registers, because behind the last column lie the caller's values (or
+  // the column of ones of a layer's input).
   CUtensorMap tc;
   memset(&tc, 0, sizeof(tc));
   const int esz = g.c_bf16 ? 2 : 4;
@@ -2141,6 +2145,7 @@ mlp_status launch_gemm_tc(const GemmArgs& g, unsigned long long wait_ns, cudaStr
                             (unsigned long long)g.ldc * esz, 32, 32))
       return MLP_ERR_CUDA;
     p.tma_store = 1;
+    p.tma_cols = (long long)g.N * esz % 16 == 0 ? g.N : g.N / 32 * 32;
   }
   return p.f16 ? launch_tiles<1>(ta, tb, tc, p, pl.pair, BN, st)
                : launch_tiles<0>(ta, tb, tc, p, pl.pair, BN, st);

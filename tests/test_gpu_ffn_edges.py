@@ -298,3 +298,41 @@ def test_host_thread_without_a_context():
         t.join()
         torch.cuda.synchronize()
         assert not raised and torch.equal(out, want)
+
+
+# ------------------------------------------------------------ products with ragged rows
+
+@pytest.mark.parametrize("out", [F32, None])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("T,n,k", [(2048, 1001, 136), (1040, 1015, 64), (20000, 1004, 72)])
+def test_gemm_leaves_what_lies_behind_its_columns(T, n, k, dtype, out):
+    """mlp_gemm (the weight gradients of these layers) into wider rows: nothing
+    past the last column is written, and the values are the product's."""
+    x, w = rnd(50, T, k, dtype), rnd(51, k, n, dtype, std=k ** -0.5)
+    for pitch in (n, n + 3, 1024, 1032):
+        c = Guarded(T, n, out or dtype, pitch)
+        M.mlp_gemm(x, w, c.v, T, n, k)
+        ref = x.double() @ w.double()
+        e = (k + 8) * 2.0 ** -23 * (x.double().abs() @ w.double().abs())
+        near(c.v, ref, rounding(out or dtype, ref) + e, "c")
+        assert c.intact(), pitch
+
+
+@pytest.mark.parametrize("prec,dtype", [(M.MLP_PREC_BF16, BF16), (M.MLP_PREC_FP16, F16)])
+def test_bias_gradients_behind_odd_hidden_widths(prec, dtype):
+    """A hidden width that is no whole number of 16-byte pieces at a large batch:
+    the column of ones behind the layer's values, which gives the next layer's
+    bias gradient, stays."""
+    dims, batch = [64, 1001, 16], 2048
+    n = M.mlp_param_count(dims)
+    p0 = 0.05 * torch.randn(n, generator=torch.Generator().manual_seed(3))
+    net = M.MLP(dims, prec=prec, max_batch=batch, params=p0)
+    x = torch.rand(batch, 64, device="cuda")
+    dl = (0.01 * torch.randn(batch, 16, device="cuda")).to(dtype)
+    for _ in range(2):
+        net.forward(x, torch.empty(batch, 16, device="cuda"))
+        net.backward(dl, batch)
+    torch.cuda.synchronize()
+    db = net.grads[-16:].double()
+    ref = dl.double()  # summed in fp32
+    near(db, ref.sum(0), (batch + 8) * 2.0 ** -23 * ref.abs().sum(0), "db")
