@@ -72,11 +72,12 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float* part, int slot, 
   }
 }
 
-// N parameter values (fp32) from column c, `fill` past n values or without a vector.
+// N parameter values (fp32) from column c (a multiple of N), `fill` past n values
+// or without a vector.
 template <int N, bool FULL = false>
-__device__ __forceinline__ void load_param(const float* p, int c, int n, bool vec, float fill,
+__device__ __forceinline__ void load_param(const float* p, int c, int n, float fill,
                                            float (&v)[N]) {
-  if (p && (FULL ? n > 0 : vec && n >= N)) {
+  if (p && (FULL ? n > 0 : n >= N)) {
 #pragma unroll
     for (int j = 0; j < N; j += 4) {
       const float4 f = __ldg(reinterpret_cast<const float4*>(p + c + j));
@@ -182,8 +183,8 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
         store_ckpt<T, FULL>(reinterpret_cast<const float(&)[N]>(v[i]), p.q + row * p.ldq,
                             p.scale + row * p.lds, c, n, p.q_vec);
       float a[N], b[N];
-      load_param<N, FULL>(p.gain, c, n, p.p_vec, 1.f, a);
-      load_param<N, FULL>(p.shift, c, n, p.p_vec, 0.f, b);
+      load_param<N, FULL>(p.gain, c, n, 1.f, a);
+      load_param<N, FULL>(p.shift, c, n, 0.f, b);
 #pragma unroll
       for (int j = 0; j < N / 2; ++j)
         v[i][j] = fma2(mul2(add2(v[i][j], f2(-mu)), f2(rho)), f2(a[2 * j], a[2 * j + 1]),
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kLoopThreads) ln_fwd_wide_kernel(const LayerNo
       float v[N], a[N], b[N];
       unpack_piece<T>(load_piece(x + c, n, p.x_vec), v);
       if (p.q) store_ckpt<T>(v, p.q + row * p.ldq, p.scale + row * p.lds, c, n, p.q_vec);
-      load_param<N>(p.gain, c, n, p.p_vec, 1.f, a);
-      load_param<N>(p.shift, c, n, p.p_vec, 0.f, b);
+      load_param<N>(p.gain, c, n, 1.f, a);
+      load_param<N>(p.shift, c, n, 0.f, b);
 #pragma unroll
       for (int j = 0; j < N; ++j) v[j] = fmaf((v[j] - mu) * rho, a[j], b[j]);
       store_piece(static_cast<T*>(p.y) + row * p.ldy + c, v, n, p.y_vec);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
     for (int i = 0; i < NV; ++i) {
       const int c = (i * 32 * WPR + t) * N, n = p.d - c;
       float gain[N];  // from L1: as registers they would cost a block per SM
-      load_param<N, FULL>(p.gain, c, n, p.p_vec, 1.f, gain);
+      load_param<N, FULL>(p.gain, c, n, 1.f, gain);
       unpack_piece<T>(rdy[i], g[i]);
       rx[i].values(xh[i]);
 #pragma unroll
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kLoopThreads) ln_bwd_wide_kernel(const LayerNo
       x.load(p, row, c, p.d - c);
       x.values(xh);
       unpack_piece<T>(load_piece(dy + c, p.d - c, p.dy_vec), g);
-      load_param<N>(p.gain, c, p.d - c, p.p_vec, 1.f, gain);
+      load_param<N>(p.gain, c, p.d - c, 1.f, gain);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         xh[j] = c + j < p.d ? (xh[j] - mu) * rho : 0.f;
@@ -562,7 +563,7 @@ mlp_status fwd_held_of(const LayerNormFwd& p, cudaStream_t st) {
 
 template <typename T, int WPR>
 mlp_status fwd_held(const LayerNormFwd& p, cudaStream_t st) {
-  const bool full = p.d % RowVec<T>::N == 0 && p.x_vec && p.y_vec && p.p_vec && (!p.q || p.q_vec);
+  const bool full = p.d % RowVec<T>::N == 0 && p.x_vec && p.y_vec && (!p.q || p.q_vec);
   return full ? fwd_held_of<T, WPR, true>(p, st) : fwd_held_of<T, WPR, false>(p, st);
 }
 
@@ -571,7 +572,6 @@ mlp_status fwd_t(LayerNormFwd p, cudaStream_t st) {
   p.x_vec = row_vec(p.x, p.ldx, sizeof(T), 16);
   p.y_vec = row_vec(p.y, p.ldy, sizeof(T), 16);
   p.q_vec = p.q && row_vec(p.q, p.ldq, 1, RowVec<T>::N);
-  p.p_vec = row_vec(p.gain, 0, 4, 16) && row_vec(p.shift, 0, 4, 16);
   LaunchScope ls("layernorm_fwd", st, p.T, p.d, sizeof(T));
   if (p.d <= 512) return fwd_held<T, 1>(p, st);
   if (p.d <= 1024) return fwd_held<T, 2>(p, st);
@@ -612,7 +612,7 @@ mlp_status bwd_held_of(const LayerNormBwd& p, int* blocks, cudaStream_t st) {
 
 template <typename T, int WPR, bool CK>
 mlp_status bwd_held(const LayerNormBwd& p, int* blocks, cudaStream_t st) {
-  const bool full = p.d % RowVec<T>::N == 0 && p.dy_vec && p.dx_vec && p.p_vec &&
+  const bool full = p.d % RowVec<T>::N == 0 && p.dy_vec && p.dx_vec &&
                     (!p.dres || p.r_vec) && (CK ? p.q_vec : p.x_vec);
   return full ? bwd_held_of<T, WPR, CK, true>(p, blocks, st)
               : bwd_held_of<T, WPR, CK, false>(p, blocks, st);
@@ -625,7 +625,6 @@ mlp_status bwd_t(LayerNormBwd p, cudaStream_t st) {
   p.q_vec = CK ? row_vec(p.q, p.ldq, 1, RowVec<T>::N) : 0;
   p.r_vec = row_vec(p.dres, p.ldr, sizeof(T), 16);
   p.dx_vec = row_vec(p.dx, p.lddx, sizeof(T), 16);
-  p.p_vec = row_vec(p.gain, 0, 4, 16);
   int blocks = bwd_blocks(p.T, p.d);
   if (p.d <= 512) MLP_CHECK((bwd_held<T, 1, CK>(p, &blocks, st)));
   else if (p.d <= 1024) MLP_CHECK((bwd_held<T, 2, CK>(p, &blocks, st)));

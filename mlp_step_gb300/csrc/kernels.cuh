@@ -186,7 +186,7 @@ struct LayerNormFwd {
   long long ldq;
   uint8_t* scale;
   long long lds;
-  int x_vec, y_vec, q_vec, p_vec;
+  int x_vec, y_vec, q_vec;
 };
 struct LayerNormBwd {
   int dtype;
@@ -210,7 +210,7 @@ struct LayerNormBwd {
   float* dgain;
   float* dshift;
   float* part;  // workspace: layernorm_ws_bytes
-  int dy_vec, x_vec, q_vec, r_vec, dx_vec, p_vec;
+  int dy_vec, x_vec, q_vec, r_vec, dx_vec;
 };
 size_t layernorm_ws_bytes(long long T, int d);
 mlp_status launch_layernorm_fwd(const LayerNormFwd& a, cudaStream_t st);
