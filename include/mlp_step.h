@@ -456,7 +456,8 @@ mlp_status mlp_layernorm_fwd(const void* x, int dtype, int ldx, const float* gai
  * The forward's input is given either as it was (x) or as its 8-bit
  * checkpoint (x_q, x_scale; x NULL), with the forward's mean and rstd either
  * way.  dres (nullable, [T][ldr]) is the gradient that reaches x past the
- * norm (the residual branch); dx may be dres itself.
+ * norm (the residual branch); dx may be dres or dy itself (the same pointer
+ * and pitch), also where those two are one.
  * workspace: mlp_layernorm_workspace_bytes(T, d) bytes. */
 size_t mlp_layernorm_workspace_bytes(int T, int d);
 mlp_status mlp_layernorm_bwd(const void* dy, int dtype, int lddy, const void* x, int ldx,

@@ -632,18 +632,19 @@ mlp_status bwd_t(LayerNormBwd p, cudaStream_t st) {
   else if (p.d <= 4096) MLP_CHECK((bwd_held<T, 8, CK>(p, &blocks, st)));
   else if (p.d <= kHeldWidth) MLP_CHECK((bwd_held<T, 16, CK>(p, &blocks, st)));
   else {
+    // the sums first: they read dy once more, which dx may overwrite
     {
-      LaunchScope ls("layernorm_bwd_wide", st, p.T, p.d, sizeof(T));
-      static PerDevice per_sm;
-      launch_k(ln_bwd_wide_kernel<T, CK>,
-               dim3(walk_blocks(ln_bwd_wide_kernel<T, CK>, kLoopThreads, per_sm, p.T, 1)),
-               dim3(kLoopThreads), 0, st, p);
+      LaunchScope ls("layernorm_bwd_wide_sums", st, p.T, p.d, sizeof(T));
+      const int stripe = 256 * RowVec<T>::N;
+      launch_k(ln_bwd_wide_sums_kernel<T, CK>, dim3((p.d + stripe - 1) / stripe, blocks),
+               dim3(256), 0, st, p);
       MLP_CHECK(launch_status());
     }
-    LaunchScope ls("layernorm_bwd_wide_sums", st, p.T, p.d, sizeof(T));
-    const int stripe = 256 * RowVec<T>::N;
-    launch_k(ln_bwd_wide_sums_kernel<T, CK>, dim3((p.d + stripe - 1) / stripe, blocks), dim3(256),
-             0, st, p);
+    LaunchScope ls("layernorm_bwd_wide", st, p.T, p.d, sizeof(T));
+    static PerDevice per_sm;
+    launch_k(ln_bwd_wide_kernel<T, CK>,
+             dim3(walk_blocks(ln_bwd_wide_kernel<T, CK>, kLoopThreads, per_sm, p.T, 1)),
+             dim3(kLoopThreads), 0, st, p);
     MLP_CHECK(launch_status());
   }
   return launch_partial_sums(p.part, blocks, 2 * p.d, 2 * p.d, p.dgain, p.d, p.dshift, st);

@@ -336,3 +336,35 @@ def test_bias_gradients_behind_odd_hidden_widths(prec, dtype):
     db = net.grads[-16:].double()
     ref = dl.double()  # summed in fp32
     near(db, ref.sum(0), (batch + 8) * 2.0 ** -23 * ref.abs().sum(0), "db")
+
+
+# ------------------------------------------------------------ in place
+
+@pytest.mark.parametrize("ck", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,d", [(1, 512), (300, 512), (77, 523), (130, 2000), (65, 4099),
+                                 (40, 8192), (380, 8209), (50, 20000)])
+def test_layernorm_backward_over_its_gradients(T, d, dtype, ck):
+    """dx over dy, and over a dres that is dy: the bits of the call with a dx of
+    its own, whatever the width."""
+    x, dy = rnd(60, T, d, dtype, shift=0.3), rnd(61, T, d, dtype, std=0.1)
+    gain = 1 + 0.2 * torch.randn(d, device="cuda")
+    mean = x.float().mean(1)
+    rstd = 1 / (x.float().var(1, unbiased=False) + 1e-5).sqrt()
+    kw = {"x": x}
+    if ck:
+        q = torch.empty(T, d, dtype=torch.int8, device="cuda")
+        s = torch.empty(T, M.mlp_ckpt8_scale_cols(d), dtype=torch.uint8, device="cuda")
+        M.mlp_ckpt8_encode(x, q, s)
+        kw = {"ckpt": (q, s)}
+    ws = bytes_for(M.mlp_layernorm_workspace_bytes(T, d))
+    for through in (False, True):
+        want, got = Guarded(T, d, dtype), rnd(62, T, d, dtype)
+        got.copy_(dy)
+        sums = [torch.empty(d, device="cuda") for _ in range(4)]
+        M.mlp_layernorm_bwd(dy, mean, rstd, want.v, sums[0], sums[1], ws, gain=gain,
+                            dres=dy if through else None, **kw)
+        M.mlp_layernorm_bwd(got, mean, rstd, got, sums[2], sums[3], ws, gain=gain,
+                            dres=got if through else None, **kw)
+        assert torch.equal(want.v, got)
+        assert torch.equal(sums[0], sums[2]) and torch.equal(sums[1], sums[3])
