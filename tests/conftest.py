@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -11,6 +12,14 @@ if ROOT not in sys.path:
 def pytest_configure(config):
     config.addinivalue_line("markers", "gpu: needs a CUDA GPU (sm_103a) and the built library")
     config.addinivalue_line("markers", "slow: takes more than a few seconds on the CPU")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _garbage_of_earlier_modules():
+    """Tensors that earlier modules left in reference cycles are freed here, not
+    in the middle of a test that counts allocated memory."""
+    gc.collect()
+    yield
 
 
 @pytest.fixture(scope="session")
