@@ -403,10 +403,13 @@ mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float ep
  * Layer norm, linear layers with activation and residual, and 8-bit activation
  * checkpoints.  The conventions at the top hold; further:
  *   - outputs do not overlap inputs, but where a call says so;
- *   - T == 0 (or no columns) writes nothing, except that gradients which are
- *     sums over the rows are set to zero;
+ *   - T == 0 writes nothing, except that gradients which are sums over the
+ *     rows are set to zero; widths are at least 1 (encoding and decoding alone
+ *     take no columns too, and write nothing), those of linear layers and 8-bit
+ *     checkpoints at most 2^24 (UNSUPPORTED_SHAPE);
  *   - sums over rows run in a fixed order without atomics, so results are the
  *     same in every run; MLP_ORDER_LINEAR does not apply here;
+ *   - calls may come from several host threads;
  *   - calls that take a workspace write it before they read it; calls that may
  *     overlap on the GPU (other streams, graphs in flight together) need
  *     workspaces of their own.  Fewer rows may need more of it (work is split
@@ -419,16 +422,18 @@ mlp_status mlp_stack_train_step(int n_blocks, int T, int d, int hidden, float ep
  * (the last group of a row may be shorter) share one scale byte b; the stored
  * int8 q stands for q 2^(b - 133).  With E = floor(log2(largest magnitude of
  * the group)): b = E + 127, at least 7, and q = x 2^(133 - b) rounded to the
- * nearest whole number (halves to even) and held to [-127, 127].  So a value
- * is off by at most 2^(E - 7) (half a step; one step, 2^(E - 6), where it was
- * held), under 1/64 of the group's largest magnitude.  A group that holds an
+ * nearest whole number (halves to even) and held to [-127, 127].  So where
+ * E >= -120 a value is off by at most 2^(E - 7) (half a step; one step,
+ * 2^(E - 6), where it was held), under 1/64 of the group's largest magnitude;
+ * in groups of smaller values, whose step stays 2^-126, by at most 2^-127
+ * (magnitudes up to that read back as 0).  A group that holds an
  * infinity or NaN gets b = 255 and reads back as NaN.  The encoding is exact
  * arithmetic, the same on every machine.
  * x, out: [rows][ld] of dtype F32, BF16 or F16; q: int8 [rows][ldq];
  * scale: bytes [rows][lds], mlp_ckpt8_scale_cols(cols) of them per row.  Any
  * pitches >= the widths; rows that start on 16 bytes (q: 8) are fastest.
- * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE (beyond 2^31 blocks of
- * 1024 16-byte pieces). */
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE (cols over 2^24, or beyond
+ * 2^31 blocks of 1024 16-byte pieces). */
 #define MLP_CKPT8_GROUP 32
 int mlp_ckpt8_scale_cols(int cols);
 mlp_status mlp_ckpt8_encode(const void* x, int x_dtype, int rows, int cols, int ldx, int8_t* q,
@@ -495,9 +500,9 @@ mlp_status mlp_stack_train_step_ckpt8(int n_blocks, int T, int d, int hidden, fl
  * Pitches of x and W in 16-bit types are multiples of 8.  d_in >= 1.
  * workspace: mlp_linear_workspace_bytes(...) bytes (0 for most 16-bit shapes;
  * NULL is then fine).
- * Activations of 16-bit layers are good to 5e-5 of f and of the two terms of f'
- * below 0 and to 3e-7 (1 + |u|) above (those of fp32 layers to a few 2^-23);
- * magnitudes below 2^-118 may read as 0.
+ * Activations are good to 5e-5 of f and of the two terms of f' where those are
+ * tiny (near 1e-36), 1e-5 at 1e-4 and a few 2^-23 near and above 0; magnitudes
+ * below 2^-118 may read as 0.
  * The tensor cores' fp32 accumulation truncates: sums are low by about 1e-9 of
  * their size per unit of d_in (1e-5 at d_in = 8,192), below the rounding of
  * 16-bit outputs.

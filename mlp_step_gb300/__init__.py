@@ -470,7 +470,8 @@ def mlp_stack_train_step_ckpt8(n_blocks, T, d, hidden, x0, target, params, veloc
 #
 # Matrices are 2-D CUDA tensors on the current device with unit stride along a
 # row; their row pitch is taken from stride(0), so column slices of wider
-# tensors are fine.  Outputs are given by the caller.  `ckpt` is an 8-bit
+# tensors are fine where the first column starts on 16 bytes (as every pointer
+# has to).  Outputs are given by the caller.  `ckpt` is an 8-bit
 # checkpoint: a pair (q, scale) of an int8 [rows, cols] and a uint8
 # [rows, mlp_ckpt8_scale_cols(cols)] matrix.
 

@@ -14,7 +14,7 @@
 // Error of the ACC = false forms, relative to the value itself for f and to the
 // sum of magnitudes of its two terms for f' (Phi and u phi; s and u s (1 - s)
 // z'): for GELU below 0, 4e-6 + u^2 2^-24; for the logistic ones (4 |z| + 16)
-// 2^-23, z the exponential's argument: 5e-5 at most, near 1e-36, and 5e-6 at
+// 2^-23, z the exponential's argument: 5e-5 at most, near 1e-36, and 1e-5 at
 // 1e-4.  Above 0, where values are of the order of 1 and u, 3e-7 of 1 + |u|
 // (f' of the tanh form up to 5e-6: 1 - s, good to 2^-23, times u z').  Half a
 // step of a 16-bit output is 2e-4 (fp16) or more; an fp32 output of a 16-bit

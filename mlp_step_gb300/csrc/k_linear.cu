@@ -25,10 +25,11 @@
 // 1,240 us = 1.77 PFLOP/s, 93 % of the library's rate; 65,536 x 1,536 -> 512
 // bf16 with residual: 75 us = 1.38 PFLOP/s).  For K of a few hundred, the
 // operands' way into shared memory (65,536 x 512 -> 1,536 bf16 without an
-// activation: 82 us, of which 64 are loads and MMAs) or the epilogue's issue
-// slots (GELU and 8-bit pre-activations: 105 us, backward with kept outputs
-// and column sums: 157 us = 28 and 30 instructions an output, at 55 % of the
-// issue rate with the sixteen warps that the registers hold).
+// activation: 82 us, of which 64 are loads and MMAs) or the epilogue (GELU and
+// 8-bit pre-activations: 105 us, backward with kept outputs and column sums:
+// 163 us = 22 and 31 instructions an output, issued in 55 and 57 % of the slots:
+// the latencies of the rest are what sixteen warps, all that the registers
+// hold, leave uncovered).
 #include <cstring>
 
 #include "linear_tc.cuh"
@@ -55,7 +56,10 @@ struct LinPlan {
 };
 
 // From the shape alone (so that workspace sizes do not depend on the device).
-// Pairs when their tiles fill most of ~76 pairs.  Otherwise the single-CTA tile
+// Pairs when their tiles fill most of ~76 pairs: at 48 tiles a K of 512 takes
+// 13.0 us in the best single tiles and 11.1 in pairs, 4,096 takes 35.0 and 27.2;
+// at 36 9.3 and 10.7, 24.8 and 26.1 (residual; from 39 on the single tiles need a
+// second round and pairs are ahead there too: 12.6 and 10.9 at 40).  Otherwise the single-CTA tile
 // and the split of K with the smallest estimated time: rounds of units over
 // ~152 CTAs, each as long as its MMAs or its epilogue.  A 64-deep block takes
 // about 512 cycles of a CTA's MMAs whatever the tile's width (measured: 500 in

@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kThreads) linear_finish_kernel(const LinearArg
 // Two batches of rows are in flight: the next one's loads are issued before
 // this one's arithmetic.  Measured with GELU (tanh) and column sums: 65,536 x
 // 1,536 bf16 108 us (5.6 TB/s), fp32 188 (6.4 TB/s); 10,007 x 1,001 fp32, a
-// value per lane and some forty instructions each, 28 (4.3 TB/s, the issue
-// slots 78 % taken; with one batch at a time 52).
+// value per lane and 64 instructions each, 27 (4.4 TB/s, the issue slots 75 %
+// taken; with one batch at a time 52).
 
 // V neighbouring values as they lie in memory, in whole registers.
 template <typename T, int V>
@@ -686,7 +686,9 @@ mlp_status act_t(const LinearArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Up to 8 rows for fp32 (whose tiled kernel computes 64 rows whatever T is).
+// Up to 8 rows, all that this kernel takes, for fp32, whose tiled kernel computes
+// 128 rows whatever T is (8 rows, here and there: 512 x 1,536 4.8 and 11.5 us,
+// 8,192 x 8,192 65 and 298; backward 9.5 and 12.7, 112 and 292).
 // In 16 bits the tensor cores take over once the FMAs, not the reading of W,
 // bound this kernel: above 2 rows of a large W (8,192 x 8,192, 4 rows: 49 us
 // here, 36 there), above 8 of a small one, 4 in the backward, whose x

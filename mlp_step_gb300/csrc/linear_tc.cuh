@@ -839,7 +839,11 @@ mlp_status launch_pair(const LinMaps& maps, const LinParams& p, cudaStream_t st)
 // Pairs: for short K the epilogue is as long as the product, so it gets
 // sixteen warps and the operand ring four stages (65,536 x 512 -> 1,536, no
 // activation: 64 us of MMAs and loads with four stages, 63 with five); for
-// long K eight warps leave room for a fifth stage.
+// long K eight warps leave room for a fifth stage.  Sixteen and eight warps,
+// 65,536 rows -> 1,536, GELU with 8-bit pre-activations: K = 512 101 and 126 us,
+// 768 137 and 138, 1,024 175 and 163, 1,536 234 and 222; the backward with column
+// sums 137 and 163, 151 and 179, 178 and 179, 235 and 241; without an activation
+// eight are ahead from 512 (79 and 70) to 1,536 (187 and 178).
 constexpr int kShortK = 16;  // k-blocks
 
 // The pairs of either operand ring.
