@@ -190,6 +190,26 @@ def test_activations_above_zero(act, dtype):
     near(du, df, rounding(dtype, df) * (1 + 1e-3) + e, "f'")
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_activation_derivatives_at_their_limits(dtype):
+    """f' of infinite and largest u where it has no limit in [0, 1], and of NaN."""
+    big = 6e4 if dtype == F16 else 3e38
+    u = torch.tensor([[math.inf, -math.inf, big, -big, 4.0, -4.0, 0.0, math.nan]],
+                     device="cuda").to(dtype)
+    dy, du = torch.full_like(u, 0.5), torch.empty_like(u)
+    inf = math.inf
+    for act, want in (("none", [0.5] * 8), ("relu", [0.5, 0, 0.5, 0, 0.5, 0, 0, None]),
+                      # 0.5 * 2 slope^2 u
+                      ("leaky2", [inf, -inf, None, None, 4, -1, 0, math.nan])):
+        M.mlp_act_bwd(dy, du, act=ACTS[act], slope=SLOPE, u=u)
+        for got, ref in zip(du[0].tolist(), want):
+            assert ref is None or got == ref or (math.isnan(ref) and math.isnan(got)), (act, got, ref)
+    for act in ("gelu", "gelu_tanh", "silu"):
+        M.mlp_act_bwd(dy, du, act=ACTS[act], u=u)
+        assert du[0, [0, 2]].tolist() == [0.5, 0.5] and du[0, 7].isnan(), act
+        assert (du[0, [1, 3]].double().abs() < 1e-30).all() and abs(du[0, 6].item() - 0.25) < 1e-6, act
+
+
 # ------------------------------------------------------------ mixed pitches
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -368,3 +388,157 @@ def test_layernorm_backward_over_its_gradients(T, d, dtype, ck):
                             dres=got if through else None, **kw)
         assert torch.equal(want.v, got)
         assert torch.equal(sums[0], sums[2]) and torch.equal(sums[1], sums[3])
+
+
+# ------------------------------------------------------------ captured calls
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("T", [1, 5, 300])
+def test_operators_captured(T, dtype):
+    """Every operator in one captured graph, replayed on new inputs: the bits of
+    the calls one by one."""
+    k, n = 520, 1001
+    x, w = rnd(70, T, k, dtype), rnd(71, k, n, dtype, std=k ** -0.5)
+    wt = rnd(72, n, k, dtype)
+    wt.copy_(w.t())
+    f = lambda z: torch.empty(z, device="cuda")  # noqa: E731
+    e = lambda c, t=dtype: Guarded(T, c, t)  # noqa: E731
+    o = {"n": e(k), "y": e(n), "u": e(n), "du": e(n), "a": e(n), "d2": e(n), "dx": e(k), "dec": e(k)}
+    v = {"mean": f(T), "rstd": f(T), "dg": f(k), "ds": f(k), "db": f(n), "db2": f(n)}
+    xq = (e(k, torch.int8).v, e(-(-k // 32), torch.uint8).v)
+    uq = (e(n, torch.int8).v, e(-(-n // 32), torch.uint8).v)
+    ws = [bytes_for(z) for z in (M.mlp_linear_workspace_bytes(T, k, n, dtype),
+                                 M.mlp_linear_bwd_workspace_bytes(T, n, k, dtype),
+                                 M.mlp_act_bwd_workspace_bytes(T, n),
+                                 M.mlp_layernorm_workspace_bytes(T, k))]
+
+    def calls():
+        M.mlp_layernorm_fwd(x, o["n"].v, mean=v["mean"], rstd=v["rstd"], ckpt=xq)
+        M.mlp_linear_fwd(o["n"].v, w, o["y"].v, act=M.MLP_ACT_SILU, u=o["u"].v, ckpt=uq,
+                         workspace=ws[0])
+        M.mlp_linear_bwd(o["n"].v, wt, o["du"].v, act=M.MLP_ACT_GELU, ckpt=uq, dbias=v["db"],
+                         a=o["a"].v, workspace=ws[1])
+        M.mlp_act_bwd(o["y"].v, o["d2"].v, act=M.MLP_ACT_GELU_TANH, u=o["u"].v, dbias=v["db2"],
+                      workspace=ws[2])
+        M.mlp_layernorm_bwd(o["n"].v, v["mean"], v["rstd"], o["dx"].v, v["dg"], v["ds"], ws[3],
+                            ckpt=xq)
+        M.mlp_ckpt8_decode(*xq, o["dec"].v)
+
+    calls()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    x.copy_(rnd(73, T, k, dtype))
+    outs = [t.v for t in o.values()] + list(v.values())
+    calls()
+    want = [t.clone() for t in outs]
+    for _ in range(2):
+        for t in outs:
+            t.fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    assert all(t.intact() for t in o.values())
+
+
+@pytest.mark.parametrize("n_blocks,T", [(1, 1), (3, 1), (3, 257)])
+def test_stack_with_8bit_checkpoints_captured(n_blocks, T):
+    """The stack's step with 8-bit checkpoints from a single token on, eager and
+    as a replayed graph."""
+    d, h, per = 512, 512, 2 * 512 * 512
+    x0, tgt = rnd(80, T, d, BF16).contiguous(), rnd(81, T, d, BF16).contiguous()
+    g0 = torch.Generator(device="cuda").manual_seed(82)
+    p0 = (0.02 * torch.randn(n_blocks * per, generator=g0, device="cuda")).to(BF16)
+    P, W = p0.float(), p0.clone()
+    V, G, L = torch.zeros_like(P), torch.zeros_like(P), torch.zeros(4, device="cuda")
+    ws = bytes_for(M.mlp_stack_ckpt8_workspace_bytes(n_blocks, T, d, h))
+
+    def reset():
+        P.copy_(p0.float())
+        W.copy_(p0)
+        V.zero_()
+        G.fill_(math.nan)
+        ws.fill_(255)
+
+    def step():
+        M.mlp_stack_train_step_ckpt8(n_blocks, T, d, h, x0, tgt, P, V, G, W, 0.02, 0.9, L, ws)
+
+    reset()
+    step()
+    want = [t.clone() for t in (P, V, G, W, L)]
+    assert want[2].isfinite().all() and want[4][0] > 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    reset()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip((P, V, G, W, L), want))
+
+
+# ------------------------------------------------------------ far offsets
+
+def test_backward_offsets_past_32_bits():
+    """Gradients and saved values in rows so far apart that element offsets pass
+    2^31: the last rows' values are those of a call on these rows alone."""
+    T, d, ld = 70_000, 64, 40_000
+    base = torch.empty(T, ld, dtype=BF16, device="cuda")
+    qb = torch.empty(T, ld, dtype=torch.int8, device="cuda")
+    col = lambda i: base[:, 128 * i:128 * i + d]  # noqa: E731
+    dy, u, du, a, dx = (col(i) for i in range(5))
+    dy.copy_(rnd(90, T, d, BF16))
+    u.copy_(rnd(91, T, d, BF16, std=1.5))
+    q, s = qb[:, 32:32 + d], torch.empty(T, 2, dtype=torch.uint8, device="cuda")
+    M.mlp_ckpt8_encode(u, q, s)
+    w = rnd(92, d, d, BF16, 0.125)
+    mean, rstd = u.float().mean(1), 1 / u.float().std(1)
+    db, dg, ds = (torch.empty(d, device="cuda") for _ in range(3))
+    last = slice(T - 300, T)
+    e = lambda: torch.empty(300, d, dtype=BF16, device="cuda")  # noqa: E731
+    ws = bytes_for(max(f(t) for t in (T, 300) for f in (
+        lambda t: M.mlp_act_bwd_workspace_bytes(t, d), lambda t: M.mlp_layernorm_workspace_bytes(t, d),
+        lambda t: M.mlp_linear_bwd_workspace_bytes(t, d, d, BF16))))
+    end = lambda t: t[last].clone(memory_format=torch.contiguous_format)  # noqa: E731
+    for kw, kw_end in (({"u": u}, {"u": end(u)}), ({"ckpt": (q, s)}, {"ckpt": (end(q), end(s))})):
+        M.mlp_act_bwd(dy, du, act=M.MLP_ACT_SILU, dbias=db, a=a, workspace=ws, **kw)
+        g, h = e(), e()
+        M.mlp_act_bwd(end(dy), g, act=M.MLP_ACT_SILU, a=h, **kw_end)
+        assert torch.equal(du[last], g) and torch.equal(a[last], h)
+        M.mlp_linear_bwd(dy, w, du, act=M.MLP_ACT_RELU, dbias=db, a=a, workspace=ws, **kw)
+        M.mlp_linear_bwd(end(dy), w, g, act=M.MLP_ACT_RELU, a=h, workspace=ws, **kw_end)
+        # 64 terms in another kernel's order, then one rounding each
+        near(du[last], g, 2 * rounding(BF16, g.double()) + 64 * 2.0 ** -22, "du")
+        assert torch.equal(a[last], h)
+        x_kw = {("x" if k == "u" else k): v for k, v in kw.items()}
+        x_end = {("x" if k == "u" else k): v for k, v in kw_end.items()}
+        M.mlp_layernorm_bwd(dy, mean, rstd, dx, dg, ds, ws, dres=dy, **x_kw)
+        M.mlp_layernorm_bwd(end(dy), end(mean), end(rstd), g, dg, ds, ws, dres=end(dy), **x_end)
+        assert torch.equal(dx[last], g)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T", [1, 8, 64])
+def test_linear_weights_past_32_bits(T, dtype):
+    """Weights of more than 2^31 elements: their last rows and columns are read
+    where they are."""
+    k, n, few = 60_000, 40_000, 40
+    w = torch.zeros(k, n, dtype=dtype, device="cuda")
+    w[-1] = rnd(93, 1, n, dtype)[0]
+    x = torch.zeros(T, k, dtype=dtype, device="cuda")
+    x[:, -1] = torch.arange(1, T + 1, device="cuda").to(dtype)
+    y = torch.empty(T, n, dtype=dtype, device="cuda")
+    ws = bytes_for(max(M.mlp_linear_workspace_bytes(T, k, n, dtype),
+                       M.mlp_linear_bwd_workspace_bytes(T, k, n, dtype)))
+    M.mlp_linear_fwd(x, w, y, workspace=ws)
+    ref = x[:, -1:].double() * w[-1].double()
+    near(y, ref, rounding(dtype, ref), "y")
+    # backward: du[:, -1] is dy . w[-1], the others 0
+    dy = torch.zeros(T, n, dtype=dtype, device="cuda")
+    dy[:, -few:] = rnd(94, T, few, dtype)
+    du = torch.empty(T, k, dtype=dtype, device="cuda")
+    M.mlp_linear_bwd(dy, w, du, workspace=ws)
+    p = dy[:, -few:].double() * w[-1, -few:].double()
+    ref = p.sum(1)
+    near(du[:, -1], ref, rounding(dtype, ref) + few * 2.0 ** -22 * p.abs().sum(1), "du")
+    assert (du[:, :-1] == 0).all()
