@@ -542,6 +542,57 @@ mlp_status mlp_act_bwd(const void* dy, int lddy, int T, int n, int dtype, int ac
                        const uint8_t* u_scale, int lds, void* du, int lddu, float* dbias,
                        void* a_out, int lda, void* workspace, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- gated units
+ * The two projections of a gated feed-forward layer, its activation and the
+ * product:
+ *   g = x W_gate + b_gate;  u = x W_up + b_up;  y = f(g) u,
+ * in one kernel that reads x once; everything is fp32 up to the one rounding of
+ * each output.  The conventions of the feed-forward operators hold.
+ * x [T][d_in], W_gate and W_up [d_in][hidden] (their own pitches: they may be
+ * the two halves of one matrix), y [T][hidden], all of the operand type dtype
+ * (BF16 or F16: tcgen05 kernels; F32: fp32 FMA); b_gate and b_up fp32 [hidden],
+ * each nullable; act any MLP_ACT_* (SILU and GELU are the usual ones).
+ * For the backward pass the pre-activations may be kept in one form, both of
+ * them: g_out and u_out (the operand type), or g_q, g_scale, u_q and u_scale
+ * (8-bit checkpoints of the unrounded g and u).
+ * Pitches of x and both W in 16-bit types are multiples of 8.
+ * workspace: mlp_glu_workspace_bytes(...) bytes (0 for most 16-bit shapes;
+ * NULL is then fine).  Precision of the activations and of the sums: as in the
+ * linear layers.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
+size_t mlp_glu_workspace_bytes(int T, int d_in, int hidden, int dtype);
+mlp_status mlp_glu_fwd(const void* x, int ldx, const void* w_gate, int ldwg, const void* w_up,
+                       int ldwu, int T, int d_in, int hidden, int dtype, const float* b_gate,
+                       const float* b_up, int act, float slope, void* y, int ldy, void* g_out,
+                       int ldg, void* u_out, int ldu, int8_t* g_q, int ldgq, uint8_t* g_scale,
+                       int ldgs, int8_t* u_q, int lduq, uint8_t* u_scale, int ldus,
+                       void* workspace, size_t ws_bytes, void* stream);
+
+/* Backward through the down projection that takes y and the gated unit: with
+ * dy [T][d_out] the gradient of the projection's output and W_down
+ * [hidden][d_out] its weight,
+ *   da = dy W_down^T;  dg = da u f'(g);  du = da f(g)   [T][hidden] each,
+ *   db_gate = sum_t dg;  db_up = sum_t du   (fp32 [hidden], both or neither;
+ *                       from the unrounded values, in a fixed order),
+ *   a_out = f(g) u      (nullable: the forward's y again, the left operand of
+ *                       dW_down = a^T dy, mlp_gemm).
+ * g and u are given in the operand type (g, u) or as 8-bit checkpoints (the
+ * others; g and u NULL).  All matrices have the type dtype; dg may be g, and
+ * du u (the same pointer and pitch).  With dg and du side by side in one
+ * [T][2 hidden] matrix, as W_gate and W_up in theirs, the remaining gradients
+ * are one product each: dx = [dg du] [W_gate W_up]^T (mlp_linear_bwd without an
+ * activation) and [dW_gate dW_up] = x^T [dg du] (mlp_gemm).
+ * Pitches of dy and W_down in 16-bit types are multiples of 8.
+ * workspace: mlp_glu_bwd_workspace_bytes(...) bytes. */
+size_t mlp_glu_bwd_workspace_bytes(int T, int hidden, int d_out, int dtype);
+mlp_status mlp_glu_bwd(const void* dy, int lddy, const void* w_down, int ldw, int T, int hidden,
+                       int d_out, int dtype, int act, float slope, const void* g, int ldg,
+                       const void* u, int ldu, const int8_t* g_q, int ldgq,
+                       const uint8_t* g_scale, int ldgs, const int8_t* u_q, int lduq,
+                       const uint8_t* u_scale, int ldus, void* dg, int lddg, void* du, int lddu,
+                       float* db_gate, float* db_up, void* a_out, int lda, void* workspace,
+                       size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

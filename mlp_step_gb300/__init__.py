@@ -118,6 +118,13 @@ SIGNATURES = {
     "mlp_linear_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "mlp_linear_bwd": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i,
                             _vp, _i, _i, _vp, _vp, _i, _vp, _sz, _vp]),
+    "mlp_glu_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "mlp_glu_fwd": (_i, [_vp, _i, _vp, _i, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _f, _vp, _i, _vp,
+                         _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _sz, _vp]),
+    "mlp_glu_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "mlp_glu_bwd": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i, _vp,
+                         _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _sz,
+                         _vp]),
     "mlp_act_bwd_workspace_bytes": (_sz, [_i, _i]),
     "mlp_act_bwd": (_i, [_vp, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp,
                          _vp, _i, _vp, _sz, _vp]),
@@ -724,3 +731,62 @@ def mlp_act_bwd(dy, du, act=MLP_ACT_NONE, slope=0.5, u=None, ckpt=None, dbias=No
     _check(load().mlp_act_bwd(dyp, lddy, T, n, _code_of(dy.dtype), act, slope, up, ldu, qp, ldq, sp,
                               lds, dup, lddu, _vec(dbias, "dbias", n, dev), ap, lda, ws, wsb,
                               _stream_of(stream, dev)), "mlp_act_bwd")
+
+
+def mlp_glu_workspace_bytes(T: int, d_in: int, hidden: int, dtype) -> int:
+    """Workspace of mlp_glu_fwd (0 for most shapes; fewer rows may need more);
+    dtype: the operands' torch dtype."""
+    return load().mlp_glu_workspace_bytes(*_sizes(T, d_in, hidden), _code_of(dtype))
+
+
+def mlp_glu_fwd(x, w_gate, w_up, y, b_gate=None, b_up=None, act=MLP_ACT_SILU, slope=0.5, g=None,
+                u=None, g_ckpt=None, u_ckpt=None, workspace=None, stream=None):
+    """y = f(x w_gate + b_gate) * (x w_up + b_up); x [T, d_in], w_gate and w_up
+    [d_in, hidden] (they may be the halves of one matrix); g, u: receive the two
+    pre-activations, g_ckpt, u_ckpt: receive them in 8 bits."""
+    T, k = x.shape
+    n = w_gate.shape[1]
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", T, k, dev)
+    wgp, ldwg = _mat(w_gate, "w_gate", k, n, dev, x.dtype)
+    wup, ldwu = _mat(w_up, "w_up", k, n, dev, x.dtype)
+    yp, ldy = _mat(y, "y", T, n, dev, x.dtype)
+    gp, ldg = _mat(g, "g", T, n, dev, x.dtype)
+    up, ldu = _mat(u, "u", T, n, dev, x.dtype)
+    ws, wsb = _ws(workspace, dev)
+    _check(load().mlp_glu_fwd(xp, ldx, wgp, ldwg, wup, ldwu, T, k, n, _code_of(x.dtype),
+                              _vec(b_gate, "b_gate", n, dev), _vec(b_up, "b_up", n, dev), act,
+                              slope, yp, ldy, gp, ldg, up, ldu,
+                              *_ckpt(g_ckpt, "g_ckpt", T, n, dev),
+                              *_ckpt(u_ckpt, "u_ckpt", T, n, dev), ws, wsb,
+                              _stream_of(stream, dev)), "mlp_glu_fwd")
+
+
+def mlp_glu_bwd_workspace_bytes(T: int, hidden: int, d_out: int, dtype) -> int:
+    """Workspace of mlp_glu_bwd for w_down [hidden, d_out] and dy [T, d_out]
+    (fewer rows may need more)."""
+    return load().mlp_glu_bwd_workspace_bytes(*_sizes(T, hidden, d_out), _code_of(dtype))
+
+
+def mlp_glu_bwd(dy, w_down, dg, du, act=MLP_ACT_SILU, slope=0.5, g=None, u=None, g_ckpt=None,
+                u_ckpt=None, db_gate=None, db_up=None, a=None, workspace=None, stream=None):
+    """With da = dy w_down^T: dg = da u f'(g), du = da f(g); dy [T, d_out],
+    w_down [hidden, d_out], g and u [T, hidden] given as they are or as 8-bit
+    checkpoints; db_gate, db_up fp32 [hidden] receive the column sums of dg and
+    du, a (dy's dtype) the activations f(g) u."""
+    T, k = dy.shape
+    n = w_down.shape[0]
+    dev = _device(dy, "dy")
+    dyp, lddy = _mat(dy, "dy", T, k, dev)
+    wp, ldw = _mat(w_down, "w_down", n, k, dev, dy.dtype)
+    dgp, lddg = _mat(dg, "dg", T, n, dev, dy.dtype)
+    dup, lddu = _mat(du, "du", T, n, dev, dy.dtype)
+    gp, ldg = _mat(g, "g", T, n, dev, dy.dtype)
+    up, ldu = _mat(u, "u", T, n, dev, dy.dtype)
+    ap, lda = _mat(a, "a", T, n, dev, dy.dtype)
+    ws, wsb = _ws(workspace, dev)
+    _check(load().mlp_glu_bwd(dyp, lddy, wp, ldw, T, n, k, _code_of(dy.dtype), act, slope, gp, ldg,
+                              up, ldu, *_ckpt(g_ckpt, "g_ckpt", T, n, dev),
+                              *_ckpt(u_ckpt, "u_ckpt", T, n, dev), dgp, lddg, dup, lddu,
+                              _vec(db_gate, "db_gate", n, dev), _vec(db_up, "db_up", n, dev), ap,
+                              lda, ws, wsb, _stream_of(stream, dev)), "mlp_glu_bwd")

@@ -111,7 +111,8 @@ bool encode_tmap_u8_2d(CUtensorMap* map, const void* base, unsigned long long in
                        unsigned long long outer, unsigned long long row_stride_bytes,
                        unsigned box_inner, unsigned box_outer) {
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, inner, outer, row_stride_bytes,
-                   box_inner, box_outer, CU_TENSOR_MAP_SWIZZLE_64B);
+                   box_inner, box_outer,
+                   box_inner == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool encode_tmap_out_2d(CUtensorMap* map, const void* base, int fp32, unsigned long long inner,

@@ -1,0 +1,91 @@
+// Gated units on the tensor cores, forward: both projections of x, the
+// activation and the product in one kernel,
+//   g = x Wg + bg,  u = x Wu + bu,  y = f(g) u,
+// fp32 from the accumulators to the one rounding of each output; g and u are
+// optionally stored, in the operand type or in 8 bits.
+//
+// One accumulator holds the gate and the up columns of the same hidden columns
+// side by side: a tile of a CTA pair (256 rows, cta_group::2, N = 256) is 128
+// hidden columns, of which the even CTA stages the gate's weights and the odd
+// one the up projection's, so the MMAs are those of an ordinary product of
+// twice the width and the epilogue finds both factors of an output in one row
+// of tensor memory, 128 columns apart.  x is read once for both products and g
+// and u never leave the SM unless they are kept.  Where such tiles are few, a
+// single CTA does the same on 128 rows (128 or 64 hidden columns), with the
+// contraction split over CTAs when even those are few (raw sums to a
+// workspace, finished by launch_glu_finish).  Warps: TMA producer, MMA issuer,
+// four to sixteen epilogue warps; two accumulators, so that the epilogue of one
+// tile overlaps the MMAs of the next.  The body is in glu_tc.cuh.
+#include "glu_launch.cuh"
+
+namespace mlp {
+
+namespace {
+
+// From the shape alone (so that workspace sizes do not depend on the device).
+// Pairs when their tiles fill most of ~76 pairs; otherwise the single-CTA tile
+// and the split of K with the smallest estimated time: rounds of units over
+// ~152 CTAs, each as long as its MMAs (a 64-deep block takes about 512 cycles
+// whatever the tile's width) or its epilogue, and the weights' way from memory.
+// A split costs the second launch and the raw sums' way through memory.
+GluPlan plan(long long T, int K, int N, bool bwd) {
+  const int kb = (K + GBK - 1) / GBK, pair_hid = bwd ? 256 : 128;
+  if (T > 128 && N > pair_hid / 2 &&
+      (T + 255) / 256 * ((N + pair_hid - 1) / pair_hid) >= 48)
+    return {kGluPair, pair_hid, 1, kb};
+  GluPlan best{};
+  double best_cycles = 1e300;
+  for (int i = 0; i < 2; ++i) {
+    const GluTile tile = bwd ? (i ? kGluNarrow : kGluWide) : (i ? kGluWide : kGluTall);
+    const int hid = i ? 64 : 128;
+    if (i == 0 && N <= hid / 2) continue;
+    const long long tiles = (T + 127) / 128 * ((N + hid - 1) / hid);
+    for (int s = 1; s <= 16; ++s) {
+      if (s > 1 && (s > kb / 2 || tiles * s > 304)) break;
+      const int per = (kb + s - 1) / s, splits = (kb + per - 1) / per;
+      const double rounds = (double)((tiles * splits + 151) / 152);
+      const double epilogue = tile == kGluTall ? (splits > 1 ? 8000 : 12000) : 4500;
+      const double mma = per * 512., read = (double)K * N * (bwd ? 2 : 4) / 3500;
+      double cycles = rounds * (mma > epilogue ? mma : epilogue);
+      cycles = (cycles > read ? cycles : read) + epilogue;
+      if (splits > 1) cycles += 5000 + splits * (double)T * N * (bwd ? 8 : 16) / 1750;
+      if (cycles < best_cycles) {
+        best_cycles = cycles;
+        best = {tile, hid, splits, per};
+      }
+    }
+  }
+  return best;
+}
+
+template <int H16>
+mlp_status launch(const GluMaps& maps, const GluParams& p, GluTile tile, cudaStream_t st) {
+  if (tile == kGluPair) {
+    const bool short_k = p.k_blocks <= 16;
+    if (glu_whole(p, false))
+      return short_k ? launch_glu_pair<4, 16, H16, kGluFwd, true>(maps, p, st)
+                     : launch_glu_pair<5, 8, H16, kGluFwd, true>(maps, p, st);
+    return short_k ? launch_glu_pair<4, 16, H16, kGluFwd, false>(maps, p, st)
+                   : launch_glu_pair<5, 8, H16, kGluFwd, false>(maps, p, st);
+  }
+  if (tile == kGluTall)
+    return p.a_bytes <= 32 * GBK * 2 ? launch_glu_single<256, 5, 4, 32, H16, kGluFwd>(maps, p, st)
+                                     : launch_glu_single<256, 4, 4, 128, H16, kGluFwd>(maps, p, st);
+  return launch_glu_single<128, 5, 8, 128, H16, kGluFwd>(maps, p, st);
+}
+
+}  // namespace
+
+int glu_tc_splits(long long T, int K, int N, bool bwd) { return plan(T, K, N, bwd).splits; }
+
+mlp_status launch_glu_tc(const GluArgs& a, bool bwd, cudaStream_t st) {
+  const GluPlan pl = plan(a.T, a.K, a.N, bwd);
+  if (bwd) return launch_glu_bwd_tc(a, pl, st);
+  GluMaps maps;
+  GluParams p;
+  MLP_CHECK(glu_setup(a, pl, false, maps, p));
+  return a.dtype == MLP_DTYPE_F16 ? launch<1>(maps, p, pl.tile, st)
+                                  : launch<0>(maps, p, pl.tile, st);
+}
+
+}  // namespace mlp

@@ -1,0 +1,45 @@
+// Gated units on the tensor cores, backward: through the down projection and
+// the gate in one kernel,
+//   da = dy Wd^T,  dg = da u f'(g),  du = da f(g),  a = f(g) u,
+// with the column sums of dg and du (the bias gradients).  g and u are read in
+// the operand type or from 8 bits.
+//
+// Tiles as in k_glu.cu, without the second weight (256 x 256 of a CTA pair,
+// 128 x 128 or 128 x 64 of one CTA).  Bound by HBM for K of a few hundred:
+// beside the product, 8 to 10 bytes move per value of da.  So the saved values
+// of an epilogue warp's next piece (32 x 32) are on their way by TMA while it
+// works on this one, and every output leaves by TMA from a box of its own.
+#include "glu_launch.cuh"
+
+namespace mlp {
+
+namespace {
+
+template <int H16, int MODE>
+mlp_status launch(const GluMaps& maps, const GluParams& p, GluTile tile, cudaStream_t st) {
+  if (tile == kGluPair) {
+    const bool short_k = p.k_blocks <= 16;
+    if (glu_whole(p, true))
+      return short_k ? launch_glu_pair<2, 16, H16, MODE, true>(maps, p, st)
+                     : launch_glu_pair<4, 8, H16, MODE, true>(maps, p, st);
+    return short_k ? launch_glu_pair<2, 16, H16, MODE, false>(maps, p, st)
+                   : launch_glu_pair<4, 8, H16, MODE, false>(maps, p, st);
+  }
+  if (tile == kGluWide) return launch_glu_single<128, 4, 8, 128, H16, MODE>(maps, p, st);
+  return launch_glu_single<64, 7, 4, 128, H16, MODE>(maps, p, st);
+}
+
+}  // namespace
+
+mlp_status launch_glu_bwd_tc(const GluArgs& a, const GluPlan& pl, cudaStream_t st) {
+  GluMaps maps;
+  GluParams p;
+  MLP_CHECK(glu_setup(a, pl, true, maps, p));
+  const bool h16 = a.dtype == MLP_DTYPE_F16;
+  if (a.q[0])
+    return h16 ? launch<1, kGluBwdCkpt>(maps, p, pl.tile, st)
+               : launch<0, kGluBwdCkpt>(maps, p, pl.tile, st);
+  return h16 ? launch<1, kGluBwd>(maps, p, pl.tile, st) : launch<0, kGluBwd>(maps, p, pl.tile, st);
+}
+
+}  // namespace mlp

@@ -1,0 +1,413 @@
+// Gated units outside the tensor-core tiles (formulas: k_glu.cu, k_glu_bwd.cu):
+// the one-launch kernel for a few rows (single tokens), and the epilogues as
+// passes of their own over raw sums (split-K partial planes, fp32 products).
+// A warp finishes 32 columns of a row at a time, one per lane: memory is
+// touched in whole rows of 32 values and a group of the 8-bit form is one warp.
+#include "act.cuh"
+#include "ckpt8.cuh"
+#include "few_rows.cuh"
+#include "kernels.cuh"
+#include "ptx.cuh"
+#include "rowvec.cuh"
+#include "trace.cuh"
+
+namespace mlp {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsAhead = 4;  // rows loaded before the first is finished
+
+// Element (m, c) of kept matrix k: the pre-activation z in the operand type or
+// in 8 bits (whole warps, lane = column of a 32-column group).
+template <typename T>
+__device__ __forceinline__ void keep(const GluArgs& a, int k, long long m, int c, bool ok,
+                                     float z) {
+  if (a.o[k]) {
+    if (ok) from_f32(z, static_cast<T*>(a.o[k])[m * a.ldo[k] + c]);
+  } else if (a.q[k]) {
+    const uint32_t top =
+        __reduce_max_sync(0xffffffffu, ok ? __float_as_uint(z) & 0x7fffffffu : 0u);
+    const uint32_t b = ckpt8_byte(top);
+    if (ok) {
+      const float held = ckpt8_must_hold(top) ? ckpt8_hold(z, ckpt8_step(b)) : z;
+      a.q[k][m * a.ldq[k] + c] =
+          b == kCkptNanByte ? (int8_t)0 : (int8_t)ckpt8_q(held, ckpt8_inv_step(b));
+    }
+    if ((c & 31) == 0) a.scale[k][m * a.lds[k] + c / kCkptGroup] = (uint8_t)b;
+  }
+}
+
+// Forward outputs of element (m, c) from its raw sums.
+template <typename T, int ACT>
+__device__ __forceinline__ void glu_out(const GluArgs& a, long long m, int c, bool ok, float g,
+                                        float u, float bg, float bu) {
+  g += bg;
+  u += bu;
+  keep<T>(a, 0, m, c, ok, g);
+  keep<T>(a, 1, m, c, ok, u);
+  const float y = act_value_of<sizeof(T) == 4, ACT>(g, a.slope) * u;
+  if (ok) from_f32(y, static_cast<T*>(a.y)[m * a.ldy + c]);
+}
+
+__device__ __forceinline__ float bias_of(const float* b, int c, bool ok) {
+  return b && ok ? __ldg(b + c) : 0.f;
+}
+
+// ------------------------------------------------------------ epilogue passes
+
+// Sums of element rows m0 .. m0 + kRowsAhead - 1 over the planes in order, four
+// of all rows at a time in flight.
+__device__ __forceinline__ void add_planes(const GluArgs& a, const float* p, long long plane,
+                                           int rows, bool ok, float (&v)[kRowsAhead]) {
+#pragma unroll
+  for (int k = 0; k < kRowsAhead; ++k) v[k] = 0.f;
+#pragma unroll 1
+  for (int s = 0; s < a.splits; s += 4) {
+    float q[kRowsAhead][4];
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        q[k][j] = ok && k < rows && s + j < a.splits ? __ldcs(p + (s + j) * plane + k * a.ldp)
+                                                     : 0.f;
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[k] += q[k][j];
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) glu_finish_fwd_kernel(const GluArgs a, int groups,
+                                                                  long long units) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const long long rb = unit / groups;
+  const int c = (int)(unit - rb * groups) * 32 + lane;
+  const bool ok = c < a.N;
+  const long long m0 = rb * kRowsAhead, plane = a.T * a.ldp;
+  const int rows = (int)min((long long)kRowsAhead, a.T - m0);
+  const float bg = bias_of(a.bias[0], c, ok), bu = bias_of(a.bias[1], c, ok);
+  float g[kRowsAhead], u[kRowsAhead];
+  const float* p = a.partial + m0 * a.ldp + c;
+  add_planes(a, p, plane, rows, ok, g);
+  add_planes(a, p + a.splits * plane, plane, rows, ok, u);
+  with_act(a.act, [&](auto tag) {
+#pragma unroll
+    for (int k = 0; k < kRowsAhead; ++k)
+      if (k < rows)  // warp-uniform
+        glu_out<T, decltype(tag)::value>(a, m0 + k, c, ok, g[k], u[k], bg, bu);
+  });
+}
+
+// Warp unit: a.part_rows rows of 32 columns, whose column sums it adds in row
+// order into one row of colpart.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) glu_finish_bwd_kernel(const GluArgs a, int groups,
+                                                                  long long units) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const long long rb = unit / groups;
+  const int c = (int)(unit - rb * groups) * 32 + lane;
+  const bool ok = c < a.N;
+  const long long m_end = min(a.T, (rb + 1) * a.part_rows), plane = a.T * a.ldp;
+  float s0 = 0.f, s1 = 0.f;
+  auto saved = [&](int k, long long m, bool in) {
+    if (!in) return 0.f;
+    if (a.q[k])
+      return (float)a.q[k][m * a.ldq[k] + c] *
+             ckpt8_step(a.scale[k][m * a.lds[k] + c / kCkptGroup]);
+    return to_f32(static_cast<const T*>(a.in[k])[m * a.ld_in[k] + c]);
+  };
+  with_act(a.act, [&](auto tag) {
+    for (long long m0 = rb * a.part_rows; m0 < m_end; m0 += kRowsAhead) {
+      const int rows = (int)min((long long)kRowsAhead, m_end - m0);
+      float g[kRowsAhead], u[kRowsAhead], da[kRowsAhead];
+#pragma unroll
+      for (int k = 0; k < kRowsAhead; ++k) {
+        g[k] = saved(0, m0 + k, ok && k < rows);
+        u[k] = saved(1, m0 + k, ok && k < rows);
+      }
+      add_planes(a, a.partial + m0 * a.ldp + c, plane, rows, ok, da);
+#pragma unroll
+      for (int k = 0; k < kRowsAhead; ++k) {
+        if (k >= rows) break;  // warp-uniform
+        const long long m = m0 + k;
+        float f;
+        const float df = act_grad_of<sizeof(T) == 4, decltype(tag)::value>(g[k], a.slope, f);
+        const float dg = da[k] * (u[k] * df), du = da[k] * f;
+        s0 += dg;
+        s1 += du;
+        if (ok) {
+          from_f32(dg, static_cast<T*>(a.o[0])[m * a.ldo[0] + c]);
+          from_f32(du, static_cast<T*>(a.o[1])[m * a.ldo[1] + c]);
+          if (a.y) from_f32(f * u[k], static_cast<T*>(a.y)[m * a.ldy + c]);
+        }
+      }
+    }
+  });
+  if (a.colpart && ok) {
+    float* o = a.colpart + rb * a.ldcp + c;
+    o[0] = s0;
+    o[a.N] = s1;
+  }
+}
+
+// ------------------------------------------------------------ a few rows
+//
+// Up to 8 rows: bound by reading both weights once.  A cluster of S CTAs takes
+// COLS accumulators, half of them gate and half up columns of the same hidden
+// columns, each CTA one slice of K; the S partial results meet in distributed
+// shared memory and the cluster's warps run the epilogue, so the call is one
+// launch without a workspace.  Each CTA: 256 threads, each with a ring of
+// 16-byte pieces of its weight that it alone fills (asynchronous copies) and
+// reads, so the stream needs no barriers and the depth of the ring, not the
+// registers, sets the bytes in flight; the rows of x are in shared memory as
+// fp32.  A thread keeps 16 bytes of columns and walks down K (runs of 128 bytes
+// of either weight per 128 accumulators in 16 bits).  All CTAs of a launch are
+// resident at once.
+
+constexpr int kFewX = 4096;  // values of x staged at a time (all rows)
+constexpr int kFewRing = 8;  // pieces of a thread's ring
+
+template <int MT, int COLS>
+struct FewShape {
+  static constexpr int kPerSm = MT <= 2 ? 4 : MT == 4 ? 3 : 2;  // CTAs an SM holds (registers)
+  static constexpr int kChunk = kFewX / MT;
+  // ring (the reduction takes its place), x, this CTA's sums
+  static constexpr int kRing = kFewRing * kThreads * 16;
+  static constexpr int kSmem = kRing + kFewX * 4 + MT * COLS * 4;
+  static_assert(8 * MT * COLS * 4 <= kRing, "reduction in the ring's place");
+};
+
+template <typename T, int MT, int COLS>
+__global__ void __launch_bounds__(kThreads, FewShape<MT, COLS>::kPerSm)
+    glu_few_kernel(const GluArgs a, int cluster, int slice, int w_vec) {
+  using Shape = FewShape<MT, COLS>;
+  constexpr int N = RowVec<T>::N;
+  constexpr int HALF = COLS / 2;      // hidden columns of a cluster
+  constexpr int LPR = COLS / N;       // lanes across the accumulators
+  constexpr int KP = kThreads / LPR;  // rows of the weights per step
+  constexpr int CHUNK = Shape::kChunk;
+  constexpr int D = kFewRing;
+  static_assert(LPR <= 32 && HALF % 32 == 0, "columns of a CTA");
+  extern __shared__ __align__(16) uint8_t few_smem[];
+  float* xs = reinterpret_cast<float*>(few_smem + Shape::kRing);  // [k][MT]
+  float* red = reinterpret_cast<float*>(few_smem);                // [warp][MT][COLS]
+  float* part = xs + kFewX;  // [MT][COLS]: this CTA's sums, read by the cluster
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint4* ring = reinterpret_cast<uint4*>(few_smem) + tid;  // slot i at [i * kThreads]
+  pdl_wait();
+  pdl_launch_dependents();
+  const int rank = blockIdx.x % cluster;
+  const int c0 = (int)(blockIdx.x / cluster) * HALF;
+  const int k_lo = rank * slice, k_hi = min(a.K, k_lo + slice);
+  const T* x = static_cast<const T*>(a.x);
+  const int which = tid % LPR / (LPR / 2);  // gate or up
+  const long long ldw = which ? a.ldw[1] : a.ldw[0];
+  const int c = c0 + tid % (LPR / 2) * N, cols = a.N - c;
+  const T* w = static_cast<const T*>(which ? a.w[1] : a.w[0]) + c;
+  const int k_first = tid / LPR;
+
+  float acc[MT][N];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < N; ++j) acc[m][j] = 0.f;
+
+  for (int kc = k_lo; kc < k_hi; kc += CHUNK) {
+    const int len = min(CHUNK, k_hi - kc);
+    if (kc > k_lo) __syncthreads();  // the previous chunk has been read
+    // step s: row k_first + s KP of the chunk
+    const T* wp = w + (long long)(kc + k_first) * ldw;
+    const long long step = (long long)KP * ldw;
+    const int steps = (len - k_first + KP - 1) / KP;
+    auto issue = [&](int st, int slot) {
+      if (st < steps) few_issue(ring + slot * kThreads, wp + st * step, cols, w_vec);
+      few_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < D - 1; ++i) issue(i, i);
+#pragma unroll 4
+    for (int i = tid; i < len * MT; i += kThreads) {
+      const int m = MT == 1 ? 0 : i / len, k = i - m * len;  // coalesced along k
+      xs[k * MT + m] = m < a.T ? to_f32(x[m * a.ldx + kc + k]) : 0.f;
+    }
+    __syncthreads();
+    for (int s0 = 0; s0 < steps; s0 += D) {
+#pragma unroll
+      for (int i = 0; i < D; ++i) {
+        few_wait<D - 2>();  // step s0 + i has landed
+        if (s0 + i < steps) {
+          F2 wv[N / 2];
+          float xv[MT];
+          unpack_piece<T>(ring[i * kThreads], wv);
+          const float* xk = xs + (k_first + (s0 + i) * KP) * MT;
+          if constexpr (MT >= 4) {
+#pragma unroll
+            for (int m = 0; m < MT; m += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(xk + m);
+              xv[m] = f.x;
+              xv[m + 1] = f.y;
+              xv[m + 2] = f.z;
+              xv[m + 3] = f.w;
+            }
+          } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) xv[m] = xk[m];
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+              const F2 r = fma2(f2(xv[m]), wv[j / 2], f2(acc[m][j], acc[m][j + 1]));
+              acc[m][j] = r.x;
+              acc[m][j + 1] = r.y;
+            }
+        }
+        issue(s0 + i + D - 1, (i + D - 1) % D);
+      }
+    }
+    few_wait<0>();
+  }
+
+  // this CTA's sums into part[m][accumulator]
+  __syncthreads();  // every thread is done with its ring
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) acc[m][j] += __shfl_xor_sync(0xffffffffu, acc[m][j], o);
+      if (lane < LPR) red[(warp * MT + m) * COLS + lane * N + j] = acc[m][j];
+    }
+  __syncthreads();
+  for (int i = tid; i < MT * COLS; i += kThreads) {
+    float s = red[i];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += red[q * MT * COLS + i];
+    part[i] = s;
+  }
+  ptx::cluster_sync();  // every CTA's sums are in place (a cluster of one: a block barrier)
+
+  // Epilogue: (row, 32-column group) units dealt over the cluster's warps.
+  const uint32_t part0 = ptx::smem_u32(part);
+  constexpr int G = HALF / 32;
+  const int units = G * (int)a.T;
+  for (int u = rank + cluster * warp; u < units; u += cluster * (kThreads / 32)) {
+    const int m = u / G, g = u % G;
+    if (c0 + g * 32 >= a.N) continue;  // warp-uniform
+    const int cc = c0 + g * 32 + lane;
+    const bool ok = cc < a.N;
+    const float bg = bias_of(a.bias[0], cc, ok), bu = bias_of(a.bias[1], cc, ok);
+    float z[2] = {0.f, 0.f};
+    for (int r = 0; r < cluster; ++r)  // in slice order
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        z[k] += ld_cluster_f32(ptx::mapa_shared(
+            part0 + (uint32_t)(m * COLS + k * HALF + g * 32 + lane) * 4u, (uint32_t)r));
+    with_act(a.act, [&](auto tag) {
+      glu_out<T, decltype(tag)::value>(a, m, cc, ok, z[0], z[1], bg, bu);
+    });
+  }
+  ptx::cluster_sync();  // no CTA leaves while its sums may still be read
+}
+
+template <typename T, int MT, int COLS>
+mlp_status few_launch(const GluArgs& a, cudaStream_t st) {
+  using Shape = FewShape<MT, COLS>;
+  static PerDevice configured;
+  if (!allow_smem(configured, glu_few_kernel<T, MT, COLS>, Shape::kSmem)) return MLP_ERR_CUDA;
+  // the widest cluster with which all CTAs are resident (on 152 SMs) and each
+  // still has 64 of K
+  const long long tiles = (a.N + COLS / 2 - 1) / (COLS / 2);
+  int cluster = 8;
+  while (cluster > 1 && (tiles * cluster > 152 * Shape::kPerSm || a.K < 64 * cluster)) --cluster;
+  const int per = (a.K + cluster - 1) / cluster;
+  const int slice = (per + 63) / 64 * 64;
+  if (tiles * cluster > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
+  const int w_vec = aligned16(a.w[0]) && aligned16(a.w[1]) && a.ldw[0] * sizeof(T) % 16 == 0 &&
+                    a.ldw[1] * sizeof(T) % 16 == 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = Shape::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  LaunchScope ls("glu_fwd_few", st, a.T, a.N, a.K);
+  cudaLaunchKernelEx(&cfg, glu_few_kernel<T, MT, COLS>, a, cluster, slice, w_vec);
+  return launch_status();
+}
+
+template <typename T, int MT>
+mlp_status few_cols(const GluArgs& a, cudaStream_t st) {
+  // 128 accumulators a cluster (longer runs of the weights) where they still
+  // give enough CTAs
+  if constexpr (MT <= 4) {
+    if ((long long)a.N / 64 * 8 >= 304) return few_launch<T, MT, 128>(a, st);
+  }
+  return few_launch<T, MT, 64>(a, st);
+}
+
+template <typename T>
+mlp_status few_rows(const GluArgs& a, cudaStream_t st) {
+  if (a.T <= 1) return few_cols<T, 1>(a, st);
+  if (a.T <= 2) return few_cols<T, 2>(a, st);
+  if (a.T <= 4) return few_cols<T, 4>(a, st);
+  return few_cols<T, 8>(a, st);
+}
+
+template <typename T>
+mlp_status finish_launch(const GluArgs& a, bool bwd, cudaStream_t st) {
+  const int groups = (a.N + 31) / 32;
+  const int unit_rows = bwd ? a.part_rows : kRowsAhead;
+  const long long units = (a.T + unit_rows - 1) / unit_rows * groups;
+  const long long blocks = (units + kThreads / 32 - 1) / (kThreads / 32);
+  if (blocks > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
+  LaunchScope ls(bwd ? "glu_bwd_finish" : "glu_fwd_finish", st, a.T, a.N, a.splits);
+  launch_k(bwd ? glu_finish_bwd_kernel<T> : glu_finish_fwd_kernel<T>, dim3((unsigned)blocks),
+           dim3(kThreads), 0, st, a, groups, units);
+  return launch_status();
+}
+
+}  // namespace
+
+// Up to 8 rows for fp32, whose tiled product computes 128 rows whatever T is.
+// In 16 bits the tensor cores take over once the FMAs, not the reading of the
+// weights, bound this kernel.
+bool glu_takes_few(long long T, int K, int N, int dtype) {
+  if (dtype == MLP_DTYPE_F32) return T <= 8;
+  return T <= 2 || (T <= 8 && (long long)K * N <= (1ll << 21));
+}
+
+mlp_status launch_glu_few(const GluArgs& a, cudaStream_t st) {
+  switch (a.dtype) {
+    case MLP_DTYPE_BF16: return few_rows<__nv_bfloat16>(a, st);
+    case MLP_DTYPE_F16: return few_rows<__half>(a, st);
+    default: return few_rows<float>(a, st);
+  }
+}
+
+mlp_status launch_glu_finish(const GluArgs& a, bool bwd, cudaStream_t st) {
+  switch (a.dtype) {
+    case MLP_DTYPE_BF16: return finish_launch<__nv_bfloat16>(a, bwd, st);
+    case MLP_DTYPE_F16: return finish_launch<__half>(a, bwd, st);
+    default: return finish_launch<float>(a, bwd, st);
+  }
+}
+
+}  // namespace mlp

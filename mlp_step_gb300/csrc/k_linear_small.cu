@@ -10,6 +10,7 @@
 
 #include "act.cuh"
 #include "ckpt8.cuh"
+#include "few_rows.cuh"
 #include "kernels.cuh"
 #include "ptx.cuh"
 #include "rowvec.cuh"
@@ -351,23 +352,6 @@ struct FewShape {
   static_assert(8 * MT * COLS * 4 <= kRing, "reduction in the ring's place");
 };
 
-// One piece of W into the thread's slot: asynchronously where it is whole and
-// aligned, else value by value (the same thread reads it, in program order).
-template <typename T>
-__device__ __forceinline__ void few_issue(uint4* slot, const T* p, int n, bool vec) {
-  if (vec && n >= RowVec<T>::N) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_u32(slot)), "l"(p)
-                 : "memory");
-  } else {
-    *slot = load_piece(p, n, false);
-  }
-}
-__device__ __forceinline__ void few_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void few_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Sums of V <= 32 values over the warp's lanes: lane L gets that of value
 // L % V.  Halving rounds as in a transposition, then a butterfly.
 template <int V>
@@ -385,12 +369,6 @@ __device__ __forceinline__ float lane_sums(float (&v)[V], int lane) {
 #pragma unroll
   for (int o = V; o < 32; o <<= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
   return v[0];
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
 }
 
 template <typename T, int MT, bool BWD, int COLS>

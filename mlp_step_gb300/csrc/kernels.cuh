@@ -277,6 +277,48 @@ mlp_status launch_linear_finish(const LinearArgs& a, bool bwd, cudaStream_t st);
 // k_linear_small.cu: the backward epilogue with dy (a.x) in the product's place.
 mlp_status launch_act_bwd(const LinearArgs& a, cudaStream_t st);
 
+// Gated units: g = x Wg + bg, u = x Wu + bu, y = f(g) u (forward), or from
+// da = dy Wd^T: dg = da u f'(g), du = da f(g), a = f(g) u and the column sums
+// of dg and du (backward).  Index 0: gate, 1: up.
+struct GluArgs {
+  int dtype;
+  long long T;
+  int K, N;  // contracted and hidden widths
+  const void* x;  // [T][K] (backward: dy)
+  long long ldx;
+  const void* w[2];  // forward [K][N] each; backward w[0] [N][K]
+  long long ldw[2];
+  int act;
+  float slope;
+  const float* bias[2];
+  void* y;  // forward y, backward a (nullable)
+  long long ldy;
+  void* o[2];  // forward: kept g and u (nullable); backward: dg and du
+  long long ldo[2];
+  const void* in[2];  // backward: saved g and u, or q / scale
+  long long ld_in[2];
+  int8_t* q[2];  // forward: g and u in 8 bits (out); backward: (in)
+  long long ldq[2];
+  uint8_t* scale[2];
+  long long lds[2];
+  float* colpart;  // backward: fp32 rows of ldcp, each N partial sums of dg, then N of du
+  int part_rows;   // rows of dg and du to a row of colpart: 32 in the tensor-core tiles
+  long long ldcp;
+  float* partial;  // fp32 planes [T][ldp] of raw sums: splits of them for the gate (backward:
+  long long ldp;   // da), then as many for the up projection
+  int splits;
+};
+// k_glu.cu: tcgen05 kernel of 16-bit operands.  splits > 1: raw partial sums
+// into a.partial, to be finished by launch_glu_finish.
+mlp_status launch_glu_tc(const GluArgs& a, bool bwd, cudaStream_t st);
+// Split count of that kernel (from the shape alone).
+int glu_tc_splits(long long T, int K, int N, bool bwd);
+// k_glu_small.cu: forward of a few rows, all types, one launch.
+bool glu_takes_few(long long T, int K, int N, int dtype);
+mlp_status launch_glu_few(const GluArgs& a, cudaStream_t st);
+// k_glu_small.cu: the epilogue over the planes of raw sums (a.partial).
+mlp_status launch_glu_finish(const GluArgs& a, bool bwd, cudaStream_t st);
+
 // Host helpers (api.cu)
 unsigned long long wait_limit_ns();
 // MLP_ORDER_LINEAR in effect (mlp_set_reduction_order)?
@@ -284,7 +326,7 @@ bool linear_order();
 bool encode_tmap_bf16_2d(CUtensorMap* map, const void* base, unsigned long long inner,
                          unsigned long long outer, unsigned long long row_stride_bytes,
                          unsigned box_inner, unsigned box_outer);
-// Bytes, 64 of them to a box row (64-byte swizzle).
+// Bytes, 64 or 32 of them to a box row (the swizzle of that width).
 bool encode_tmap_u8_2d(CUtensorMap* map, const void* base, unsigned long long inner,
                        unsigned long long outer, unsigned long long row_stride_bytes,
                        unsigned box_inner, unsigned box_outer);
