@@ -71,6 +71,9 @@ typedef int mlp_status;
 #define MLP_ACT_SILU 5               /* u / (1 + exp(-u)); of an infinite u, all of
                                         them and their derivatives give their limits */
 
+#define MLP_GATE_PLAIN 0             /* a gate as it is given                        */
+#define MLP_GATE_SIGMOID 1           /* 1 / (1 + exp(-z)) of what is given           */
+
 #define MLP_PREC_FP32 0              /* fp32 operands, fp32 SIMT kernels             */
 #define MLP_PREC_BF16 1              /* bf16 operands, fp32 accumulation in tensor
                                         memory, fp32 epilogue ([vk] "The Debugging
@@ -592,6 +595,71 @@ mlp_status mlp_glu_bwd(const void* dy, int lddy, const void* w_down, int ldw, in
                        const uint8_t* u_scale, int ldus, void* dg, int lddg, void* du, int lddu,
                        float* db_gate, float* db_up, void* a_out, int lda, void* workspace,
                        size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------- dropout
+ * y = residual + keep x / (1 - p) (residual nullable), all [T][d] of dtype F32,
+ * BF16 or F16; y may be x or residual.  The mask is never stored: whether value
+ * (row t, column c) is kept follows from its place by the counter-based generator
+ * Philox4x32-10, whose counter is (c / 8, t, site, step) and whose key is the
+ * seed; the four words are eight 16-bit numbers r for eight neighbouring
+ * columns, low halves first, and a value is dropped where r < floor(2^16 p + 1/2).
+ * So p counts in steps of 2^-16 (kept values are divided by that step's 1 - p,
+ * which leaves their mean as it was), and the gradient is the same call on dy
+ * (without the residual, whose gradient is dy).  Dropped values give 0 whatever
+ * they were.  rng: device memory, {seed, step}, read by the kernel, so that a
+ * captured graph draws new masks when a step between replays changes them (of
+ * step the low 32 bits count).  site tells the places apart that share them.
+ * 0 <= p <= 1; rng may be NULL where p is 0 (8-byte aligned otherwise).
+ * d at most 2^24.  Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
+mlp_status mlp_dropout(const void* x, int ldx, const void* residual, int ldr, int T, int d,
+                       int dtype, float p, const uint64_t* rng, uint32_t site, void* y, int ldy,
+                       void* stream);
+
+/* ---------------------------------------------------------------- residual norm
+ * What stands between two blocks, in one pass: the norm of the block's output b,
+ * its gate, dropout, the scaled residual sum, and the norm before the next block.
+ * Per row of x and b [T][d]:
+ *   c = post_gain b rb,  rb = 1 / sqrt(mean_i b_i^2 + eps)   (post_norm != 0)
+ *   c = post_gain b                                          (post_norm == 0)
+ *   h = x + scale G dropout(c)
+ *   n = next_gain h rh,  rh = 1 / sqrt(mean_i h_i^2 + eps)
+ * G is the matrix `gate` [T][d] or its logistic function (gate_act), or 1 (gate
+ * NULL); dropout as in mlp_dropout (p, rng, site).  post_gain and next_gain: fp32
+ * [d], nullable (1).  h and n: outputs; n is nullable (then without next_gain and
+ * h_rstd_out).  With b NULL there is the norm of x alone: n = next_gain x rx, h
+ * NULL, and nothing that belongs to b.  b_rstd_out and h_rstd_out: fp32 [T]
+ * (nullable), rb and rh for the backward pass.  n is computed from the unrounded
+ * h.  All matrices have the type dtype (F32, BF16 or F16); statistics and
+ * arithmetic are fp32.  h may be x or b.  1 <= d <= 65536.
+ * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
+mlp_status mlp_resnorm_fwd(const void* x, int ldx, const void* b, int ldb, int dtype,
+                           int post_norm, const float* post_gain, const void* gate, int ldgate,
+                           int gate_act, float scale, float p, const uint64_t* rng,
+                           uint32_t site, int T, int d, float eps, const float* next_gain,
+                           void* h, int ldh, void* n, int ldn, float* b_rstd_out,
+                           float* h_rstd_out, void* stream);
+
+/* Backward: with dh the gradient that reaches h past the norm and dn that of n
+ * (either nullable, not both), hh = h rh, bb = b rb (or b),
+ *   t = dn next_gain;  dx = dh + rh (t - hh mean_i(t_i hh_i));  e = scale dx,
+ *   dgate = e dropout(c) G';  v = dropout(e G) (the same mask);
+ *   db = rb (v post_gain - bb mean_i(v_i post_gain_i bb_i))   (or v post_gain),
+ *   dpost_gain = sum_t v bb;  dnext_gain = sum_t dn hh   (fp32 [d], nullable,
+ *                                                        overwritten).
+ * h, h_rstd: the forward's (x and its rstd where there was no b); needed with
+ * dn.  b, gate and b_rstd (with post_norm): as in the forward; db goes with b and
+ * dgate with gate.  dx may be dh or dn, db may be b, dgate may be gate (the same
+ * pointer and pitch).  workspace: mlp_resnorm_workspace_bytes(T, d) bytes where
+ * either sum is wanted. */
+size_t mlp_resnorm_workspace_bytes(int T, int d);
+mlp_status mlp_resnorm_bwd(const void* dh, int lddh, const void* dn, int lddn, const void* h,
+                           int ldh, const float* h_rstd, const float* next_gain, const void* b,
+                           int ldb, int dtype, int post_norm, const float* post_gain,
+                           const float* b_rstd, const void* gate, int ldgate, int gate_act,
+                           float scale, float p, const uint64_t* rng, uint32_t site, int T, int d,
+                           void* dx, int lddx, void* db, int lddb, void* dgate, int lddgate,
+                           float* dpost_gain, float* dnext_gain, void* workspace, size_t ws_bytes,
+                           void* stream);
 
 #ifdef __cplusplus
 }

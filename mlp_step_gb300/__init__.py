@@ -17,7 +17,7 @@ import os
 __all__ = [
     "MlpError", "load", "lib_path",
     "MLP_ACT_NONE", "MLP_ACT_RELU", "MLP_ACT_LEAKY_RELU_SQ", "MLP_ACT_GELU",
-    "MLP_ACT_GELU_TANH", "MLP_ACT_SILU", "MLP_CKPT8_GROUP",
+    "MLP_ACT_GELU_TANH", "MLP_ACT_SILU", "MLP_CKPT8_GROUP", "MLP_GATE_PLAIN", "MLP_GATE_SIGMOID",
     "MLP_PREC_FP32", "MLP_PREC_BF16", "MLP_PREC_FP16", "MLP_DTYPE_F32", "MLP_DTYPE_BF16",
     "MLP_DTYPE_U8", "MLP_DTYPE_F16", "MLP_ORDER_FAST", "MLP_ORDER_LINEAR",
 ]
@@ -36,6 +36,8 @@ MLP_ACT_LEAKY_RELU_SQ = 2
 MLP_ACT_GELU = 3
 MLP_ACT_GELU_TANH = 4
 MLP_ACT_SILU = 5
+MLP_GATE_PLAIN = 0
+MLP_GATE_SIGMOID = 1
 MLP_PREC_FP32 = 0
 MLP_PREC_BF16 = 1
 MLP_PREC_FP16 = 2
@@ -125,6 +127,13 @@ SIGNATURES = {
     "mlp_glu_bwd": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i, _vp,
                          _i, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _vp, _sz,
                          _vp]),
+    "mlp_dropout": (_i, [_vp, _i, _vp, _i, _i, _i, _i, _f, _vp, ctypes.c_uint32, _vp, _i, _vp]),
+    "mlp_resnorm_fwd": (_i, [_vp, _i, _vp, _i, _i, _i, _vp, _vp, _i, _i, _f, _f, _vp,
+                             ctypes.c_uint32, _i, _i, _f, _vp, _vp, _i, _vp, _i, _vp, _vp, _vp]),
+    "mlp_resnorm_workspace_bytes": (_sz, [_i, _i]),
+    "mlp_resnorm_bwd": (_i, [_vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _i, _i, _i, _vp, _vp, _vp,
+                             _i, _i, _f, _f, _vp, ctypes.c_uint32, _i, _i, _vp, _i, _vp, _i, _vp,
+                             _i, _vp, _vp, _vp, _sz, _vp]),
     "mlp_act_bwd_workspace_bytes": (_sz, [_i, _i]),
     "mlp_act_bwd": (_i, [_vp, _i, _i, _i, _i, _i, _f, _vp, _i, _vp, _i, _vp, _i, _vp, _i, _vp,
                          _vp, _i, _vp, _sz, _vp]),
@@ -790,3 +799,88 @@ def mlp_glu_bwd(dy, w_down, dg, du, act=MLP_ACT_SILU, slope=0.5, g=None, u=None,
                               *_ckpt(u_ckpt, "u_ckpt", T, n, dev), dgp, lddg, dup, lddu,
                               _vec(db_gate, "db_gate", n, dev), _vec(db_up, "db_up", n, dev), ap,
                               lda, ws, wsb, _stream_of(stream, dev)), "mlp_glu_bwd")
+
+
+def _rng(rng, dev):
+    """Address of a generator's state, an int64 CUDA tensor {seed, step}; None for None."""
+    if rng is None:
+        return None
+    if rng.shape != (2,) or rng.dtype is not _torch.int64 or rng.stride(0) != 1:
+        raise ValueError("rng must be two contiguous torch.int64 values, seed and step (got %s %s)"
+                         % (rng.dtype, tuple(rng.shape)))
+    if rng.get_device() != dev:
+        raise ValueError("rng must be on the current CUDA device (got %s)" % rng.device)
+    return rng.data_ptr()
+
+
+def _site(site):
+    if not 0 <= site < 1 << 32:
+        raise ValueError("site must be in [0, 2^32) (got %s)" % site)
+    return site
+
+
+def mlp_dropout(x, y, p, rng=None, site=0, residual=None, stream=None):
+    """y = residual + keep x / (1 - p), the mask from the place of each value and
+    rng (an int64 CUDA tensor {seed, step}); the gradient is the same call on dy."""
+    T, d = x.shape
+    dev = _device(x, "x")
+    xp, ldx = _mat(x, "x", T, d, dev)
+    rp, ldr = _mat(residual, "residual", T, d, dev, x.dtype)
+    yp, ldy = _mat(y, "y", T, d, dev, x.dtype)
+    _check(load().mlp_dropout(xp, ldx, rp, ldr, T, d, _code_of(x.dtype), p, _rng(rng, dev),
+                              _site(site), yp, ldy, _stream_of(stream, dev)), "mlp_dropout")
+
+
+def mlp_resnorm_fwd(x, n=None, next_gain=None, h_rstd=None, b=None, h=None, post_norm=False,
+                    post_gain=None, b_rstd=None, gate=None, gate_act=MLP_GATE_PLAIN, scale=1.0,
+                    p=0.0, rng=None, site=0, eps=1e-6, stream=None):
+    """h = x + scale gate dropout(post_gain norm(b)) and n = next_gain norm(h) (norm:
+    over the root mean square of the row; of b only with post_norm), or n alone of
+    x where there is no b; b_rstd, h_rstd: fp32 [T] kept for the backward."""
+    T, d = x.shape
+    dev = _device(x, "x")
+    dt = x.dtype
+    xp, ldx = _mat(x, "x", T, d, dev)
+    bp, ldb = _mat(b, "b", T, d, dev, dt)
+    gp, ldg = _mat(gate, "gate", T, d, dev, dt)
+    hp, ldh = _mat(h, "h", T, d, dev, dt)
+    np_, ldn = _mat(n, "n", T, d, dev, dt)
+    _check(load().mlp_resnorm_fwd(xp, ldx, bp, ldb, _code_of(dt), 1 if post_norm else 0,
+                                  _vec(post_gain, "post_gain", d, dev), gp, ldg, gate_act, scale,
+                                  p, _rng(rng, dev), _site(site), T, d, eps,
+                                  _vec(next_gain, "next_gain", d, dev), hp, ldh, np_, ldn,
+                                  _vec(b_rstd, "b_rstd", T, dev), _vec(h_rstd, "h_rstd", T, dev),
+                                  _stream_of(stream, dev)), "mlp_resnorm_fwd")
+
+
+def mlp_resnorm_workspace_bytes(T: int, d: int) -> int:
+    """Workspace of mlp_resnorm_bwd with dpost_gain or dnext_gain."""
+    return load().mlp_resnorm_workspace_bytes(*_sizes(T, d))
+
+
+def mlp_resnorm_bwd(dx, dh=None, dn=None, h=None, h_rstd=None, next_gain=None, b=None, db=None,
+                    post_norm=False, post_gain=None, b_rstd=None, gate=None, dgate=None,
+                    gate_act=MLP_GATE_PLAIN, scale=1.0, p=0.0, rng=None, site=0, dpost_gain=None,
+                    dnext_gain=None, workspace=None, stream=None):
+    """Backward of mlp_resnorm_fwd from dh (the gradient of h past the norm) and / or
+    dn: dx, db and dgate of the inputs' type, dpost_gain and dnext_gain fp32 [d]."""
+    T, d = dx.shape
+    dev = _device(dx, "dx")
+    dt = dx.dtype
+    dxp, lddx = _mat(dx, "dx", T, d, dev)
+    dhp, lddh = _mat(dh, "dh", T, d, dev, dt)
+    dnp, lddn = _mat(dn, "dn", T, d, dev, dt)
+    hp, ldh = _mat(h, "h", T, d, dev, dt)
+    bp, ldb = _mat(b, "b", T, d, dev, dt)
+    dbp, lddb = _mat(db, "db", T, d, dev, dt)
+    gp, ldg = _mat(gate, "gate", T, d, dev, dt)
+    dgp, lddg = _mat(dgate, "dgate", T, d, dev, dt)
+    ws, wsb = _ws(workspace, dev)
+    _check(load().mlp_resnorm_bwd(dhp, lddh, dnp, lddn, hp, ldh, _vec(h_rstd, "h_rstd", T, dev),
+                                  _vec(next_gain, "next_gain", d, dev), bp, ldb, _code_of(dt),
+                                  1 if post_norm else 0, _vec(post_gain, "post_gain", d, dev),
+                                  _vec(b_rstd, "b_rstd", T, dev), gp, ldg, gate_act, scale, p,
+                                  _rng(rng, dev), _site(site), T, d, dxp, lddx, dbp, lddb, dgp,
+                                  lddg, _vec(dpost_gain, "dpost_gain", d, dev),
+                                  _vec(dnext_gain, "dnext_gain", d, dev), ws, wsb,
+                                  _stream_of(stream, dev)), "mlp_resnorm_bwd")

@@ -4,6 +4,7 @@
 
 #include <cuda.h>
 #include "common.cuh"
+#include "philox.cuh"
 
 namespace mlp {
 
@@ -318,6 +319,64 @@ bool glu_takes_few(long long T, int K, int N, int dtype);
 mlp_status launch_glu_few(const GluArgs& a, cudaStream_t st);
 // k_glu_small.cu: the epilogue over the planes of raw sums (a.partial).
 mlp_status launch_glu_finish(const GluArgs& a, bool bwd, cudaStream_t st);
+
+// k_dropout.cu: y = res + dropout(x); the *_vec flags are the launcher's own.
+struct Dropout {
+  int dtype;
+  const void* x;
+  long long ldx;
+  const void* res;  // nullable
+  long long ldr;
+  long long T;
+  int d;
+  DropArgs drop;
+  void* y;
+  long long ldy;
+  int x_vec, r_vec, y_vec;
+};
+mlp_status launch_dropout(const Dropout& p, cudaStream_t st);
+
+// k_resnorm.cu: c = post_gain b rstd(b), h = x + scale gate dropout(c),
+// n = next_gain h rstd(h), and the backward.  The *_vec flags are the launchers'
+// own.
+struct ResNorm {
+  int dtype;
+  long long T;
+  int d;
+  float eps;
+  // forward: input; backward: gradient of h besides the norm's (nullable)
+  const void* x;
+  long long ldx;
+  const void* b;  // nullable: no block output
+  long long ldb;
+  const void* z;  // nullable: no gate
+  long long ldz;
+  int sigmoid;  // gate: the logistic function of z instead of z
+  float scale;
+  int post;                // norm of b
+  const float* post_gain;  // nullable: 1
+  const float* next_gain;  // nullable: 1
+  DropArgs drop;
+  void* h;  // forward: output (nullable without b); backward: input (with dn)
+  long long ldh;
+  void* n;  // forward: output (nullable: no second norm); backward: dn, input
+  long long ldn;
+  float* b_rstd;  // forward: nullable outputs; backward: inputs
+  float* h_rstd;
+  // backward
+  void* dx;
+  long long lddx;
+  void* db;
+  long long lddb;
+  void* dz;
+  long long lddz;
+  float* part;  // rows of 2 d partial sums, dnext_gain then dpost_gain (nullable)
+  int vec;      // kXVec | ...
+};
+size_t resnorm_ws_bytes(long long T, int d);
+mlp_status launch_resnorm_fwd(const ResNorm& a, cudaStream_t st);
+mlp_status launch_resnorm_bwd(const ResNorm& a, float* dnext_gain, float* dpost_gain,
+                              cudaStream_t st);
 
 // Host helpers (api.cu)
 unsigned long long wait_limit_ns();
