@@ -11,13 +11,15 @@ namespace mlp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 4;  // pieces of a thread whose loads are in flight together
+constexpr int kPerSm = 5;  // blocks
+constexpr int kAhead = 2;  // pieces of a thread whose loads are in flight together
 
 // A thread's pieces (16 bytes) lie a grid's stride apart, row and column
-// carried along (step_rows rows and step_cols pieces, wrapping).
-template <typename T>
-__global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p, int per_row,
-                                                           long long step_rows, int step_cols) {
+// carried along (step_rows rows and step_cols pieces, wrapping).  FULL: all rows
+// are whole aligned pieces.
+template <typename T, bool FULL>
+__global__ void __launch_bounds__(kThreads, kPerSm)
+    dropout_kernel(const Dropout p, uint32_t per_row, uint32_t step_rows, uint32_t step_cols) {
   constexpr int N = RowVec<T>::N;
   pdl_wait();
   pdl_launch_dependents();
@@ -25,20 +27,22 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p, int 
   const T* res = static_cast<const T*>(p.res);
   T* y = static_cast<T*>(p.y);
   const DropKey key(p.drop);
-  const long long first = (long long)blockIdx.x * kThreads + threadIdx.x;
-  long long row = first / per_row;
-  int q = (int)(first - row * per_row);
-  while (row < p.T) {
+  // pitches and row numbers are ints at the C boundary: one widening
+  // multiplication a piece
+  const uint32_t rows = (uint32_t)p.T;
+  const uint32_t ldx = (uint32_t)p.ldx, ldr = (uint32_t)p.ldr, ldy = (uint32_t)p.ldy;
+  const unsigned long long first = (unsigned long long)blockIdx.x * kThreads + threadIdx.x;
+  uint32_t row = (uint32_t)(first / per_row), q = (uint32_t)(first % per_row);
+  while (row < rows) {
     uint4 rx[kAhead], rr[kAhead];
-    long long at[kAhead];
-    int col[kAhead];
+    uint32_t at[kAhead], col[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       at[k] = row;
       col[k] = q * N;
-      const int n = row < p.T ? p.d - col[k] : 0;
-      rx[k] = load_piece(x + row * p.ldx + col[k], n, p.x_vec);
-      if (res) rr[k] = load_piece(res + row * p.ldr + col[k], n, p.r_vec);
+      const int n = row < rows ? p.d - (int)col[k] : 0;
+      rx[k] = load_piece_of<FULL>(x + (uint64_t)row * ldx + col[k], n, p.x_vec);
+      if (res) rr[k] = load_piece_of<FULL>(res + (uint64_t)row * ldr + col[k], n, p.r_vec);
       row += step_rows;
       q += step_cols;
       if (q >= per_row) {
@@ -48,13 +52,14 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p, int 
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      if (at[k] >= p.T) break;
+      if (at[k] >= rows) break;
       F2 v[N / 2];
       unpack_piece<T>(rx[k], v);
       if (p.drop.threshold) {
-        const uint32_t bits = drop_bits<N>(p.drop, key, (uint32_t)at[k], col[k]);
+        uint32_t w[N / 2];
+        drop_words<N>(p.drop, key, at[k], (int)col[k], w);
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) v[j] = drop2(v[j], bits, 2 * j, p.drop.scale);
+        for (int j = 0; j < N / 2; ++j) v[j] = drop2(v[j], w[j], key, p.drop.scale);
       }
       if (res) {
         F2 r[N / 2];
@@ -62,31 +67,37 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const Dropout p, int 
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) v[j] = add2(v[j], r[j]);
       }
-      store_piece(y + at[k] * p.ldy + col[k], reinterpret_cast<const float(&)[N]>(v),
-                  p.d - col[k], p.y_vec);
+      store_piece_of<FULL>(y + (uint64_t)at[k] * ldy + col[k],
+                           reinterpret_cast<const float(&)[N]>(v), p.d - (int)col[k], p.y_vec);
     }
   }
 }
 
+template <typename T, bool FULL>
+mlp_status launch_of(const Dropout& p, cudaStream_t st) {
+  constexpr int N = RowVec<T>::N;
+  const uint32_t per_row = (uint32_t)((p.d - 1) / N + 1);
+  const long long pieces = p.T * per_row;
+  const long long most = (long long)num_sms() * kPerSm;
+  long long blocks = (pieces + kThreads - 1) / kThreads;
+  if (blocks > most) blocks = most;
+  const uint32_t step = (uint32_t)blocks * kThreads;
+  LaunchScope ls("dropout", st, p.T, p.d, sizeof(T));
+  launch_k(dropout_kernel<T, FULL>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p, per_row,
+           step / per_row, step % per_row);
+  return launch_status();
+}
+
 template <typename T>
 mlp_status launch_t(Dropout p, cudaStream_t st) {
-  constexpr int N = RowVec<T>::N;
   auto vec = [](const void* m, long long ld) {
     return m && aligned16(m) && ld * (long long)sizeof(T) % 16 == 0;
   };
   p.x_vec = vec(p.x, p.ldx);
   p.r_vec = vec(p.res, p.ldr);
   p.y_vec = vec(p.y, p.ldy);
-  const int per_row = (p.d - 1) / N + 1;
-  const long long pieces = p.T * per_row;
-  const long long most = (long long)num_sms() * 8;
-  long long blocks = (pieces + kThreads - 1) / kThreads;
-  if (blocks > most) blocks = most;
-  const long long step = blocks * kThreads;
-  LaunchScope ls("dropout", st, p.T, p.d, sizeof(T));
-  launch_k(dropout_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0, st, p, per_row,
-           step / per_row, (int)(step % per_row));
-  return launch_status();
+  const bool full = p.d % RowVec<T>::N == 0 && p.x_vec && p.y_vec && (!p.res || p.r_vec);
+  return full ? launch_of<T, true>(p, st) : launch_of<T, false>(p, st);
 }
 
 }  // namespace

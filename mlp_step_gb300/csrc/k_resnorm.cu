@@ -30,33 +30,78 @@ namespace mlp {
 
 namespace {
 
+constexpr int kBlockWidth = 8192;  // widest row held by one block
 constexpr int kMaxCluster = 8;
+
+// Values of a row per thread: two 16-byte pieces.
+template <typename T>
+constexpr int vpt() {
+  return 2 * RowVec<T>::N;
+}
 
 // Bits of ResNorm::vec: 16-byte pieces of that matrix's rows are aligned.
 enum { kXVec = 1, kBVec = 2, kZVec = 4, kHVec = 8, kNVec = 16, kDxVec = 32, kDbVec = 64,
        kDzVec = 128 };
 
+// What the blocks of a cluster exchange for a row's sum: each sends its own to
+// every block's `in` (asynchronous stores, counted in bytes by the receiver's
+// barrier) and waits for all.  Nothing else is ordered by it, where a cluster
+// barrier would wait for the row's stores.  Two turns: a block sends for a turn
+// again only after the other turn's sums arrived, which were sent after all
+// threads had read this one's.
+struct Exchange {
+  float in[2][kMaxCluster];
+  unsigned long long full[2];
+};
+
+__device__ __forceinline__ void send_f32(uint32_t to, float v, uint32_t bar) {
+  asm volatile(
+      "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(to),
+      "r"(__float_as_uint(v)), "r"(bar)
+      : "memory");
+}
+
 // Sums of one value over the row: over a block's warps, then (WIDE) over the
-// cluster's blocks in rank order.  Callers alternate `turn`, so that one barrier
-// a call (each) is enough.
+// cluster's blocks in rank order.  Callers' turns alternate, so that one barrier
+// a call (each) is enough.  A wait that runs out is recorded, and no more are
+// begun: the rows are then finished with what is there.
 template <int WPR, bool WIDE, int ROWS>
 struct RowSum {
   float (*part)[ROWS][WPR];  // [2][ROWS][WPR]
-  float* mine;               // WIDE: [2] in this block's shared memory
-  int slot, warp_in_row, cluster, turn;
+  Exchange* ex;              // WIDE: in this block's shared memory
+  int slot, warp_in_row, rank, cluster;
+  unsigned long long wait_ns;
+  int* err;
+  int turn = 0;
+  uint32_t phase = 0;  // of this turn's barrier
+  bool dead = false;
   __device__ __forceinline__ float operator()(float v) {
     float s[1] = {v};
     row_sums<WPR>(s, part[turn][slot], slot, warp_in_row);
     if constexpr (WIDE) {
-      if (threadIdx.x == 0) mine[turn] = s[0];
-      ptx::cluster_sync();
-      const uint32_t at = ptx::smem_u32(mine + turn);
+      uint64_t* bar = reinterpret_cast<uint64_t*>(&ex->full[turn]);
+      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)cluster * 4u);
+      if (threadIdx.x < 32 && (int)threadIdx.x < cluster)
+        send_f32(ptx::mapa_shared(ptx::smem_u32(&ex->in[turn][rank]), threadIdx.x), s[0],
+                 ptx::mapa_shared(ptx::smem_u32(bar), threadIdx.x));
+      if (!dead)
+        dead = !ptx::mbar_wait_cluster_bounded(bar, phase, wait_ns, err, DEVERR_TIMEOUT_PEER);
       s[0] = 0.f;
-      for (int r = 0; r < cluster; ++r)
-        s[0] += ld_cluster_f32(ptx::mapa_shared(at, (uint32_t)r));
+      for (int r = 0; r < cluster; ++r) s[0] += ex->in[turn][r];
+      if (turn) phase ^= 1;
     }
     turn ^= 1;
     return s[0];
+  }
+  __device__ __forceinline__ void begin() {
+    if constexpr (WIDE) {
+      if (threadIdx.x == 0) {
+        ptx::mbar_init(reinterpret_cast<uint64_t*>(&ex->full[0]), 1);
+        ptx::mbar_init(reinterpret_cast<uint64_t*>(&ex->full[1]), 1);
+        ptx::fence_mbar_init();
+      }
+      ptx::cluster_sync();
+    }
   }
 };
 
@@ -79,89 +124,192 @@ __device__ __forceinline__ F2 logistic2(F2 z, F2& one_minus) {
   return s;
 }
 
+// A thread's pieces of the rows ahead, in shared memory: MATS matrices, AHEAD + 1
+// rows, each 16-byte piece at a place of its own that this thread alone fills
+// (asynchronous copies) and reads.  So what is in flight takes no registers and
+// no barrier.
+template <typename T, int MATS, int AHEAD, int THREADS>
+struct Ring {
+  static constexpr int NV = vpt<T>() / RowVec<T>::N;
+  static constexpr int BYTES = MATS * (AHEAD + 1) * NV * THREADS * 16;
+  uint4* mine;
+  int stage;  // of the current row
+  __device__ __forceinline__ uint4* at(int s, int m, int i) const {
+    return mine + ((s * MATS + m) * NV + i) * THREADS;
+  }
+  // piece i of matrix m of the current row
+  __device__ __forceinline__ uint4 operator()(int m, int i) const { return *at(stage, m, i); }
+  // Zeros in a piece that no row has, which no copy writes.
+  __device__ __forceinline__ void clear(int i) const {
+#pragma unroll
+    for (int s = 0; s <= AHEAD; ++s)
+#pragma unroll
+      for (int m = 0; m < MATS; ++m) *at(s, m, i) = make_uint4(0, 0, 0, 0);
+  }
+};
+
+// Piece of n values at p into its place: asynchronously in 16 bytes, for fp32 rows
+// that start anywhere in 4 (10,007 x 1,001 fp32 forward 99 us with loads and
+// stores of the thread's own), else by the thread.
+template <typename T, bool FULL>
+__device__ __forceinline__ void issue_piece(uint4* place, const T* p, int n, bool vec) {
+  if constexpr (FULL) {
+    n = RowVec<T>::N;
+    vec = true;
+  }
+  if constexpr (sizeof(T) == 4 && !FULL) {
+    if (!(vec && n >= 4)) {
+      const uint32_t to = ptx::smem_u32(place);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < n)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4 * j), "l"(p + j)
+                       : "memory");
+        else
+          asm volatile("st.shared.b32 [%0], 0;" ::"r"(to + 4 * j) : "memory");
+      }
+      return;
+    }
+  }
+  few_issue(place, p, n, vec);
+}
+
+// Values past the row's end, where 0 times a scale that is not finite would not
+// be 0 (FULL: whole pieces only).
+template <bool FULL, int N>
+__device__ __forceinline__ void zero_past(F2 (&v)[N / 2], int n) {
+  if (FULL ? n <= 0 : n < N) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+      if (FULL || 2 * j >= n) v[j].x = 0.f;
+      if (FULL || 2 * j + 1 >= n) v[j].y = 0.f;
+    }
+  }
+}
+
+// Where a thread's share of the rows lies: piece i at column c0 + i 32 WPR N.
+template <typename T, int WPR, bool WIDE>
+struct Place {
+  static constexpr int ROWS = HeldBlock<WPR>::ROWS, N = RowVec<T>::N;
+  static constexpr int WIDTH = vpt<T>() * 32 * WPR;  // columns of a block
+  int slot, t, rank, c0;
+  uint32_t row, stride;  // (unsigned: a row number past T is below 2^32)
+  __device__ __forceinline__ explicit Place(int cluster) {
+    slot = threadIdx.x / (32 * WPR);
+    t = threadIdx.x % (32 * WPR);
+    rank = WIDE ? (int)(blockIdx.x % cluster) : 0;
+    c0 = rank * WIDTH + t * N;
+    stride = WIDE ? gridDim.x / cluster : gridDim.x * ROWS;
+    row = WIDE ? blockIdx.x / cluster : blockIdx.x * ROWS + slot;
+  }
+  __device__ __forceinline__ int col(int i) const { return c0 + i * 32 * WPR * N; }
+  // this thread's first value of row r of a matrix (pitches are ints at the C
+  // boundary: one widening multiplication)
+  __device__ __forceinline__ T* in(const void* m, long long ld, uint32_t r) const {
+    return static_cast<T*>(const_cast<void*>(m)) + ((uint64_t)r * (uint32_t)ld + c0);
+  }
+};
+
 template <typename T, int WPR, bool FULL, bool WIDE>
 __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
-                                  (sizeof(T) == 2 ? 768 : 512) / HeldBlock<WPR>::THREADS)
+                                  1024 / HeldBlock<WPR>::THREADS)
     resnorm_fwd_kernel(const ResNorm p, int cluster) {
-  constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
+  constexpr int N = RowVec<T>::N, NV = vpt<T>() / N, ROWS = HeldBlock<WPR>::ROWS;
+  constexpr int THREADS = HeldBlock<WPR>::THREADS, step = 32 * WPR * N;
   __shared__ float part[2][ROWS][WPR];
-  __shared__ float mine[2];
+  __shared__ Exchange ex;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   pdl_wait();
   pdl_launch_dependents();
-  const int slot = threadIdx.x / (32 * WPR), t = threadIdx.x % (32 * WPR);
-  const int rank = WIDE ? (int)(blockIdx.x % cluster) : 0;
-  const int c_first = rank * kHeldWidth + t * N;  // piece i at c_first + i 32 WPR N
-  const long long stride = WIDE ? gridDim.x / cluster : (long long)gridDim.x * ROWS;
-  long long row = WIDE ? blockIdx.x / cluster : (long long)blockIdx.x * ROWS + slot;
+  Place<T, WPR, WIDE> at(cluster);
+  const uint32_t rows = (uint32_t)p.T;
   const float inv_d = 1.f / (float)p.d;
   const bool block = p.b != nullptr, gate = p.z != nullptr;
   const DropKey key(p.drop);
-  RowSum<WPR, WIDE, ROWS> sum{part, mine, slot, t >> 5, cluster, 0};
-  uint4 rx[NV], rb[NV], rz[NV];
-  auto load = [&](long long r) {
+  RowSum<WPR, WIDE, ROWS> sum{part, &ex, at.slot, at.t >> 5, at.rank, cluster, p.wait_ns, p.err};
+  sum.begin();
+  Ring<T, 3, 1, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 0};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c_first + i * 32 * WPR * N;
-      const int n = r < p.T ? p.d - c : 0;
-      rx[i] = load_piece_of<FULL>(static_cast<const T*>(p.x) + r * p.ldx + c, n, p.vec & kXVec);
-      if (block)
-        rb[i] = load_piece_of<FULL>(static_cast<const T*>(p.b) + r * p.ldb + c, n, p.vec & kBVec);
-      if (gate)
-        rz[i] = load_piece_of<FULL>(static_cast<const T*>(p.z) + r * p.ldz + c, n, p.vec & kZVec);
+  for (int i = 0; i < NV; ++i)
+    if (FULL && at.col(i) >= p.d) ring.clear(i);
+  auto issue = [&](int s, uint32_t r) {
+    if (r < rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = p.d - at.col(i);
+        if (FULL && n <= 0) continue;
+        issue_piece<T, FULL>(ring.at(s, 0, i), at.in(p.x, p.ldx, r) + i * step, n, p.vec & kXVec);
+        if (block)
+          issue_piece<T, FULL>(ring.at(s, 1, i), at.in(p.b, p.ldb, r) + i * step, n, p.vec & kBVec);
+        if (gate)
+          issue_piece<T, FULL>(ring.at(s, 2, i), at.in(p.z, p.ldz, r) + i * step, n, p.vec & kZVec);
+      }
     }
+    few_commit();
   };
-  load(row);
-  for (; row < p.T; row += stride) {  // uniform over the threads that share a row
+  issue(0, at.row);
+  for (; at.row < rows; at.row += at.stride) {  // uniform over the threads that share a row
+    const uint32_t row = at.row;
+    issue(ring.stage ^ 1, row + at.stride);
+    few_wait<1>();
     F2 v[NV][N / 2];
     if (block) {
       F2 s2 = f2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        unpack_piece<T>(rb[i], v[i]);
+        unpack_piece<T>(ring(1, i), v[i]);
+        zero_past<FULL, N>(v[i], p.d - at.col(i));
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) s2 = fma2(v[i][j], v[i][j], s2);
       }
       float rho = 1.f;
       if (p.post) {
         rho = rsqrtf(sum(s2.x + s2.y) * inv_d + p.eps);  // two ulp
-        if (p.b_rstd && rank == 0 && t == 0) p.b_rstd[row] = rho;
+        if (p.b_rstd && at.rank == 0 && at.t == 0) p.b_rstd[row] = rho;
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = c_first + i * 32 * WPR * N, n = p.d - c;
+        const int c = at.col(i), n = p.d - c;
         float g[N];
         load_param<N, FULL>(p.post_gain, c, n, 1.f, g);
-        const uint32_t bits =
-            p.drop.threshold ? drop_bits<N>(p.drop, key, (uint32_t)row, c) : 0u;
-        F2 x[N / 2], z[N / 2];
-        unpack_piece<T>(rx[i], x);
-        if (gate) unpack_piece<T>(rz[i], z);
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          F2 e = mul2(mul2(v[i][j], f2(rho)), f2(g[2 * j], g[2 * j + 1]));
-          if (p.drop.threshold) e = drop2(e, bits, 2 * j, p.drop.scale);
-          if (gate) {
-            F2 rest;
-            e = mul2(e, p.sigmoid ? logistic2<T>(z[j], rest) : z[j]);
-          }
-          v[i][j] = fma2(e, f2(p.scale), x[j]);
-          // past the row's end (where 0 times a scale that is not finite would not be 0)
-          if (2 * j >= n) v[i][j].x = 0.f;
-          if (2 * j + 1 >= n) v[i][j].y = 0.f;
+        for (int j = 0; j < N / 2; ++j)
+          v[i][j] = mul2(mul2(v[i][j], f2(rho)), f2(g[2 * j], g[2 * j + 1]));
+        if (p.drop.threshold) {
+          uint32_t w[N / 2];
+          drop_words<N>(p.drop, key, row, c, w);
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) v[i][j] = drop2(v[i][j], w[j], key, p.drop.scale);
         }
+        if (gate) {
+          F2 z[N / 2], rest;
+          unpack_piece<T>(ring(2, i), z);
+          if (p.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) z[j] = logistic2<T>(z[j], rest);
+          }
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) v[i][j] = mul2(v[i][j], z[j]);
+        }
+        F2 x[N / 2];
+        unpack_piece<T>(ring(0, i), x);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) v[i][j] = fma2(v[i][j], f2(p.scale), x[j]);
+        zero_past<FULL, N>(v[i], n);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) unpack_piece<T>(rx[i], v[i]);
+      for (int i = 0; i < NV; ++i) {
+        unpack_piece<T>(ring(0, i), v[i]);
+        zero_past<FULL, N>(v[i], p.d - at.col(i));
+      }
     }
-    load(row + stride);
     if (p.h) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = c_first + i * 32 * WPR * N;
-        store_piece_of<FULL>(static_cast<T*>(p.h) + row * p.ldh + c,
-                             reinterpret_cast<const float(&)[N]>(v[i]), p.d - c, p.vec & kHVec);
-      }
+      for (int i = 0; i < NV; ++i)
+        store_piece_of<FULL>(at.in(p.h, p.ldh, row) + i * step,
+                             reinterpret_cast<const float(&)[N]>(v[i]), p.d - at.col(i),
+                             p.vec & kHVec);
     }
     if (p.n) {
       F2 s2 = f2(0.f);
@@ -170,93 +318,123 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) s2 = fma2(v[i][j], v[i][j], s2);
       const float rho = rsqrtf(sum(s2.x + s2.y) * inv_d + p.eps);
-      if (p.h_rstd && rank == 0 && t == 0) p.h_rstd[row] = rho;
+      if (p.h_rstd && at.rank == 0 && at.t == 0) p.h_rstd[row] = rho;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = c_first + i * 32 * WPR * N, n = p.d - c;
+        const int c = at.col(i), n = p.d - c;
         float g[N];
         load_param<N, FULL>(p.next_gain, c, n, 1.f, g);
 #pragma unroll
         for (int j = 0; j < N / 2; ++j)
           v[i][j] = mul2(mul2(v[i][j], f2(rho)), f2(g[2 * j], g[2 * j + 1]));
-        store_piece_of<FULL>(static_cast<T*>(p.n) + row * p.ldn + c,
+        store_piece_of<FULL>(at.in(p.n, p.ldn, row) + i * step,
                              reinterpret_cast<const float(&)[N]>(v[i]), n, p.vec & kNVec);
       }
     }
+    ring.stage ^= 1;
   }
   if constexpr (WIDE) ptx::cluster_sync();  // no block leaves while its sums may be read
 }
 
+// Rows ahead in the backward's ring: one; none for fp32 rows of 512 threads, where
+// a second row would not fit: the places of what has been read are filled with
+// the next row's at once.
+template <typename T, int WPR>
+constexpr int bwd_ahead() {
+  return sizeof(T) == 4 && WPR == 32 ? 0 : 1;
+}
+
 template <typename T, int WPR, bool FULL, bool WIDE>
 __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
-                                  sizeof(T) == 2 ? 512 / HeldBlock<WPR>::THREADS : 1)
+                                  WPR == 32 ? 1 : 512 / HeldBlock<WPR>::THREADS)
     resnorm_bwd_kernel(const ResNorm p, int cluster) {
-  constexpr int N = RowVec<T>::N, NV = kPerThread / N, ROWS = HeldBlock<WPR>::ROWS;
+  constexpr int N = RowVec<T>::N, NV = vpt<T>() / N, ROWS = HeldBlock<WPR>::ROWS;
+  constexpr int THREADS = HeldBlock<WPR>::THREADS, step = 32 * WPR * N;
   __shared__ float part[2][ROWS][WPR];
-  __shared__ float mine[2];
-  extern __shared__ __align__(16) float sums_mem[];  // ROWS > 1: one slot's values at a time
+  __shared__ Exchange ex;
+  extern __shared__ __align__(16) uint8_t ring_mem[];
   pdl_wait();
   pdl_launch_dependents();
-  const int slot = threadIdx.x / (32 * WPR), t = threadIdx.x % (32 * WPR);
-  const int rank = WIDE ? (int)(blockIdx.x % cluster) : 0;
-  const int c_first = rank * kHeldWidth + t * N;
-  const long long stride = WIDE ? gridDim.x / cluster : (long long)gridDim.x * ROWS;
-  long long row = WIDE ? blockIdx.x / cluster : (long long)blockIdx.x * ROWS + slot;
+  Place<T, WPR, WIDE> at(cluster);
+  const uint32_t rows = (uint32_t)p.T;
   const float inv_d = 1.f / (float)p.d;
   const bool block = p.b != nullptr, gate = p.z != nullptr, next = p.n != nullptr;
   const DropKey key(p.drop);
-  RowSum<WPR, WIDE, ROWS> sum{part, mine, slot, t >> 5, cluster, 0};
+  RowSum<WPR, WIDE, ROWS> sum{part, &ex, at.slot, at.t >> 5, at.rank, cluster, p.wait_ns, p.err};
+  sum.begin();
   F2 dnext[NV][N / 2], dpost[NV][N / 2];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) dnext[i][j] = dpost[i][j] = f2(0.f);
-  uint4 rx[NV], rn[NV], rh[NV];
-  auto load = [&](long long r) {
+  constexpr int AHEAD = bwd_ahead<T, WPR>();
+  Ring<T, 5, AHEAD, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 0};
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c_first + i * 32 * WPR * N;
-      const int n = r < p.T ? p.d - c : 0;
-      if (next) {
-        rn[i] = load_piece_of<FULL>(static_cast<const T*>(p.n) + r * p.ldn + c, n, p.vec & kNVec);
-        rh[i] = load_piece_of<FULL>(static_cast<const T*>(p.h) + r * p.ldh + c, n, p.vec & kHVec);
+  for (int i = 0; i < NV; ++i)
+    if (FULL && at.col(i) >= p.d) ring.clear(i);
+  float rh_n = 0.f, rb_n = 0.f;  // the next row's
+  // dn, h and dh of row r, one group of copies, and b and z, another
+  auto issue_norm = [&](int s, uint32_t r) {
+    if (r < rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = p.d - at.col(i);
+        if (FULL && n <= 0) continue;
+        if (next) {
+          issue_piece<T, FULL>(ring.at(s, 0, i), at.in(p.n, p.ldn, r) + i * step, n, p.vec & kNVec);
+          issue_piece<T, FULL>(ring.at(s, 1, i), at.in(p.h, p.ldh, r) + i * step, n, p.vec & kHVec);
+        }
+        if (p.x)
+          issue_piece<T, FULL>(ring.at(s, 2, i), at.in(p.x, p.ldx, r) + i * step, n, p.vec & kXVec);
       }
-      rx[i] = p.x ? load_piece_of<FULL>(static_cast<const T*>(p.x) + r * p.ldx + c, n,
-                                        p.vec & kXVec)
-                  : make_uint4(0, 0, 0, 0);
+      if (next) rh_n = p.h_rstd[r];
     }
+    few_commit();
   };
-  load(row);
-  for (; row < p.T; row += stride) {
-    // this row's b and z are in flight over the first reduction
-    uint4 rb[NV], rz[NV];
+  auto issue_block = [&](int s, uint32_t r) {
+    if (r < rows) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c_first + i * 32 * WPR * N;
-      if (block)
-        rb[i] = load_piece_of<FULL>(static_cast<const T*>(p.b) + row * p.ldb + c, p.d - c,
-                                    p.vec & kBVec);
-      if (gate)
-        rz[i] = load_piece_of<FULL>(static_cast<const T*>(p.z) + row * p.ldz + c, p.d - c,
-                                    p.vec & kZVec);
+      for (int i = 0; i < NV; ++i) {
+        const int n = p.d - at.col(i);
+        if (FULL && n <= 0) continue;
+        if (block)
+          issue_piece<T, FULL>(ring.at(s, 3, i), at.in(p.b, p.ldb, r) + i * step, n, p.vec & kBVec);
+        if (gate)
+          issue_piece<T, FULL>(ring.at(s, 4, i), at.in(p.z, p.ldz, r) + i * step, n, p.vec & kZVec);
+      }
+      if (p.post) rb_n = p.b_rstd[r];
+    }
+    few_commit();
+  };
+  issue_norm(0, at.row);
+  issue_block(0, at.row);
+  for (; at.row < rows; at.row += at.stride) {
+    const uint32_t row = at.row, then = row + at.stride;
+    const float rh = rh_n, rb = p.post ? rb_n : 1.f;
+    if constexpr (AHEAD) {
+      issue_norm(ring.stage ^ 1, then);
+      issue_block(ring.stage ^ 1, then);
+      few_wait<2>();
+    } else {
+      few_wait<1>();
     }
     F2 v[NV][N / 2];  // dh'
     if (next) {
-      const float rho = p.h_rstd[row];
       F2 hh[NV][N / 2];
       F2 s2 = f2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = c_first + i * 32 * WPR * N, n = p.d - c;
+        const int c = at.col(i), n = p.d - c;
         float g[N];
         load_param<N, FULL>(p.next_gain, c, n, 1.f, g);
-        unpack_piece<T>(rn[i], v[i]);
-        unpack_piece<T>(rh[i], hh[i]);
+        unpack_piece<T>(ring(0, i), v[i]);
+        unpack_piece<T>(ring(1, i), hh[i]);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) hh[i][j] = mul2(hh[i][j], f2(rh));
+        zero_past<FULL, N>(v[i], n);
+        zero_past<FULL, N>(hh[i], n);
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
-          hh[i][j] = mul2(hh[i][j], f2(rho));
-          if (2 * j >= n) hh[i][j].x = 0.f;
-          if (2 * j + 1 >= n) hh[i][j].y = 0.f;
           dnext[i][j] = fma2(v[i][j], hh[i][j], dnext[i][j]);
           v[i][j] = mul2(v[i][j], f2(g[2 * j], g[2 * j + 1]));
           s2 = fma2(v[i][j], hh[i][j], s2);
@@ -264,92 +442,118 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       }
       const float m = sum(s2.x + s2.y) * inv_d;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        F2 x[N / 2];
-        unpack_piece<T>(rx[i], x);
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < N / 2; ++j)
-          v[i][j] = fma2(fma2(hh[i][j], f2(-m), v[i][j]), f2(rho), x[j]);
+          v[i][j] = mul2(fma2(hh[i][j], f2(-m), v[i][j]), f2(rh));
+      if (p.x) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          F2 x[N / 2];
+          unpack_piece<T>(ring(2, i), x);
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) v[i][j] = add2(v[i][j], x[j]);
+        }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) unpack_piece<T>(rx[i], v[i]);
+      for (int i = 0; i < NV; ++i) unpack_piece<T>(ring(2, i), v[i]);
     }
-    load(row + stride);
+    if constexpr (!AHEAD) {
+      issue_norm(0, then);
+      few_wait<1>();
+    }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c_first + i * 32 * WPR * N;
-      store_piece_of<FULL>(static_cast<T*>(p.dx) + row * p.lddx + c,
-                           reinterpret_cast<const float(&)[N]>(v[i]), p.d - c, p.vec & kDxVec);
+    for (int i = 0; i < NV; ++i)
+      store_piece_of<FULL>(at.in(p.dx, p.lddx, row) + i * step,
+                           reinterpret_cast<const float(&)[N]>(v[i]), p.d - at.col(i),
+                           p.vec & kDxVec);
+    if (!block) {
+      if constexpr (AHEAD) ring.stage ^= 1;
+      else issue_block(0, then);
+      continue;
     }
-    if (!block) continue;
-    const float rho = p.post ? p.b_rstd[row] : 1.f;
     F2 s2 = f2(0.f);
     F2 bb[NV][N / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = c_first + i * 32 * WPR * N, n = p.d - c;
+      const int c = at.col(i), n = p.d - c;
       float g[N];
       load_param<N, FULL>(p.post_gain, c, n, 1.f, g);
-      const uint32_t bits = p.drop.threshold ? drop_bits<N>(p.drop, key, (uint32_t)row, c) : 0u;
-      unpack_piece<T>(rb[i], bb[i]);
-      F2 z[N / 2], dz[N / 2];
-      if (gate) unpack_piece<T>(rz[i], z);
+      uint32_t w[N / 2];
+      if (p.drop.threshold) drop_words<N>(p.drop, key, row, c, w);
+      unpack_piece<T>(ring(3, i), bb[i]);
 #pragma unroll
       for (int j = 0; j < N / 2; ++j) {
-        bb[i][j] = mul2(bb[i][j], f2(rho));
-        if (2 * j >= n) bb[i][j].x = 0.f;
-        if (2 * j + 1 >= n) bb[i][j].y = 0.f;
-        const F2 g2 = f2(g[2 * j], g[2 * j + 1]);
-        F2 e = mul2(v[i][j], f2(p.scale));
-        if (gate) {
-          const F2 c2 = mul2(bb[i][j], g2);
-          dz[j] = mul2(e, p.drop.threshold ? drop2(c2, bits, 2 * j, p.drop.scale) : c2);
-          if (p.sigmoid) {
+        bb[i][j] = mul2(bb[i][j], f2(rb));
+        v[i][j] = mul2(v[i][j], f2(p.scale));
+      }
+      zero_past<FULL, N>(bb[i], n);
+      zero_past<FULL, N>(v[i], n);
+      if (gate) {
+        F2 z[N / 2], dz[N / 2];
+        unpack_piece<T>(ring(4, i), z);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+          dz[j] = mul2(bb[i][j], f2(g[2 * j], g[2 * j + 1]));
+          if (p.drop.threshold) dz[j] = drop2(dz[j], w[j], key, p.drop.scale);
+          dz[j] = mul2(dz[j], v[i][j]);
+        }
+        if (p.sigmoid) {
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) {
             F2 rest;
             z[j] = logistic2<T>(z[j], rest);
             dz[j] = mul2(dz[j], mul2(z[j], rest));
           }
-          e = mul2(e, z[j]);
         }
-        if (p.drop.threshold) e = drop2(e, bits, 2 * j, p.drop.scale);
-        dpost[i][j] = fma2(e, bb[i][j], dpost[i][j]);
-        v[i][j] = mul2(e, g2);
+        store_piece_of<FULL>(at.in(p.dz, p.lddz, row) + i * step,
+                             reinterpret_cast<const float(&)[N]>(dz), n, p.vec & kDzVec);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) v[i][j] = mul2(v[i][j], z[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) {
+        if (p.drop.threshold) v[i][j] = drop2(v[i][j], w[j], key, p.drop.scale);
+        dpost[i][j] = fma2(v[i][j], bb[i][j], dpost[i][j]);
+        v[i][j] = mul2(v[i][j], f2(g[2 * j], g[2 * j + 1]));
         s2 = fma2(v[i][j], bb[i][j], s2);
       }
-      if (gate)
-        store_piece_of<FULL>(static_cast<T*>(p.dz) + row * p.lddz + c,
-                             reinterpret_cast<const float(&)[N]>(dz), n, p.vec & kDzVec);
     }
-    float m = 0.f;
-    if (p.post) m = sum(s2.x + s2.y) * inv_d;
+    if constexpr (AHEAD) ring.stage ^= 1;
+    else issue_block(0, then);
+    if (p.post) {
+      const float m = sum(s2.x + s2.y) * inv_d;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = c_first + i * 32 * WPR * N;
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j)
-        if (p.post) v[i][j] = mul2(fma2(bb[i][j], f2(-m), v[i][j]), f2(rho));
-      store_piece_of<FULL>(static_cast<T*>(p.db) + row * p.lddb + c,
-                           reinterpret_cast<const float(&)[N]>(v[i]), p.d - c, p.vec & kDbVec);
+        for (int j = 0; j < N / 2; ++j)
+          v[i][j] = mul2(fma2(bb[i][j], f2(-m), v[i][j]), f2(rb));
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      store_piece_of<FULL>(at.in(p.db, p.lddb, row) + i * step,
+                           reinterpret_cast<const float(&)[N]>(v[i]), p.d - at.col(i),
+                           p.vec & kDbVec);
   }
   if (p.part) {
-    // this block's partial sums, row slots added in order
+    // this block's partial sums, row slots added in order, in the ring's place
+    few_wait<0>();
     float* out = p.part + (long long)(WIDE ? blockIdx.x / cluster : blockIdx.x) * 2 * p.d;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       F2(&a)[NV][N / 2] = which ? dpost : dnext;
       if constexpr (ROWS > 1) {
-        F2* sums = reinterpret_cast<F2*>(sums_mem) + t;  // value k at [k * 32 WPR]
+        F2* sums = reinterpret_cast<F2*>(ring_mem) + at.t;  // value k at [k * 32 WPR]
         for (int k = 1; k < ROWS; ++k) {
           __syncthreads();
-          if (slot == k)
+          if (at.slot == k)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
               for (int j = 0; j < N / 2; ++j) sums[(i * N / 2 + j) * 32 * WPR] = a[i][j];
           __syncthreads();
-          if (slot == 0)
+          if (at.slot == 0)
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -357,10 +561,10 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
                 a[i][j] = add2(a[i][j], sums[(i * N / 2 + j) * 32 * WPR]);
         }
       }
-      if (slot == 0)
+      if (at.slot == 0)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int c = c_first + i * 32 * WPR * N;
+          const int c = at.col(i);
           float* o = out + (long long)which * p.d + c;
 #pragma unroll
           for (int j = 0; j < N / 2; ++j) {
@@ -408,10 +612,15 @@ int bwd_blocks(long long T, int d) {
 template <typename T, int WPR, bool FULL, bool WIDE>
 mlp_status fwd_of(const ResNorm& p, cudaStream_t st) {
   using B = HeldBlock<WPR>;
+  constexpr int kWidth = vpt<T>() * 32 * WPR;
   auto kernel = resnorm_fwd_kernel<T, WPR, FULL, WIDE>;
   static PerDevice per_sm;
-  const int cluster = WIDE ? (p.d + kHeldWidth - 1) / kHeldWidth : 1;
-  int blocks = walk_blocks(kernel, B::THREADS, per_sm, WIDE ? 1ll << 40 : p.T, B::ROWS);
+  constexpr int kSmem = Ring<T, 3, 1, B::THREADS>::BYTES;
+  static_assert(kSmem <= 225 * 1024, "shared memory");
+  static PerDevice configured;
+  if (!allow_smem(configured, kernel, kSmem)) return MLP_ERR_CUDA;
+  const int cluster = WIDE ? (p.d + kWidth - 1) / kWidth : 1;
+  int blocks = walk_blocks(kernel, B::THREADS, per_sm, WIDE ? 1ll << 40 : p.T, B::ROWS, kSmem);
   if (WIDE) {
     blocks /= cluster;
     if (blocks < 1) blocks = 1;
@@ -419,21 +628,26 @@ mlp_status fwd_of(const ResNorm& p, cudaStream_t st) {
     blocks *= cluster;
   }
   LaunchScope ls("resnorm_fwd", st, p.T, p.d, sizeof(T));
-  return launch_rows(kernel, blocks, B::THREADS, 0, cluster, p, st);
+  return launch_rows(kernel, blocks, B::THREADS, kSmem, cluster, p, st);
 }
 
 template <typename T, int WPR, bool FULL, bool WIDE>
 mlp_status bwd_of(const ResNorm& p, int* rows, cudaStream_t st) {
   using B = HeldBlock<WPR>;
+  constexpr int kWidth = vpt<T>() * 32 * WPR;
   auto kernel = resnorm_bwd_kernel<T, WPR, FULL, WIDE>;
   static PerDevice per_sm;
-  const int cluster = WIDE ? (p.d + kHeldWidth - 1) / kHeldWidth : 1;
-  int resident = walk_blocks(kernel, B::THREADS, per_sm, WIDE ? 1ll << 40 : p.T, B::ROWS);
+  constexpr int kSmem = Ring<T, 5, bwd_ahead<T, WPR>(), B::THREADS>::BYTES;
+  static_assert(kSmem <= 225 * 1024, "shared memory");
+  static_assert(B::ROWS == 1 || 32 * WPR * vpt<T>() * 4 <= kSmem, "sums in the ring's place");
+  static PerDevice configured;
+  if (!allow_smem(configured, kernel, kSmem)) return MLP_ERR_CUDA;
+  const int cluster = WIDE ? (p.d + kWidth - 1) / kWidth : 1;
+  int resident = walk_blocks(kernel, B::THREADS, per_sm, WIDE ? 1ll << 40 : p.T, B::ROWS, kSmem);
   if (WIDE) resident = resident / cluster > 0 ? resident / cluster : 1;
   if (resident < *rows) *rows = resident;
-  const size_t smem = B::ROWS > 1 && p.part ? (size_t)32 * WPR * kPerThread * 4 : 0;
   LaunchScope ls("resnorm_bwd", st, p.T, p.d, sizeof(T));
-  return launch_rows(kernel, *rows * cluster, B::THREADS, (int)smem, cluster, p, st);
+  return launch_rows(kernel, *rows * cluster, B::THREADS, kSmem, cluster, p, st);
 }
 
 template <typename T, int WPR, bool WIDE, bool BWD>
@@ -446,6 +660,9 @@ mlp_status of_form(const ResNorm& p, bool full, int* rows, cudaStream_t st) {
 
 template <typename T, bool BWD>
 mlp_status of_type(ResNorm p, int* rows, cudaStream_t st) {
+  p.wait_ns = wait_limit_ns();
+  p.err = device_error_word();
+  if (!p.err) return MLP_ERR_CUDA;
   p.vec = 0;
   bool full = p.d % RowVec<T>::N == 0;
   auto look = [&](const void* m, long long ld, int bit) {
@@ -463,12 +680,15 @@ mlp_status of_type(ResNorm p, int* rows, cudaStream_t st) {
     look(p.db, p.lddb, kDbVec);
     look(p.dz, p.lddz, kDzVec);
   }
-  if (p.d <= 512) return of_form<T, 1, false, BWD>(p, full, rows, st);
-  if (p.d <= 1024) return of_form<T, 2, false, BWD>(p, full, rows, st);
-  if (p.d <= 2048) return of_form<T, 4, false, BWD>(p, full, rows, st);
-  if (p.d <= 4096) return of_form<T, 8, false, BWD>(p, full, rows, st);
-  if (p.d <= kHeldWidth) return of_form<T, 16, false, BWD>(p, full, rows, st);
-  return of_form<T, 16, true, BWD>(p, full, rows, st);
+  const int warps = (p.d + 32 * vpt<T>() - 1) / (32 * vpt<T>());
+  if (warps <= 1) return of_form<T, 1, false, BWD>(p, full, rows, st);
+  if (warps <= 2) return of_form<T, 2, false, BWD>(p, full, rows, st);
+  if (warps <= 4) return of_form<T, 4, false, BWD>(p, full, rows, st);
+  if (warps <= 8) return of_form<T, 8, false, BWD>(p, full, rows, st);
+  constexpr int kMost = kBlockWidth / (32 * vpt<T>());  // 16, or 32 for fp32
+  if (kMost > 16 && warps <= 16) return of_form<T, 16, false, BWD>(p, full, rows, st);
+  if (warps <= kMost) return of_form<T, kMost, false, BWD>(p, full, rows, st);
+  return of_form<T, kMost, true, BWD>(p, full, rows, st);
 }
 
 template <bool BWD>

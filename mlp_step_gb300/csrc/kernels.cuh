@@ -372,6 +372,8 @@ struct ResNorm {
   long long lddz;
   float* part;  // rows of 2 d partial sums, dnext_gain then dpost_gain (nullable)
   int vec;      // kXVec | ...
+  unsigned long long wait_ns;
+  int* err;
 };
 size_t resnorm_ws_bytes(long long T, int d);
 mlp_status launch_resnorm_fwd(const ResNorm& a, cudaStream_t st);

@@ -78,10 +78,11 @@ bool row_vec(const void* p, long long ld, int esz, int bytes) {
 // Blocks of a row-walking launch: as many as are resident at once (more would
 // run as a second, ragged wave), at most one per row set.
 template <typename K>
-int walk_blocks(K kernel, int threads, PerDevice& resident, long long T, int rows_per_block) {
+int walk_blocks(K kernel, int threads, PerDevice& resident, long long T, int rows_per_block,
+                int smem = 0) {
   const int per_sm = resident.get(current_device(), [&] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess) {
       cudaGetLastError();
       n = 1;
     }

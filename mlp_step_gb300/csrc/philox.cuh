@@ -18,9 +18,12 @@ struct DropArgs {
   float scale;         // of what is kept: 2^16 / (2^16 - threshold), 0 where nothing is
 };
 
+// What a thread keeps of them.
 struct DropKey {
   uint32_t k0, k1, step;
+  uint32_t below;  // of 32 bits, whose upper half is a number: dropped up to here
   __device__ __forceinline__ explicit DropKey(const DropArgs& a) : k0(0), k1(0), step(0) {
+    below = (a.threshold << 16) - 1u;  // (all ones for a threshold of 2^16)
     if (a.threshold) {
       const unsigned long long seed = a.rng[0];
       k0 = (uint32_t)seed;
@@ -43,26 +46,22 @@ __device__ __forceinline__ void philox10(uint32_t (&c)[4], uint32_t k0, uint32_t
   }
 }
 
-// Bit j: value j of the N (4 or 8) from column c (a multiple of N) of `row` is kept.
+// The random words of the N (4 or 8) values from column c (a multiple of N) of
+// `row`: two numbers each, the even column's in the low half.
 template <int N>
-__device__ __forceinline__ uint32_t drop_bits(const DropArgs& a, const DropKey& key, uint32_t row,
-                                              int c) {
-  uint32_t w[4] = {(uint32_t)c >> 3, row, a.site, key.step};
-  philox10(w, key.k0, key.k1);
-  uint32_t bits = 0;
+__device__ __forceinline__ void drop_words(const DropArgs& a, const DropKey& key, uint32_t row,
+                                           int c, uint32_t (&w)[N / 2]) {
+  uint32_t v[4] = {(uint32_t)c >> 3, row, a.site, key.step};
+  philox10(v, key.k0, key.k1);
 #pragma unroll
-  for (int j = 0; j < N / 2; ++j) {
-    const uint32_t v = N == 8 ? w[j] : (c & 4) ? w[2 + j] : w[j];
-    bits |= (uint32_t)((v & 0xffffu) >= a.threshold) << (2 * j);
-    bits |= (uint32_t)((v >> 16) >= a.threshold) << (2 * j + 1);
-  }
-  return bits;
+  for (int j = 0; j < N / 2; ++j) w[j] = N == 8 ? v[j] : (c & 4) ? v[2 + j] : v[j];
 }
 
-// What is kept times its scale, 0 where dropped (a dropped NaN or infinity too).
-__device__ __forceinline__ F2 drop2(F2 v, uint32_t bits, int j, float scale) {
+// What is kept of two values times its scale, 0 where dropped (a dropped NaN or
+// infinity too).
+__device__ __forceinline__ F2 drop2(F2 v, uint32_t word, const DropKey& key, float scale) {
   const F2 s = mul2(v, f2(scale));
-  return f2(bits >> j & 1 ? s.x : 0.f, bits >> (j + 1) & 1 ? s.y : 0.f);
+  return f2((word << 16) > key.below ? s.x : 0.f, word > key.below ? s.y : 0.f);
 }
 
 }  // namespace mlp
