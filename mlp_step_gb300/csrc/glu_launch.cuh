@@ -22,19 +22,19 @@ namespace {
 
 template <int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
 __global__ void
-    __launch_bounds__(GluLayout<0, BN, STAGES, EW, AROWS, MODE != kGluFwd>::THREADS, 1)
+    __launch_bounds__(GluLayout<0, BN, STAGES, EW, AROWS, MODE>::THREADS, 1)
     glu_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluParams p) {
   glu_body<0, BN, STAGES, EW, AROWS, H16, MODE, false>(maps, p);
 }
 
 template <int BN, int STAGES, int EW, int AROWS, int H16, int MODE>
 mlp_status launch_glu_single(const GluMaps& maps, const GluParams& p, cudaStream_t st) {
-  using L = GluLayout<0, BN, STAGES, EW, AROWS, MODE != kGluFwd>;
+  using L = GluLayout<0, BN, STAGES, EW, AROWS, MODE>;
   auto kernel = glu_kernel<BN, STAGES, EW, AROWS, H16, MODE>;
   static PerDevice configured;
   if (!allow_smem(configured, kernel, L::SMEM)) return MLP_ERR_CUDA;
   const int grid = p.units < num_sms() ? p.units : num_sms();
-  LaunchScope ls(MODE != kGluFwd ? "glu_bwd" : "glu_fwd", st, p.a.T, p.a.N, p.a.K);
+  LaunchScope ls(glu_is_bwd(MODE) ? "glu_bwd" : "glu_fwd", st, p.a.T, p.a.N, p.a.K);
   launch_k(kernel, dim3(grid), dim3(L::THREADS), L::SMEM, st, maps, p);
   return launch_status();
 }

@@ -34,27 +34,32 @@ namespace {
 constexpr int GBK = 64;
 constexpr int kGluBox = 2048;  // 32 rows x 64 bytes (8-bit values: 32 bytes a row)
 
-// MODE: forward, backward from 16-bit pre-activations, backward from 8-bit ones.
-enum { kGluFwd, kGluBwd, kGluBwdCkpt };
+// MODE: forward that keeps its pre-activations in 16 bits, or in 8 or not at all;
+// backward from 16-bit pre-activations, from 8-bit ones.
+enum { kGluFwdKeep, kGluFwd, kGluBwd, kGluBwdCkpt };
+constexpr bool glu_is_bwd(int mode) { return mode >= kGluBwd; }
 
 // EW: epilogue warps.  AROWS: rows of x that a stage holds; with fewer than 128
 // the MMA reads on into what follows, which only feeds accumulator rows that
 // are never stored.  The forward's accumulator is half gate, half up columns of
-// the same hidden columns.  Staging boxes of an epilogue warp: y, g, u;
-// backward: saved g and u, dg, du, a.
-template <int PAIR, int BN, int STAGES, int EW, int AROWS, bool BWD>
+// the same hidden columns.  Staging boxes of an epilogue warp: y, g, u (8-bit
+// ones are half as large); backward: saved g and u, dg, du, a.
+template <int PAIR, int BN, int STAGES, int EW, int AROWS, int MODE>
 struct GluLayout {
+  static constexpr bool BWD = glu_is_bwd(MODE);
   static constexpr int A_BYTES = AROWS * GBK * 2;
   static constexpr int B_COLS = PAIR ? 128 : BN;  // operand columns staged per CTA
   static constexpr int B_BYTES = B_COLS * GBK * 2;
   static constexpr int ACC = PAIR ? 256 : BN;       // accumulator columns per CTA
   static constexpr int HID = BWD ? ACC : ACC / 2;   // hidden columns of a tile
-  static constexpr int SPAN = HID / (EW / 4);       // of an epilogue warp
-  static constexpr int STAGE = (BWD ? 5 : 3) * kGluBox;
+  static constexpr int PIECES = HID / 32;           // units of a lane quarter's warps in a tile
+  static constexpr int SHARE = EW / 4;              // ... and these warps
+  static constexpr int KEPT = MODE == kGluFwdKeep || MODE == kGluBwd ? kGluBox : kGluBox / 2;
+  static constexpr int STAGE = (BWD ? 3 : 1) * kGluBox + 2 * KEPT;
   static constexpr int THREADS = 64 + 32 * EW;      // + producer, MMA issuer
   static constexpr int SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + EW * STAGE + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * ACC;
-  static_assert(SPAN % 32 == 0, "an epilogue unit is 32 columns");
+  static_assert(PIECES >= SHARE, "every epilogue warp has a unit of every tile");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -81,8 +86,9 @@ __device__ __forceinline__ void store_raw(float* p, const F2 (&v)[16]) {
 // that the epilogue's scalar work is decided when it is compiled.
 template <int PAIR, int BN, int STAGES, int EW, int AROWS, int H16, int MODE, bool WHOLE>
 __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p) {
-  constexpr bool BWD = MODE != kGluFwd, CK = MODE == kGluBwdCkpt;
-  using L = GluLayout<PAIR, BN, STAGES, EW, AROWS, BWD>;
+  constexpr bool BWD = glu_is_bwd(MODE), CK = MODE == kGluBwdCkpt;
+  using L = GluLayout<PAIR, BN, STAGES, EW, AROWS, MODE>;
+  constexpr int KEPT = L::KEPT;
   static_assert(AROWS == 128 || (STAGES * L::B_BYTES >= 16384 && !PAIR), "reads past the x ring");
   constexpr int ACC = L::ACC, HID = L::HID;
   constexpr int TILE_M = PAIR ? 256 : 128;
@@ -278,16 +284,17 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
   } else {
     const int ew = warp - 2;
     const int quarter = warp & 3;  // tensor-memory lanes [32 q, 32 q + 32)
-    const int c_first = (ew >> 2) * L::SPAN;
     const uint32_t tempty0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(tempty), 0) : 0u;
     uint8_t* in_box = stg + ew * L::STAGE;                  // backward: saved g, u
-    uint8_t* out_box = in_box + (BWD ? 2 * kGluBox : 0);    // y, g, u; dg, du, a
+    uint8_t* out_box = in_box + (BWD ? 2 * KEPT : 0);       // y, g, u; dg, du, a
     bool stores = false;      // a store of this warp may still read its boxes
     bool in_flight = false;   // saved values are on their way
     uint32_t in_phase = 0;
     uint32_t sb[2] = {0, 0};  // their scale bytes of this row
 
-    // One unit is 32 columns of the warp's 32 rows; units go tile by tile.
+    // One unit is 32 columns of the warp's 32 rows; units go tile by tile, dealt
+    // in turn over the warps of a lane quarter: `start` is this warp's first in
+    // the tile.
     struct Unit {
       int row0, n0;
     };
@@ -297,7 +304,7 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
         int tm, tn;
         tile_of(p, splits == 1 ? u : u / splits, tm, tn);
         t.row0 = tm * TILE_M + (int)rank * 128 + quarter * 32;
-        t.n0 = tn * HID + c_first + c;
+        t.n0 = tn * HID + c;
       }
       return t;
     };
@@ -322,10 +329,10 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
       if (tma_in) {
         __syncwarp();
         if (lane == 0) {
-          ptx::mbar_arrive_expect_tx(&in_full[ew], CK ? kGluBox : 2 * kGluBox);
+          ptx::mbar_arrive_expect_tx(&in_full[ew], 2 * KEPT);
 #pragma unroll
           for (int k = 0; k < 2; ++k)
-            ptx::tma_load_2d(in_box + k * kGluBox, &maps.in[k], &in_full[ew], t.n0, t.row0);
+            ptx::tma_load_2d(in_box + k * KEPT, &maps.in[k], &in_full[ew], t.n0, t.row0);
         }
         in_flight = true;
       }
@@ -344,15 +351,19 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
       }
     };
 
-    Unit next = locate(worker, 0);
+    int start = ew >> 2;
+    Unit next = locate(worker, 32 * start);
     if (BWD && splits == 1) request(next);
     for (int u = worker; u < p.units; u += workers) {
       if (*s_abort) break;
       bool ready = false;
-      for (int c = 0; c < L::SPAN; c += 32) {
+      int c = 32 * start;
+      start -= L::PIECES % L::SHARE;
+      if (start < 0) start += L::SHARE;
+      for (; c < HID; c += 32 * L::SHARE) {
         const Unit t = next;
-        const bool last = c + 32 >= L::SPAN;
-        next = last ? locate(u + workers, 0) : locate(u, c + 32);
+        const bool last = c + 32 * L::SHARE >= HID;
+        next = last ? locate(u + workers, 32 * start) : locate(u, c + 32 * L::SHARE);
         const long long m = (long long)t.row0 + lane;
         const bool row_ok = m < a.T;
         if (!ready) {
@@ -371,7 +382,7 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
         const int cols = WHOLE ? 32 : min(32, a.N - t.n0);
         const int rows = (int)min(32ll, a.T - t.row0);
         const uint32_t from = tmem_base + ((uint32_t)(quarter * 32) << 16) +
-                              (uint32_t)(acc * ACC + c_first + c);
+                              (uint32_t)(acc * ACC + c);
         F2 v[16], w[16];
         if (!WHOLE && splits > 1) {
           // raw sums: gate planes, then (forward) up planes
@@ -398,22 +409,21 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
           boxes_free();
           // one projection's piece: bias, and the kept form into its box
           auto projection = [&](int k, F2 (&z)[16]) {
-            float4 b4[8];
             const float* bias = a.bias[k];
             if (bias && whole) {
+              float4 b4[8];
 #pragma unroll
               for (int j = 0; j < 8; ++j) b4[j] = load_bias4(bias + t.n0 + 4 * j);
+              take32(from + k * HID, z);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                z[2 * j] = add2(z[2 * j], f2(b4[j].x, b4[j].y));
+                z[2 * j + 1] = add2(z[2 * j + 1], f2(b4[j].z, b4[j].w));
+              }
             } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) b4[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+              take32(from + k * HID, z);
             }
-            take32(from + k * HID, z);
             if (k == 1 && last) release();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              z[2 * j] = add2(z[2 * j], f2(b4[j].x, b4[j].y));
-              z[2 * j + 1] = add2(z[2 * j + 1], f2(b4[j].z, b4[j].w));
-            }
             if (!whole) {
               // columns past N: zero, so that they take no part in the 8-bit
               // group's scale
@@ -424,8 +434,8 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
                 z[j].y = o ? z[j].y + (bias ? __ldg(bias + t.n0 + 2 * j + 1) : 0.f) : 0.f;
               }
             }
-            uint8_t* kept = out_box + (1 + k) * kGluBox;
-            if (a.o[k]) {
+            uint8_t* kept = out_box + kGluBox + k * KEPT;
+            if (MODE == kGluFwdKeep) {
               pack_row<H16>(kept, 64, lane, 0, z);
             } else if (a.q[k]) {
               uint32_t q[8];
@@ -446,7 +456,7 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
 #pragma unroll
           for (int j = 0; j < 16; ++j) v[j] = mul2(v[j], w[j]);
           pack_row<H16>(out_box, 64, lane, 0, v);
-          const bool kept = a.o[0] || a.q[0];
+          const bool kept = MODE == kGluFwdKeep || a.q[0];
           const bool by_y = tma_y && whole, by_o = kept && tma_o && whole;
           if (by_y || by_o) {
             ptx::fence_proxy_async_smem();
@@ -456,7 +466,7 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
               if (by_y) ptx::tma_store_2d(&maps.y, out_box, t.n0, t.row0);
               if (by_o) {
                 ptx::tma_store_2d(&maps.o[0], out_box + kGluBox, t.n0, t.row0);
-                ptx::tma_store_2d(&maps.o[1], out_box + 2 * kGluBox, t.n0, t.row0);
+                ptx::tma_store_2d(&maps.o[1], out_box + kGluBox + KEPT, t.n0, t.row0);
               }
               ptx::bulk_commit_group();
             }
@@ -466,9 +476,9 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
           if (kept && !by_o) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              if (a.o[k]) copy16(out_box + (1 + k) * kGluBox, a.o[k], a.ldo[k]);
+              if (MODE == kGluFwdKeep) copy16(out_box + kGluBox + k * KEPT, a.o[k], a.ldo[k]);
               else
-                warp_copy<true>(out_box + (1 + k) * kGluBox, 32,
+                warp_copy<true>(out_box + kGluBox + k * KEPT, 32,
                                 reinterpret_cast<uint8_t*>(a.q[k]) + t.row0 * a.ldq[k] + t.n0,
                                 a.ldq[k], rows, cols, 1, lane);
             }
@@ -488,11 +498,11 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               if (CK)
-                warp_copy<false>(in_box + k * kGluBox, 32,
+                warp_copy<false>(in_box + k * KEPT, 32,
                                  reinterpret_cast<uint8_t*>(a.q[k]) + t.row0 * a.ldq[k] + t.n0,
                                  a.ldq[k], rows, cols, 1, lane);
               else
-                warp_copy<false>(in_box + k * kGluBox, 64,
+                warp_copy<false>(in_box + k * KEPT, 64,
                                  static_cast<uint8_t*>(const_cast<void*>(a.in[k])) +
                                      (t.row0 * a.ld_in[k] + t.n0) * 2,
                                  a.ld_in[k] * 2, rows, cols * 2, 2, lane);
@@ -507,7 +517,7 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
 #pragma unroll
             for (int j = 0; j < RAW / 4; ++j) {
               const uint4 q = *reinterpret_cast<const uint4*>(
-                  chunk_at(in_box + k * kGluBox, CK ? 32 : 64, lane, j));
+                  chunk_at(in_box + k * KEPT, CK ? 32 : 64, lane, j));
               raw[k][4 * j] = q.x;
               raw[k][4 * j + 1] = q.y;
               raw[k][4 * j + 2] = q.z;
@@ -627,20 +637,20 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
 
 template <int STAGES, int EW, int H16, int MODE, bool WHOLE>
 __global__ void __cluster_dims__(2, 1, 1)
-    __launch_bounds__(GluLayout<1, 256, STAGES, EW, 128, MODE != kGluFwd>::THREADS, 1)
+    __launch_bounds__(GluLayout<1, 256, STAGES, EW, 128, MODE>::THREADS, 1)
     glu_pair_kernel(const __grid_constant__ GluMaps maps, const __grid_constant__ GluParams p) {
   glu_body<1, 256, STAGES, EW, 128, H16, MODE, WHOLE>(maps, p);
 }
 
 template <int STAGES, int EW, int H16, int MODE, bool WHOLE>
 mlp_status launch_glu_pair(const GluMaps& maps, const GluParams& p, cudaStream_t st) {
-  using L = GluLayout<1, 256, STAGES, EW, 128, MODE != kGluFwd>;
+  using L = GluLayout<1, 256, STAGES, EW, 128, MODE>;
   auto kernel = glu_pair_kernel<STAGES, EW, H16, MODE, WHOLE>;
   static PerDevice resident;
   const int max_pairs = resident_pairs(resident, kernel, L::THREADS, L::SMEM);
   if (max_pairs < 1) return MLP_ERR_CUDA;
   const int pairs = p.units < max_pairs ? p.units : max_pairs;
-  LaunchScope ls(MODE != kGluFwd ? "glu_bwd_pair" : "glu_fwd_pair", st, p.a.T, p.a.N, p.a.K);
+  LaunchScope ls(glu_is_bwd(MODE) ? "glu_bwd_pair" : "glu_fwd_pair", st, p.a.T, p.a.N, p.a.K);
   launch_k(kernel, dim3(2 * pairs), dim3(L::THREADS), L::SMEM, st, maps, p);
   return launch_status();
 }

@@ -58,20 +58,27 @@ GluPlan plan(long long T, int K, int N, bool bwd) {
   return best;
 }
 
-template <int H16>
+// Epilogue warps of a pair: twelve, whose 128 registers hold a unit without
+// spills (65,536 x 512 -> 1,408 bf16 SiLU with 8-bit g and u: sixteen 167 us,
+// twelve 151, eight 153; without kept values 127, 122, 120; GELU and 8-bit values
+// 174, 164, 167); eight where both are kept in 16 bits, whose boxes would take an
+// operand stage beside twelve (171, 163, 149).
+template <int H16, int MODE>
 mlp_status launch(const GluMaps& maps, const GluParams& p, GluTile tile, cudaStream_t st) {
-  if (tile == kGluPair) {
-    const bool short_k = p.k_blocks <= 16;
-    if (glu_whole(p, false))
-      return short_k ? launch_glu_pair<4, 16, H16, kGluFwd, true>(maps, p, st)
-                     : launch_glu_pair<5, 8, H16, kGluFwd, true>(maps, p, st);
-    return short_k ? launch_glu_pair<4, 16, H16, kGluFwd, false>(maps, p, st)
-                   : launch_glu_pair<5, 8, H16, kGluFwd, false>(maps, p, st);
-  }
+  constexpr int EW = MODE == kGluFwdKeep ? 8 : 12;
+  if (tile == kGluPair)
+    return glu_whole(p, false) ? launch_glu_pair<5, EW, H16, MODE, true>(maps, p, st)
+                               : launch_glu_pair<5, EW, H16, MODE, false>(maps, p, st);
   if (tile == kGluTall)
-    return p.a_bytes <= 32 * GBK * 2 ? launch_glu_single<256, 5, 4, 32, H16, kGluFwd>(maps, p, st)
-                                     : launch_glu_single<256, 4, 4, 128, H16, kGluFwd>(maps, p, st);
-  return launch_glu_single<128, 5, 8, 128, H16, kGluFwd>(maps, p, st);
+    return p.a_bytes <= 32 * GBK * 2 ? launch_glu_single<256, 5, 4, 32, H16, MODE>(maps, p, st)
+                                     : launch_glu_single<256, 4, 4, 128, H16, MODE>(maps, p, st);
+  return launch_glu_single<128, 5, 8, 128, H16, MODE>(maps, p, st);
+}
+
+template <int H16>
+mlp_status launch_mode(const GluMaps& maps, const GluParams& p, GluTile tile, cudaStream_t st) {
+  return p.a.o[0] ? launch<H16, kGluFwdKeep>(maps, p, tile, st)
+                  : launch<H16, kGluFwd>(maps, p, tile, st);
 }
 
 }  // namespace
@@ -84,8 +91,8 @@ mlp_status launch_glu_tc(const GluArgs& a, bool bwd, cudaStream_t st) {
   GluMaps maps;
   GluParams p;
   MLP_CHECK(glu_setup(a, pl, false, maps, p));
-  return a.dtype == MLP_DTYPE_F16 ? launch<1>(maps, p, pl.tile, st)
-                                  : launch<0>(maps, p, pl.tile, st);
+  return a.dtype == MLP_DTYPE_F16 ? launch_mode<1>(maps, p, pl.tile, st)
+                                  : launch_mode<0>(maps, p, pl.tile, st);
 }
 
 }  // namespace mlp

@@ -15,15 +15,23 @@ namespace mlp {
 
 namespace {
 
+// 16-bit saved values take boxes twice as large as 8-bit ones: beside twelve
+// epilogue warps a ring of three operand stages, which long K feels, beside
+// eight one of four (us with twelve and eight, K = 512 194 and 210, 1,024 134
+// and 118, 1,536 224 and 198, 8,192 425 and 374).
+constexpr int kShortK = 12;  // k-blocks
+
 template <int H16, int MODE>
 mlp_status launch(const GluMaps& maps, const GluParams& p, GluTile tile, cudaStream_t st) {
   if (tile == kGluPair) {
-    const bool short_k = p.k_blocks <= 16;
-    if (glu_whole(p, true))
-      return short_k ? launch_glu_pair<2, 16, H16, MODE, true>(maps, p, st)
-                     : launch_glu_pair<4, 8, H16, MODE, true>(maps, p, st);
-    return short_k ? launch_glu_pair<2, 16, H16, MODE, false>(maps, p, st)
-                   : launch_glu_pair<4, 8, H16, MODE, false>(maps, p, st);
+    if constexpr (MODE == kGluBwd) {
+      if (p.k_blocks > kShortK)
+        return glu_whole(p, true) ? launch_glu_pair<4, 8, H16, MODE, true>(maps, p, st)
+                                  : launch_glu_pair<4, 8, H16, MODE, false>(maps, p, st);
+    }
+    constexpr int STAGES = MODE == kGluBwd ? 3 : 4;
+    return glu_whole(p, true) ? launch_glu_pair<STAGES, 12, H16, MODE, true>(maps, p, st)
+                              : launch_glu_pair<STAGES, 12, H16, MODE, false>(maps, p, st);
   }
   if (tile == kGluWide) return launch_glu_single<128, 4, 8, 128, H16, MODE>(maps, p, st);
   return launch_glu_single<64, 7, 4, 128, H16, MODE>(maps, p, st);
