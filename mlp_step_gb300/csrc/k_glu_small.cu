@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kThreads, FewShape<MT, COLS>::kPerSm)
   constexpr int CHUNK = Shape::kChunk;
   constexpr int D = kFewRing;
   static_assert(LPR <= 32 && HALF % 32 == 0, "columns of a CTA");
+  static_assert(KP == 8 || LPR < 32, "a warp's lanes share a row");
   extern __shared__ __align__(16) uint8_t few_smem[];
   float* xs = reinterpret_cast<float*>(few_smem + Shape::kRing);  // [k][MT]
   float* red = reinterpret_cast<float*>(few_smem);                // [warp][MT][COLS]

@@ -187,6 +187,20 @@ __device__ __forceinline__ void zero_past(F2 (&v)[N / 2], int n) {
   }
 }
 
+// v times the N values of a parameter vector from column c (without one: 1).
+template <bool FULL, int N>
+__device__ __forceinline__ void times(F2 (&v)[N / 2], const float* gain, int c, int n) {
+  if (!gain) return;
+  float g[N];
+  load_param<N, FULL>(gain, c, n, 1.f, g);
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) v[j] = mul2(v[j], f2(g[2 * j], g[2 * j + 1]));
+}
+
+// FORM: what the launch promises of the rows.  kFull: whole aligned pieces,
+// kExact: and exactly as many as the threads that share a row hold.
+enum { kAny, kFull, kExact };
+
 // Where a thread's share of the rows lies: piece i at column c0 + i 32 WPR N.
 template <typename T, int WPR, bool WIDE>
 struct Place {
@@ -203,6 +217,11 @@ struct Place {
     row = WIDE ? blockIdx.x / cluster : blockIdx.x * ROWS + slot;
   }
   __device__ __forceinline__ int col(int i) const { return c0 + i * 32 * WPR * N; }
+  // columns from piece i's first to the row's end (EXACT: known to hold the piece)
+  template <bool EXACT>
+  __device__ __forceinline__ int left(int d, int i) const {
+    return EXACT ? N : d - col(i);
+  }
   // this thread's first value of row r of a matrix (pitches are ints at the C
   // boundary: one widening multiplication)
   __device__ __forceinline__ T* in(const void* m, long long ld, uint32_t r) const {
@@ -210,12 +229,13 @@ struct Place {
   }
 };
 
-template <typename T, int WPR, bool FULL, bool WIDE>
+template <typename T, int WPR, int FORM, bool WIDE>
 __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
                                   1024 / HeldBlock<WPR>::THREADS)
     resnorm_fwd_kernel(const ResNorm p, int cluster) {
   constexpr int N = RowVec<T>::N, NV = vpt<T>() / N, ROWS = HeldBlock<WPR>::ROWS;
   constexpr int THREADS = HeldBlock<WPR>::THREADS, step = 32 * WPR * N;
+  constexpr bool FULL = FORM != kAny, EXACT = FORM == kExact;
   __shared__ float part[2][ROWS][WPR];
   __shared__ Exchange ex;
   extern __shared__ __align__(16) uint8_t ring_mem[];
@@ -231,12 +251,12 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   Ring<T, 3, 1, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 0};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (FULL && at.col(i) >= p.d) ring.clear(i);
+    if (FULL && !EXACT && at.col(i) >= p.d) ring.clear(i);
   auto issue = [&](int s, uint32_t r) {
     if (r < rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int n = p.d - at.col(i);
+        const int n = at.template left<EXACT>(p.d, i);
         if (FULL && n <= 0) continue;
         issue_piece<T, FULL>(ring.at(s, 0, i), at.in(p.x, p.ldx, r) + i * step, n, p.vec & kXVec);
         if (block)
@@ -254,27 +274,26 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
     few_wait<1>();
     F2 v[NV][N / 2];
     if (block) {
-      F2 s2 = f2(0.f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        unpack_piece<T>(ring(1, i), v[i]);
-        zero_past<FULL, N>(v[i], p.d - at.col(i));
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) s2 = fma2(v[i][j], v[i][j], s2);
-      }
+      for (int i = 0; i < NV; ++i) unpack_piece<T>(ring(1, i), v[i]);
       float rho = 1.f;
       if (p.post) {
+        F2 s2 = f2(0.f);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) s2 = fma2(v[i][j], v[i][j], s2);
         rho = rsqrtf(sum(s2.x + s2.y) * inv_d + p.eps);  // two ulp
         if (p.b_rstd && at.rank == 0 && at.t == 0) p.b_rstd[row] = rho;
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = at.col(i), n = p.d - c;
-        float g[N];
-        load_param<N, FULL>(p.post_gain, c, n, 1.f, g);
+        const int c = at.col(i), n = at.template left<EXACT>(p.d, i);
+        if (p.post) {
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j)
-          v[i][j] = mul2(mul2(v[i][j], f2(rho)), f2(g[2 * j], g[2 * j + 1]));
+          for (int j = 0; j < N / 2; ++j) v[i][j] = mul2(v[i][j], f2(rho));
+        }
+        times<FULL, N>(v[i], p.post_gain, c, n);
         if (p.drop.threshold) {
           uint32_t w[N / 2];
           drop_words<N>(p.drop, key, row, c, w);
@@ -299,16 +318,13 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        unpack_piece<T>(ring(0, i), v[i]);
-        zero_past<FULL, N>(v[i], p.d - at.col(i));
-      }
+      for (int i = 0; i < NV; ++i) unpack_piece<T>(ring(0, i), v[i]);
     }
     if (p.h) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         store_piece_of<FULL>(at.in(p.h, p.ldh, row) + i * step,
-                             reinterpret_cast<const float(&)[N]>(v[i]), p.d - at.col(i),
+                             reinterpret_cast<const float(&)[N]>(v[i]), at.template left<EXACT>(p.d, i),
                              p.vec & kHVec);
     }
     if (p.n) {
@@ -321,12 +337,10 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       if (p.h_rstd && at.rank == 0 && at.t == 0) p.h_rstd[row] = rho;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = at.col(i), n = p.d - c;
-        float g[N];
-        load_param<N, FULL>(p.next_gain, c, n, 1.f, g);
+        const int c = at.col(i), n = at.template left<EXACT>(p.d, i);
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j)
-          v[i][j] = mul2(mul2(v[i][j], f2(rho)), f2(g[2 * j], g[2 * j + 1]));
+        for (int j = 0; j < N / 2; ++j) v[i][j] = mul2(v[i][j], f2(rho));
+        times<FULL, N>(v[i], p.next_gain, c, n);
         store_piece_of<FULL>(at.in(p.n, p.ldn, row) + i * step,
                              reinterpret_cast<const float(&)[N]>(v[i]), n, p.vec & kNVec);
       }
@@ -344,12 +358,13 @@ constexpr int bwd_ahead() {
   return sizeof(T) == 4 && WPR == 32 ? 0 : 1;
 }
 
-template <typename T, int WPR, bool FULL, bool WIDE>
+template <typename T, int WPR, int FORM, bool WIDE>
 __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
                                   WPR == 32 ? 1 : 512 / HeldBlock<WPR>::THREADS)
     resnorm_bwd_kernel(const ResNorm p, int cluster) {
   constexpr int N = RowVec<T>::N, NV = vpt<T>() / N, ROWS = HeldBlock<WPR>::ROWS;
   constexpr int THREADS = HeldBlock<WPR>::THREADS, step = 32 * WPR * N;
+  constexpr bool FULL = FORM != kAny, EXACT = FORM == kExact;
   __shared__ float part[2][ROWS][WPR];
   __shared__ Exchange ex;
   extern __shared__ __align__(16) uint8_t ring_mem[];
@@ -371,14 +386,14 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   Ring<T, 5, AHEAD, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 0};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (FULL && at.col(i) >= p.d) ring.clear(i);
+    if (FULL && !EXACT && at.col(i) >= p.d) ring.clear(i);
   float rh_n = 0.f, rb_n = 0.f;  // the next row's
   // dn, h and dh of row r, one group of copies, and b and z, another
   auto issue_norm = [&](int s, uint32_t r) {
     if (r < rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int n = p.d - at.col(i);
+        const int n = at.template left<EXACT>(p.d, i);
         if (FULL && n <= 0) continue;
         if (next) {
           issue_piece<T, FULL>(ring.at(s, 0, i), at.in(p.n, p.ldn, r) + i * step, n, p.vec & kNVec);
@@ -395,7 +410,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
     if (r < rows) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int n = p.d - at.col(i);
+        const int n = at.template left<EXACT>(p.d, i);
         if (FULL && n <= 0) continue;
         if (block)
           issue_piece<T, FULL>(ring.at(s, 3, i), at.in(p.b, p.ldb, r) + i * step, n, p.vec & kBVec);
@@ -424,21 +439,17 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       F2 s2 = f2(0.f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = at.col(i), n = p.d - c;
-        float g[N];
-        load_param<N, FULL>(p.next_gain, c, n, 1.f, g);
+        const int c = at.col(i), n = at.template left<EXACT>(p.d, i);
         unpack_piece<T>(ring(0, i), v[i]);
         unpack_piece<T>(ring(1, i), hh[i]);
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) hh[i][j] = mul2(hh[i][j], f2(rh));
-        zero_past<FULL, N>(v[i], n);
         zero_past<FULL, N>(hh[i], n);
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          dnext[i][j] = fma2(v[i][j], hh[i][j], dnext[i][j]);
-          v[i][j] = mul2(v[i][j], f2(g[2 * j], g[2 * j + 1]));
-          s2 = fma2(v[i][j], hh[i][j], s2);
-        }
+        for (int j = 0; j < N / 2; ++j) dnext[i][j] = fma2(v[i][j], hh[i][j], dnext[i][j]);
+        times<FULL, N>(v[i], p.next_gain, c, n);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) s2 = fma2(v[i][j], hh[i][j], s2);
       }
       const float m = sum(s2.x + s2.y) * inv_d;
 #pragma unroll
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       store_piece_of<FULL>(at.in(p.dx, p.lddx, row) + i * step,
-                           reinterpret_cast<const float(&)[N]>(v[i]), p.d - at.col(i),
+                           reinterpret_cast<const float(&)[N]>(v[i]), at.template left<EXACT>(p.d, i),
                            p.vec & kDxVec);
     if (!block) {
       if constexpr (AHEAD) ring.stage ^= 1;
@@ -477,28 +488,30 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
     F2 bb[NV][N / 2];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = at.col(i), n = p.d - c;
-      float g[N];
-      load_param<N, FULL>(p.post_gain, c, n, 1.f, g);
+      const int c = at.col(i), n = at.template left<EXACT>(p.d, i);
       uint32_t w[N / 2];
       if (p.drop.threshold) drop_words<N>(p.drop, key, row, c, w);
       unpack_piece<T>(ring(3, i), bb[i]);
+      if (p.post) {
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        bb[i][j] = mul2(bb[i][j], f2(rb));
-        v[i][j] = mul2(v[i][j], f2(p.scale));
+        for (int j = 0; j < N / 2; ++j) bb[i][j] = mul2(bb[i][j], f2(rb));
+        zero_past<FULL, N>(bb[i], n);
       }
-      zero_past<FULL, N>(bb[i], n);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) v[i][j] = mul2(v[i][j], f2(p.scale));
       zero_past<FULL, N>(v[i], n);
       if (gate) {
         F2 z[N / 2], dz[N / 2];
         unpack_piece<T>(ring(4, i), z);
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-          dz[j] = mul2(bb[i][j], f2(g[2 * j], g[2 * j + 1]));
-          if (p.drop.threshold) dz[j] = drop2(dz[j], w[j], key, p.drop.scale);
-          dz[j] = mul2(dz[j], v[i][j]);
+        for (int j = 0; j < N / 2; ++j) dz[j] = bb[i][j];
+        times<FULL, N>(dz, p.post_gain, c, n);
+        if (p.drop.threshold) {
+#pragma unroll
+          for (int j = 0; j < N / 2; ++j) dz[j] = drop2(dz[j], w[j], key, p.drop.scale);
         }
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) dz[j] = mul2(dz[j], v[i][j]);
         if (p.sigmoid) {
 #pragma unroll
           for (int j = 0; j < N / 2; ++j) {
@@ -512,13 +525,15 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) v[i][j] = mul2(v[i][j], z[j]);
       }
+      if (p.drop.threshold) {
 #pragma unroll
-      for (int j = 0; j < N / 2; ++j) {
-        if (p.drop.threshold) v[i][j] = drop2(v[i][j], w[j], key, p.drop.scale);
-        dpost[i][j] = fma2(v[i][j], bb[i][j], dpost[i][j]);
-        v[i][j] = mul2(v[i][j], f2(g[2 * j], g[2 * j + 1]));
-        s2 = fma2(v[i][j], bb[i][j], s2);
+        for (int j = 0; j < N / 2; ++j) v[i][j] = drop2(v[i][j], w[j], key, p.drop.scale);
       }
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) dpost[i][j] = fma2(v[i][j], bb[i][j], dpost[i][j]);
+      times<FULL, N>(v[i], p.post_gain, c, n);
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) s2 = fma2(v[i][j], bb[i][j], s2);
     }
     if constexpr (AHEAD) ring.stage ^= 1;
     else issue_block(0, then);
@@ -533,7 +548,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       store_piece_of<FULL>(at.in(p.db, p.lddb, row) + i * step,
-                           reinterpret_cast<const float(&)[N]>(v[i]), p.d - at.col(i),
+                           reinterpret_cast<const float(&)[N]>(v[i]), at.template left<EXACT>(p.d, i),
                            p.vec & kDbVec);
   }
   if (p.part) {
@@ -609,11 +624,11 @@ int bwd_blocks(long long T, int d) {
   return (int)(need < kBwdBlocks ? need : kBwdBlocks);
 }
 
-template <typename T, int WPR, bool FULL, bool WIDE>
+template <typename T, int WPR, int FORM, bool WIDE>
 mlp_status fwd_of(const ResNorm& p, cudaStream_t st) {
   using B = HeldBlock<WPR>;
   constexpr int kWidth = vpt<T>() * 32 * WPR;
-  auto kernel = resnorm_fwd_kernel<T, WPR, FULL, WIDE>;
+  auto kernel = resnorm_fwd_kernel<T, WPR, FORM, WIDE>;
   static PerDevice per_sm;
   constexpr int kSmem = Ring<T, 3, 1, B::THREADS>::BYTES;
   static_assert(kSmem <= 225 * 1024, "shared memory");
@@ -631,11 +646,11 @@ mlp_status fwd_of(const ResNorm& p, cudaStream_t st) {
   return launch_rows(kernel, blocks, B::THREADS, kSmem, cluster, p, st);
 }
 
-template <typename T, int WPR, bool FULL, bool WIDE>
+template <typename T, int WPR, int FORM, bool WIDE>
 mlp_status bwd_of(const ResNorm& p, int* rows, cudaStream_t st) {
   using B = HeldBlock<WPR>;
   constexpr int kWidth = vpt<T>() * 32 * WPR;
-  auto kernel = resnorm_bwd_kernel<T, WPR, FULL, WIDE>;
+  auto kernel = resnorm_bwd_kernel<T, WPR, FORM, WIDE>;
   static PerDevice per_sm;
   constexpr int kSmem = Ring<T, 5, bwd_ahead<T, WPR>(), B::THREADS>::BYTES;
   static_assert(kSmem <= 225 * 1024, "shared memory");
@@ -652,10 +667,15 @@ mlp_status bwd_of(const ResNorm& p, int* rows, cudaStream_t st) {
 
 template <typename T, int WPR, bool WIDE, bool BWD>
 mlp_status of_form(const ResNorm& p, bool full, int* rows, cudaStream_t st) {
+  const bool exact = full && p.d % (vpt<T>() * 32 * WPR) == 0;
   if constexpr (BWD)
-    return full ? bwd_of<T, WPR, true, WIDE>(p, rows, st) : bwd_of<T, WPR, false, WIDE>(p, rows, st);
+    return exact  ? bwd_of<T, WPR, kExact, WIDE>(p, rows, st)
+           : full ? bwd_of<T, WPR, kFull, WIDE>(p, rows, st)
+                  : bwd_of<T, WPR, kAny, WIDE>(p, rows, st);
   else
-    return full ? fwd_of<T, WPR, true, WIDE>(p, st) : fwd_of<T, WPR, false, WIDE>(p, st);
+    return exact  ? fwd_of<T, WPR, kExact, WIDE>(p, st)
+           : full ? fwd_of<T, WPR, kFull, WIDE>(p, st)
+                  : fwd_of<T, WPR, kAny, WIDE>(p, st);
 }
 
 template <typename T, bool BWD>
