@@ -124,27 +124,26 @@ __device__ __forceinline__ F2 logistic2(F2 z, F2& one_minus) {
   return s;
 }
 
-// A thread's pieces of the rows ahead, in shared memory: MATS matrices, AHEAD + 1
-// rows, each 16-byte piece at a place of its own that this thread alone fills
-// (asynchronous copies) and reads.  So what is in flight takes no registers and
-// no barrier.
-template <typename T, int MATS, int AHEAD, int THREADS>
+// A thread's pieces of the rows ahead, in shared memory: `mats` matrices (those
+// that the call has: what the ring leaves is L1, where the gains are kept),
+// AHEAD + 1 rows, each 16-byte piece at a place of its own that this thread alone
+// fills (asynchronous copies) and reads.  So what is in flight takes no registers
+// and no barrier.
+template <typename T, int AHEAD, int THREADS>
 struct Ring {
   static constexpr int NV = vpt<T>() / RowVec<T>::N;
-  static constexpr int BYTES = MATS * (AHEAD + 1) * NV * THREADS * 16;
+  static constexpr int bytes(int mats) { return mats * (AHEAD + 1) * NV * THREADS * 16; }
   uint4* mine;
+  int mats;
   int stage;  // of the current row
   __device__ __forceinline__ uint4* at(int s, int m, int i) const {
-    return mine + ((s * MATS + m) * NV + i) * THREADS;
+    return mine + ((s * mats + m) * NV + i) * THREADS;
   }
   // piece i of matrix m of the current row
   __device__ __forceinline__ uint4 operator()(int m, int i) const { return *at(stage, m, i); }
   // Zeros in a piece that no row has, which no copy writes.
   __device__ __forceinline__ void clear(int i) const {
-#pragma unroll
-    for (int s = 0; s <= AHEAD; ++s)
-#pragma unroll
-      for (int m = 0; m < MATS; ++m) *at(s, m, i) = make_uint4(0, 0, 0, 0);
+    for (int m = 0; m < mats * (AHEAD + 1); ++m) *at(0, m, i) = make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -248,7 +247,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
   const DropKey key(p.drop);
   RowSum<WPR, WIDE, ROWS> sum{part, &ex, at.slot, at.t >> 5, at.rank, cluster, p.wait_ns, p.err};
   sum.begin();
-  Ring<T, 3, 1, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 0};
+  Ring<T, 1, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 1 + block + gate, 0};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (FULL && !EXACT && at.col(i) >= p.d) ring.clear(i);
@@ -383,7 +382,10 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) dnext[i][j] = dpost[i][j] = f2(0.f);
   constexpr int AHEAD = bwd_ahead<T, WPR>();
-  Ring<T, 5, AHEAD, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x, 0};
+  // places of dh, b and z behind dn and h
+  const int mx = next ? 2 : 0, mb = mx + (p.x != nullptr), mz = mb + 1;
+  Ring<T, AHEAD, THREADS> ring{reinterpret_cast<uint4*>(ring_mem) + threadIdx.x,
+                               mb + block + gate, 0};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (FULL && !EXACT && at.col(i) >= p.d) ring.clear(i);
@@ -400,7 +402,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
           issue_piece<T, FULL>(ring.at(s, 1, i), at.in(p.h, p.ldh, r) + i * step, n, p.vec & kHVec);
         }
         if (p.x)
-          issue_piece<T, FULL>(ring.at(s, 2, i), at.in(p.x, p.ldx, r) + i * step, n, p.vec & kXVec);
+          issue_piece<T, FULL>(ring.at(s, mx, i), at.in(p.x, p.ldx, r) + i * step, n, p.vec & kXVec);
       }
       if (next) rh_n = p.h_rstd[r];
     }
@@ -413,9 +415,9 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
         const int n = at.template left<EXACT>(p.d, i);
         if (FULL && n <= 0) continue;
         if (block)
-          issue_piece<T, FULL>(ring.at(s, 3, i), at.in(p.b, p.ldb, r) + i * step, n, p.vec & kBVec);
+          issue_piece<T, FULL>(ring.at(s, mb, i), at.in(p.b, p.ldb, r) + i * step, n, p.vec & kBVec);
         if (gate)
-          issue_piece<T, FULL>(ring.at(s, 4, i), at.in(p.z, p.ldz, r) + i * step, n, p.vec & kZVec);
+          issue_piece<T, FULL>(ring.at(s, mz, i), at.in(p.z, p.ldz, r) + i * step, n, p.vec & kZVec);
       }
       if (p.post) rb_n = p.b_rstd[r];
     }
@@ -461,14 +463,14 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           F2 x[N / 2];
-          unpack_piece<T>(ring(2, i), x);
+          unpack_piece<T>(ring(mx, i), x);
 #pragma unroll
           for (int j = 0; j < N / 2; ++j) v[i][j] = add2(v[i][j], x[j]);
         }
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) unpack_piece<T>(ring(2, i), v[i]);
+      for (int i = 0; i < NV; ++i) unpack_piece<T>(ring(mx, i), v[i]);
     }
     if constexpr (!AHEAD) {
       issue_norm(0, then);
@@ -491,7 +493,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       const int c = at.col(i), n = at.template left<EXACT>(p.d, i);
       uint32_t w[N / 2];
       if (p.drop.threshold) drop_words<N>(p.drop, key, row, c, w);
-      unpack_piece<T>(ring(3, i), bb[i]);
+      unpack_piece<T>(ring(mb, i), bb[i]);
       if (p.post) {
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) bb[i][j] = mul2(bb[i][j], f2(rb));
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(HeldBlock<WPR>::THREADS,
       zero_past<FULL, N>(v[i], n);
       if (gate) {
         F2 z[N / 2], dz[N / 2];
-        unpack_piece<T>(ring(4, i), z);
+        unpack_piece<T>(ring(mz, i), z);
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) dz[j] = bb[i][j];
         times<FULL, N>(dz, p.post_gain, c, n);
@@ -630,7 +632,8 @@ mlp_status fwd_of(const ResNorm& p, cudaStream_t st) {
   constexpr int kWidth = vpt<T>() * 32 * WPR;
   auto kernel = resnorm_fwd_kernel<T, WPR, FORM, WIDE>;
   static PerDevice per_sm;
-  constexpr int kSmem = Ring<T, 3, 1, B::THREADS>::BYTES;
+  using R = Ring<T, 1, B::THREADS>;
+  constexpr int kSmem = R::bytes(3);
   static_assert(kSmem <= 225 * 1024, "shared memory");
   static PerDevice configured;
   if (!allow_smem(configured, kernel, kSmem)) return MLP_ERR_CUDA;
@@ -643,7 +646,7 @@ mlp_status fwd_of(const ResNorm& p, cudaStream_t st) {
     blocks *= cluster;
   }
   LaunchScope ls("resnorm_fwd", st, p.T, p.d, sizeof(T));
-  return launch_rows(kernel, blocks, B::THREADS, kSmem, cluster, p, st);
+  return launch_rows(kernel, blocks, B::THREADS, R::bytes(1 + !!p.b + !!p.z), cluster, p, st);
 }
 
 template <typename T, int WPR, int FORM, bool WIDE>
@@ -652,9 +655,11 @@ mlp_status bwd_of(const ResNorm& p, int* rows, cudaStream_t st) {
   constexpr int kWidth = vpt<T>() * 32 * WPR;
   auto kernel = resnorm_bwd_kernel<T, WPR, FORM, WIDE>;
   static PerDevice per_sm;
-  constexpr int kSmem = Ring<T, 5, bwd_ahead<T, WPR>(), B::THREADS>::BYTES;
+  using R = Ring<T, bwd_ahead<T, WPR>(), B::THREADS>;
+  constexpr int kSmem = R::bytes(5);
   static_assert(kSmem <= 225 * 1024, "shared memory");
-  static_assert(B::ROWS == 1 || 32 * WPR * vpt<T>() * 4 <= kSmem, "sums in the ring's place");
+  static_assert(B::ROWS == 1 || 32 * WPR * vpt<T>() * 4 <= R::bytes(1),
+                "sums in the ring's place");
   static PerDevice configured;
   if (!allow_smem(configured, kernel, kSmem)) return MLP_ERR_CUDA;
   const int cluster = WIDE ? (p.d + kWidth - 1) / kWidth : 1;
@@ -662,7 +667,8 @@ mlp_status bwd_of(const ResNorm& p, int* rows, cudaStream_t st) {
   if (WIDE) resident = resident / cluster > 0 ? resident / cluster : 1;
   if (resident < *rows) *rows = resident;
   LaunchScope ls("resnorm_bwd", st, p.T, p.d, sizeof(T));
-  return launch_rows(kernel, *rows * cluster, B::THREADS, kSmem, cluster, p, st);
+  return launch_rows(kernel, *rows * cluster, B::THREADS,
+                     R::bytes(2 * !!p.n + !!p.x + !!p.b + !!p.z), cluster, p, st);
 }
 
 template <typename T, int WPR, bool WIDE, bool BWD>
