@@ -60,7 +60,7 @@ GluPath glu_path(long long T, int K, int N, int dtype, bool bwd) {
   p.few = !bwd && glu_takes_few(T, K, N, dtype);
   if (p.few) return p;
   if (dtype == MLP_DTYPE_F32) {
-    p.splits = linear_f32_splits(T, K, N);
+    p.splits = linear_f32_splits(T, K, N, bwd ? 1 : 2);
   } else {
     p.splits = glu_tc_splits(T, K, N, bwd);
     if (p.splits == 1) p.splits = 0;
@@ -92,11 +92,10 @@ mlp_status run_glu(GluArgs a, const GluPath& gp, bool bwd, float* db_gate, float
     l.x = a.x; l.ldx = a.ldx;
     l.ldp = a.ldp;
     l.splits = a.splits;
-    for (int k = 0; k < (bwd ? 1 : 2); ++k) {
-      l.w = a.w[k]; l.ldw = a.ldw[k];
-      l.partial = a.partial + (long long)k * a.splits * a.T * a.ldp;
-      MLP_CHECK(launch_linear_f32(l, bwd, st));
-    }
+    l.w = a.w[0]; l.ldw = a.ldw[0];
+    l.w2 = a.w[1]; l.ldw2 = a.ldw[1];  // (none in the backward)
+    l.partial = a.partial;
+    MLP_CHECK(launch_linear_f32(l, bwd, st));
   } else {
     MLP_CHECK(launch_glu_tc(a, bwd, st));
   }

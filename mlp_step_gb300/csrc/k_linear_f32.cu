@@ -114,16 +114,19 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
   const int c0 = (int)(blockIdx.x - tm * tiles_n) * TN;
   const int k_lo = blockIdx.y * k_per, k_hi = min(a.K, k_lo + k_per);
   const float* x = static_cast<const float*>(a.x);
-  const float* w = static_cast<const float*>(a.w);
+  // of two products of the same x: the second's weight and planes
+  const bool second = !BWD && blockIdx.z;
+  const float* w = static_cast<const float*>(second ? a.w2 : a.w);
+  const long long ldw = second ? a.ldw2 : a.ldw;
   RowStager xs(x, a.ldx, r0, a.T, k_lo, tid);
-  RowStager wr(w, a.ldw, c0, BWD ? a.N : 0, k_lo, tid);
+  RowStager wr(w, ldw, c0, BWD ? a.N : 0, k_lo, tid);
   auto stage = [&](int st, int k0) {
     float* sa = smem + st * 2 * TK * PITCH;
     float* sb = sa + TK * PITCH;
     if (k0 < k_hi) {
       xs.stage(sa, k_hi - k0, x, tid);
       if constexpr (BWD) wr.stage(sb, k_hi - k0, w, tid);
-      else stage_cols(sb, w, a.ldw, c0, a.N, k0, k_hi, w_vec, tid);
+      else stage_cols(sb, w, ldw, c0, a.N, k0, k_hi, w_vec, tid);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   // planes have whole 32-column pieces (ldp a multiple of 32): only whole
   // quads past ldp are left out
-  float* out = a.partial + (long long)blockIdx.y * a.T * a.ldp;
+  float* out = a.partial + (long long)(blockIdx.z * gridDim.y + blockIdx.y) * a.T * a.ldp;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const long long r = r0 + (i < 4 ? 0 : 64) + ty * 4 + (i & 3);
@@ -182,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_f32_kernel(const LinearArg
 // over 304 places, each k taking an SM 260 cycles with one block on it and 380
 // with two (49 and 67 % of the FMA rate), and the raw sums' way through memory
 // and the pass that adds them, four planes at a time.
-int linear_f32_splits(long long T, int K, int N) {
-  const long long tiles = (T + TM - 1) / TM * ((N + TN - 1) / TN);
+int linear_f32_splits(long long T, int K, int N, int products) {
+  const long long tiles = (T + TM - 1) / TM * ((N + TN - 1) / TN) * products;
   int best = 1;
   double best_cycles = 1e300;
   for (int s = 1; s <= 32; ++s) {
@@ -192,7 +195,7 @@ int linear_f32_splits(long long T, int K, int N) {
     const int splits = (K + per - 1) / per;
     const long long blocks = tiles * splits, waves = (blocks + 303) / 304;
     const double cycles = (blocks <= 152 ? 260. : waves * 380.) * per + waves * 6000. +
-                          splits * (double)T * N * 8 / 3000 + (splits + 3) / 4 * 1500.;
+                          splits * (double)T * N * products * 8 / 3000 + (splits + 3) / 4 * 1500.;
     if (cycles < best_cycles) {
       best_cycles = cycles;
       best = splits;
@@ -204,9 +207,10 @@ int linear_f32_splits(long long T, int K, int N) {
 mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st) {
   const long long tiles = (a.T + TM - 1) / TM * ((a.N + TN - 1) / TN);
   if (tiles > 0x7fffffffll) return MLP_ERR_UNSUPPORTED_SHAPE;
-  const dim3 grid((unsigned)tiles, a.splits);
+  const dim3 grid((unsigned)tiles, a.splits, a.w2 ? 2 : 1);
   const int per = ((a.K + a.splits - 1) / a.splits + TK - 1) / TK * TK;
-  const int w_vec = reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.ldw % 4 == 0;
+  const int w_vec = reinterpret_cast<uintptr_t>(a.w) % 16 == 0 && a.ldw % 4 == 0 &&
+                    (!a.w2 || (reinterpret_cast<uintptr_t>(a.w2) % 16 == 0 && a.ldw2 % 4 == 0));
   auto kernel = bwd ? linear_f32_kernel<true> : linear_f32_kernel<false>;
   static PerDevice configured[2];
   if (!allow_smem(configured[bwd], kernel, kSmem)) return MLP_ERR_CUDA;

@@ -229,6 +229,8 @@ struct LinearArgs {
   long long ldx;
   const void* w;  // forward [K][N], backward [N][K]
   long long ldw;
+  const void* w2;  // launch_linear_f32, forward: a second product of x (nullable), whose
+  long long ldw2;  // planes lie behind the first's
   int act;
   float slope;
   const float* bias;
@@ -268,7 +270,7 @@ mlp_status launch_linear_tc(const LinearArgs& a, bool bwd, cudaStream_t st);
 int linear_tc_splits(long long T, int K, int N);
 // k_linear_f32.cu: raw fp32 sums into a.partial, K in linear_f32_splits parts.
 mlp_status launch_linear_f32(const LinearArgs& a, bool bwd, cudaStream_t st);
-int linear_f32_splits(long long T, int K, int N);
+int linear_f32_splits(long long T, int K, int N, int products = 1);
 // k_linear_small.cu: a few rows, all types, one launch; in the backward it
 // writes the column sums to `dbias` itself.
 bool linear_takes_few(long long T, int K, int N, int dtype, bool bwd);
