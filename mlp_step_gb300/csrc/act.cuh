@@ -143,10 +143,10 @@ __device__ __forceinline__ F2 act_grad2(F2 u, float slope, F2& value) {
     const F2 b = mul2(mul2(c, s), fma2(s, f2(-1.f), f2(1.f)));
     return fma2(b, w, s);
   } else if constexpr (ACT == MLP_ACT_SILU) {
-    const F2 c = f2(copysignf(abs_upto(u.x, kLogisticEnd), u.x),
-                    copysignf(abs_upto(u.y, kLogisticEnd), u.y));
-    const F2 s = sigmoid2(c);
-    value = mul2(above2(u, kLogisticEnd), s);
+    const F2 s = sigmoid2(u);  // 0 and 1 beyond the end
+    const F2 m = above2(u, kLogisticEnd);
+    const F2 c = f2(fminf(m.x, kLogisticEnd), fminf(m.y, kLogisticEnd));
+    value = mul2(m, s);
     return fma2(mul2(c, s), fma2(s, f2(-1.f), f2(1.f)), s);
   } else {
     value = u;

@@ -363,7 +363,8 @@ __device__ __forceinline__ void glu_body(const GluMaps& maps, const GluParams& p
       for (; c < HID; c += 32 * L::SHARE) {
         const Unit t = next;
         const bool last = c + 32 * L::SHARE >= HID;
-        next = last ? locate(u + workers, 32 * start) : locate(u, c + 32 * L::SHARE);
+        if (last) next = locate(u + workers, 32 * start);
+        else next.n0 += 32 * L::SHARE;
         const long long m = (long long)t.row0 + lane;
         const bool row_ok = m < a.T;
         if (!ready) {
