@@ -14,8 +14,14 @@
 // single CTA does the same on 128 rows (128 or 64 hidden columns), with the
 // contraction split over CTAs when even those are few (raw sums to a
 // workspace, finished by launch_glu_finish).  Warps: TMA producer, MMA issuer,
-// four to sixteen epilogue warps; two accumulators, so that the epilogue of one
+// four to twelve epilogue warps; two accumulators, so that the epilogue of one
 // tile overlaps the MMAs of the next.  The body is in glu_tc.cuh.
+//
+// Bound: the MMAs for long K (4,096 x 8,192 -> 8,192 fp16 610 us = 1.80 PFLOP/s, 94 %
+// of the library's rate, with both pre-activations kept 614).  For K of a few
+// hundred the epilogue (65,536 x 512 -> 1,408 bf16 SiLU: 122 us = 1.55 PFLOP/s, of
+// which loads and MMAs alone take 104 and the accumulators' way to registers 5; with
+// g and u kept 149, in 8 bits 151).
 #include "glu_launch.cuh"
 
 namespace mlp {
@@ -23,15 +29,18 @@ namespace mlp {
 namespace {
 
 // From the shape alone (so that workspace sizes do not depend on the device).
-// Pairs when their tiles fill most of ~76 pairs; otherwise the single-CTA tile
-// and the split of K with the smallest estimated time: rounds of units over
-// ~152 CTAs, each as long as its MMAs (a 64-deep block takes about 512 cycles
-// whatever the tile's width) or its epilogue, and the weights' way from memory.
-// A split costs the second launch and the raw sums' way through memory.
+// Pairs from 40 of their tiles on (us in pairs and in the best single tiles, K =
+// 512 and 4,096: forward 33 tiles 14.8 and 12.8, 31 and 29; 44 tiles 14.8 and 14.8, 31
+// and 35; 55 tiles 14.8 and 16.9, 31 and 35; backward 36 tiles 23 and 21, 42 and 37; 48
+// tiles 23 and 27, 42 and 54).  Otherwise the single-CTA tile and the split of K with
+// the smallest estimated time: rounds of units over ~152 CTAs, each as long as its
+// MMAs (a 64-deep block takes about 512 cycles whatever the tile's width) or its
+// epilogue, and the weights' way from memory.  A split costs the second launch and
+// the raw sums' way through memory.
 GluPlan plan(long long T, int K, int N, bool bwd) {
   const int kb = (K + GBK - 1) / GBK, pair_hid = bwd ? 256 : 128;
   if (T > 128 && N > pair_hid / 2 &&
-      (T + 255) / 256 * ((N + pair_hid - 1) / pair_hid) >= 48)
+      (T + 255) / 256 * ((N + pair_hid - 1) / pair_hid) >= 40)
     return {kGluPair, pair_hid, 1, kb};
   GluPlan best{};
   double best_cycles = 1e300;

@@ -354,22 +354,16 @@ mlp_status few_launch(const GluArgs& a, cudaStream_t st) {
   return launch_status();
 }
 
-template <typename T, int MT>
-mlp_status few_cols(const GluArgs& a, cudaStream_t st) {
-  // 128 accumulators a cluster (longer runs of the weights) where they still
-  // give enough CTAs
-  if constexpr (MT <= 4) {
-    if ((long long)a.N / 64 * 8 >= 304) return few_launch<T, MT, 128>(a, st);
-  }
-  return few_launch<T, MT, 64>(a, st);
-}
-
+// 128 accumulators a cluster, whose runs of the weights are longer (us with 128 and
+// 64, one row, bf16: 512 -> 1,408 8.8 and 10.8, 4,096 -> 11,008 35.5 and 39.4, 8,192
+// -> 8,192 47.6 and 53.8; four rows of the last 62 and 70); 64 for eight rows, whose
+// sums would not fit the registers.
 template <typename T>
 mlp_status few_rows(const GluArgs& a, cudaStream_t st) {
-  if (a.T <= 1) return few_cols<T, 1>(a, st);
-  if (a.T <= 2) return few_cols<T, 2>(a, st);
-  if (a.T <= 4) return few_cols<T, 4>(a, st);
-  return few_cols<T, 8>(a, st);
+  if (a.T <= 1) return few_launch<T, 1, 128>(a, st);
+  if (a.T <= 2) return few_launch<T, 2, 128>(a, st);
+  if (a.T <= 4) return few_launch<T, 4, 128>(a, st);
+  return few_launch<T, 8, 64>(a, st);
 }
 
 template <typename T>
@@ -389,10 +383,13 @@ mlp_status finish_launch(const GluArgs& a, bool bwd, cudaStream_t st) {
 
 // Up to 8 rows for fp32, whose tiled product computes 128 rows whatever T is.
 // In 16 bits the tensor cores take over once the FMAs, not the reading of the
-// weights, bound this kernel.
+// weights, bound this kernel: above 2 rows, 8 of small weights (us here and there
+// with cold weights, bf16: 512 -> 1,408 T = 1 9 and 13, 4 11 and 13, 8 13 and 13; 1,024
+// -> 2,816 T = 2 13 and 15, 4 15 and 15, 8 17 and 15; 8,192 -> 8,192 T = 1 48 and 54, 2
+// 52 and 54, 3 62 and 54, 8 140 and 54).
 bool glu_takes_few(long long T, int K, int N, int dtype) {
   if (dtype == MLP_DTYPE_F32) return T <= 8;
-  return T <= 2 || (T <= 8 && (long long)K * N <= (1ll << 21));
+  return T <= 2 || (T <= 8 && (long long)K * N <= (1ll << 20));
 }
 
 mlp_status launch_glu_few(const GluArgs& a, cudaStream_t st) {
