@@ -18,23 +18,35 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRowsAhead = 4;  // rows loaded before the first is finished
 
+// Value at column c of row m (pitches are ints at the C boundary: one widening
+// multiplication).
+template <typename T>
+__device__ __forceinline__ T* at(void* base, long long ld, long long m, int c) {
+  return static_cast<T*>(base) + ((unsigned long long)(uint32_t)m * (uint32_t)ld + (uint32_t)c);
+}
+template <typename T>
+__device__ __forceinline__ const T* at(const void* base, long long ld, long long m, int c) {
+  return static_cast<const T*>(base) +
+         ((unsigned long long)(uint32_t)m * (uint32_t)ld + (uint32_t)c);
+}
+
 // Element (m, c) of kept matrix k: the pre-activation z in the operand type or
 // in 8 bits (whole warps, lane = column of a 32-column group).
 template <typename T>
 __device__ __forceinline__ void keep(const GluArgs& a, int k, long long m, int c, bool ok,
                                      float z) {
   if (a.o[k]) {
-    if (ok) from_f32(z, static_cast<T*>(a.o[k])[m * a.ldo[k] + c]);
+    if (ok) from_f32(z, *at<T>(a.o[k], a.ldo[k], m, c));
   } else if (a.q[k]) {
     const uint32_t top =
         __reduce_max_sync(0xffffffffu, ok ? __float_as_uint(z) & 0x7fffffffu : 0u);
     const uint32_t b = ckpt8_byte(top);
     if (ok) {
       const float held = ckpt8_must_hold(top) ? ckpt8_hold(z, ckpt8_step(b)) : z;
-      a.q[k][m * a.ldq[k] + c] =
+      *at<int8_t>(a.q[k], a.ldq[k], m, c) =
           b == kCkptNanByte ? (int8_t)0 : (int8_t)ckpt8_q(held, ckpt8_inv_step(b));
     }
-    if ((c & 31) == 0) a.scale[k][m * a.lds[k] + c / kCkptGroup] = (uint8_t)b;
+    if ((c & 31) == 0) *at<uint8_t>(a.scale[k], a.lds[k], m, c / kCkptGroup) = (uint8_t)b;
   }
 }
 
@@ -47,7 +59,7 @@ __device__ __forceinline__ void glu_out(const GluArgs& a, long long m, int c, bo
   keep<T>(a, 0, m, c, ok, g);
   keep<T>(a, 1, m, c, ok, u);
   const float y = act_value_of<sizeof(T) == 4, ACT>(g, a.slope) * u;
-  if (ok) from_f32(y, static_cast<T*>(a.y)[m * a.ldy + c]);
+  if (ok) from_f32(y, *at<T>(a.y, a.ldy, m, c));
 }
 
 __device__ __forceinline__ float bias_of(const float* b, int c, bool ok) {
@@ -56,25 +68,25 @@ __device__ __forceinline__ float bias_of(const float* b, int c, bool ok) {
 
 // ------------------------------------------------------------ epilogue passes
 
-// Sums of element rows m0 .. m0 + kRowsAhead - 1 over the planes in order, four
-// of all rows at a time in flight.
-__device__ __forceinline__ void add_planes(const GluArgs& a, const float* p, long long plane,
-                                           int rows, bool ok, float (&v)[kRowsAhead]) {
+// Sums of rows m0 .. m0 + rows - 1 at column c over the planes in order, four
+// planes of all rows in flight.  (Planes have whole 32-column pieces, so lanes
+// past the last column read as well.)
+__device__ __forceinline__ void add_planes(const float* p, long long plane, int splits, int ldp,
+                                           int rows, float (&v)[kRowsAhead]) {
 #pragma unroll
   for (int k = 0; k < kRowsAhead; ++k) v[k] = 0.f;
 #pragma unroll 1
-  for (int s = 0; s < a.splits; s += 4) {
-    float q[kRowsAhead][4];
+  for (int s = 0; s < splits; s += 4, p += 4 * plane) {
+    float q[4][kRowsAhead];
 #pragma unroll
-    for (int k = 0; k < kRowsAhead; ++k)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        q[k][j] = ok && k < rows && s + j < a.splits ? __ldcs(p + (s + j) * plane + k * a.ldp)
-                                                     : 0.f;
+      for (int k = 0; k < kRowsAhead; ++k)
+        q[j][k] = s + j < splits && k < rows ? __ldcs(p + j * plane + k * ldp) : 0.f;
 #pragma unroll
-    for (int k = 0; k < kRowsAhead; ++k)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[k] += q[k][j];
+      for (int k = 0; k < kRowsAhead; ++k) v[k] += q[j][k];
   }
 }
 
@@ -94,8 +106,8 @@ __global__ void __launch_bounds__(kThreads) glu_finish_fwd_kernel(const GluArgs 
   const float bg = bias_of(a.bias[0], c, ok), bu = bias_of(a.bias[1], c, ok);
   float g[kRowsAhead], u[kRowsAhead];
   const float* p = a.partial + m0 * a.ldp + c;
-  add_planes(a, p, plane, rows, ok, g);
-  add_planes(a, p + a.splits * plane, plane, rows, ok, u);
+  add_planes(p, plane, a.splits, (int)a.ldp, rows, g);
+  add_planes(p + a.splits * plane, plane, a.splits, (int)a.ldp, rows, u);
   with_act(a.act, [&](auto tag) {
 #pragma unroll
     for (int k = 0; k < kRowsAhead; ++k)
@@ -122,9 +134,9 @@ __global__ void __launch_bounds__(kThreads) glu_finish_bwd_kernel(const GluArgs 
   auto saved = [&](int k, long long m, bool in) {
     if (!in) return 0.f;
     if (a.q[k])
-      return (float)a.q[k][m * a.ldq[k] + c] *
-             ckpt8_step(a.scale[k][m * a.lds[k] + c / kCkptGroup]);
-    return to_f32(static_cast<const T*>(a.in[k])[m * a.ld_in[k] + c]);
+      return (float)*at<int8_t>(a.q[k], a.ldq[k], m, c) *
+             ckpt8_step(*at<uint8_t>(a.scale[k], a.lds[k], m, c / kCkptGroup));
+    return to_f32(*at<T>(a.in[k], a.ld_in[k], m, c));
   };
   with_act(a.act, [&](auto tag) {
     for (long long m0 = rb * a.part_rows; m0 < m_end; m0 += kRowsAhead) {
@@ -135,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) glu_finish_bwd_kernel(const GluArgs 
         g[k] = saved(0, m0 + k, ok && k < rows);
         u[k] = saved(1, m0 + k, ok && k < rows);
       }
-      add_planes(a, a.partial + m0 * a.ldp + c, plane, rows, ok, da);
+      add_planes(a.partial + m0 * a.ldp + c, plane, a.splits, (int)a.ldp, rows, da);
 #pragma unroll
       for (int k = 0; k < kRowsAhead; ++k) {
         if (k >= rows) break;  // warp-uniform
@@ -146,9 +158,9 @@ __global__ void __launch_bounds__(kThreads) glu_finish_bwd_kernel(const GluArgs 
         s0 += dg;
         s1 += du;
         if (ok) {
-          from_f32(dg, static_cast<T*>(a.o[0])[m * a.ldo[0] + c]);
-          from_f32(du, static_cast<T*>(a.o[1])[m * a.ldo[1] + c]);
-          if (a.y) from_f32(f * u[k], static_cast<T*>(a.y)[m * a.ldy + c]);
+          from_f32(dg, *at<T>(a.o[0], a.ldo[0], m, c));
+          from_f32(du, *at<T>(a.o[1], a.ldo[1], m, c));
+          if (a.y) from_f32(f * u[k], *at<T>(a.y, a.ldy, m, c));
         }
       }
     }
