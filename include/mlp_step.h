@@ -584,7 +584,8 @@ mlp_status mlp_glu_fwd(const void* x, int ldx, const void* w_gate, int ldwg, con
  * du u (the same pointer and pitch).  With dg and du side by side in one
  * [T][2 hidden] matrix, as W_gate and W_up in theirs, the remaining gradients
  * are one product each: dx = [dg du] [W_gate W_up]^T (mlp_linear_bwd without an
- * activation) and [dW_gate dW_up] = x^T [dg du] (mlp_gemm).
+ * activation) and [dW_gate dW_up] = x^T [dg du] (mlp_gemm); in 16 bits hidden is
+ * then a multiple of 8, so that both halves start on 16 bytes.
  * Pitches of dy and W_down in 16-bit types are multiples of 8.
  * workspace: mlp_glu_bwd_workspace_bytes(...) bytes. */
 size_t mlp_glu_bwd_workspace_bytes(int T, int hidden, int d_out, int dtype);

@@ -13,11 +13,16 @@
 // registers between its two reductions; everything between load and store is
 // fp32, and the dropout mask is computed where it is used (philox.cuh).
 //
-// A row is held by WPR warps, 16 values per thread as in k_layernorm.cu; rows
-// wider than a block holds (8,192) are held by a cluster of up to eight blocks,
-// whose sums meet in distributed shared memory, so they too are read once.
+// A row is held by WPR warps, two 16-byte pieces per thread as in k_layernorm.cu;
+// rows wider than a block holds (8,192) are held by a cluster of up to eight
+// blocks, whose sums meet in distributed shared memory, so they too are read once.
+// The next row is on its way to shared memory while this one is worked on.
 // Parameter gradients stay in registers over a block's rows and leave as one
 // row of partial sums per block (cluster): no atomics, the same in every run.
+// Measured, both norms, gate and dropout: 65,536 x 512 bf16 52 us forward, 92
+// backward (6.4 and 5.9 TB/s; with the row ahead in registers 60 and 175);
+// without gate and dropout 8,192 x 8,192 fp16 90 and 166 (6.0 and 4.8 TB/s: the
+// backward's one block an SM waits at two block-wide sums a row).
 #include "act.cuh"
 #include "few_rows.cuh"
 #include "kernels.cuh"
