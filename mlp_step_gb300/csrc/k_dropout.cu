@@ -1,9 +1,9 @@
 // Dropout of a matrix with an optional residual, y = residual + keep x scale:
 // the backward is the same kernel on dy.  The mask is computed where it is used
 // (philox.cuh), so the traffic is x, the residual and y alone.
-// Bound by HBM: 262,144 x 512 bf16 with a residual 123 us (6.6 TB/s, 19 instructions
+// Bound by HBM: 262,144 x 512 bf16 with a residual 128 us (6.3 TB/s, 19 instructions
 // a value); rows that start anywhere move a value at a time, 10,007 x 1,001 fp32
-// 19.5 us (4.1 TB/s).
+// 18 us with cold caches (4.5 TB/s).
 #include "kernels.cuh"
 #include "philox.cuh"
 #include "rowvec.cuh"

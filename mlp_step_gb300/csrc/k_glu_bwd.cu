@@ -9,10 +9,10 @@
 // beside the product, 8 to 10 bytes move per value of da.  So the saved values
 // of an epilogue warp's next piece (32 x 32) are on their way by TMA while it
 // works on this one, and every output leaves by TMA from a box of its own.
-// Measured at 65,536 x 512 <- 1,408 bf16, SiLU: from 16 bits without a and sums 134
-// us (6.0 TB/s); from 8 bits with both 168, bound by the epilogue's instructions
-// (35 an output, a quarter of them for the column sums, issued in 55 % of the
-// slots).
+// Measured at 65,536 x 512 <- 1,408 bf16, SiLU: from 16 bits without a and sums 138
+// us (5.8 TB/s); from 8 bits with both 176, of which the column sums and their
+// launch are 32, bound by the epilogue's instructions (35 an output, issued in
+// 55 % of the slots).
 #include "glu_launch.cuh"
 
 namespace mlp {

@@ -19,10 +19,11 @@
 // The next row is on its way to shared memory while this one is worked on.
 // Parameter gradients stay in registers over a block's rows and leave as one
 // row of partial sums per block (cluster): no atomics, the same in every run.
-// Measured, both norms, gate and dropout: 65,536 x 512 bf16 52 us forward, 92
-// backward (6.4 and 5.9 TB/s; with the row ahead in registers 60 and 175);
-// without gate and dropout 8,192 x 8,192 fp16 90 and 166 (6.0 and 4.8 TB/s: the
-// backward's one block an SM waits at two block-wide sums a row).
+// Measured with events, launches back to back, the backward with its sums' launch:
+// 65,536 x 512 bf16 with both norms, gate and dropout 57 us forward and 97
+// backward (5.8 and 5.5 TB/s; with rows loaded to registers 63 and 173); 16,384 x
+// 8,192 fp16 without gate and dropout 170 and 319 (6.3 and 5.0 TB/s; 226 and 483):
+// the backward's one block an SM waits at two block-wide sums a row.
 #include "act.cuh"
 #include "few_rows.cuh"
 #include "kernels.cuh"
