@@ -599,7 +599,7 @@ mlp_status mlp_glu_bwd(const void* dy, int lddy, const void* w_down, int ldw, in
 
 /* ---------------------------------------------------------------- dropout
  * y = residual + keep x / (1 - p) (residual nullable), all [T][d] of dtype F32,
- * BF16 or F16; y may be x or residual.  The mask is never stored: whether value
+ * BF16 or F16; y may be x or residual (the same pointer and pitch).  The mask is never stored: whether value
  * (row t, column c) is kept follows from its place by the counter-based generator
  * Philox4x32-10, whose counter is (c / 8, t, site, step) and whose key is the
  * seed; the four words are eight 16-bit numbers r for eight neighbouring
@@ -631,7 +631,8 @@ mlp_status mlp_dropout(const void* x, int ldx, const void* residual, int ldr, in
  * NULL, and nothing that belongs to b.  b_rstd_out and h_rstd_out: fp32 [T]
  * (nullable), rb and rh for the backward pass.  n is computed from the unrounded
  * h.  All matrices have the type dtype (F32, BF16 or F16); statistics and
- * arithmetic are fp32.  h may be x or b.  1 <= d <= 65536.
+ * arithmetic are fp32.  h may be x or b (the same pointer and pitch).
+ * 1 <= d <= 65536.
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
 mlp_status mlp_resnorm_fwd(const void* x, int ldx, const void* b, int ldb, int dtype,
                            int post_norm, const float* post_gain, const void* gate, int ldgate,

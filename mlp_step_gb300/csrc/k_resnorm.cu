@@ -154,7 +154,7 @@ struct Ring {
 };
 
 // Piece of n values at p into its place: asynchronously in 16 bytes, for fp32 rows
-// that start anywhere in 4 (10,007 x 1,001 fp32 forward 99 us with loads and
+// that start anywhere in 4 (10,007 x 1,001 fp32 forward 66 us, 99 with loads and
 // stores of the thread's own), else by the thread.
 template <typename T, bool FULL>
 __device__ __forceinline__ void issue_piece(uint4* place, const T* p, int n, bool vec) {
