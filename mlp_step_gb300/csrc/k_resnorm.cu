@@ -24,6 +24,8 @@
 // backward (5.8 and 5.5 TB/s; with rows loaded to registers 63 and 173); 16,384 x
 // 8,192 fp16 without gate and dropout 170 and 319 (6.3 and 5.0 TB/s; 226 and 483):
 // the backward's one block an SM waits at two block-wide sums a row.
+#include <cfloat>
+
 #include "act.cuh"
 #include "few_rows.cuh"
 #include "kernels.cuh"
@@ -112,8 +114,10 @@ struct RowSum {
 };
 
 // The logistic function s of two values, and what s' is s times: 1 - s =
-// e^(-z) s, which keeps its precision where s is near 1 (e^(-z) held to a finite
-// value, where s makes the product 0).  The accurate functions for fp32 rows.
+// e^(-z) s, which keeps its precision where s is near 1 and is 1 where s is tiny,
+// as far as s is not 0: it reads as 0 once e^(-z) is past 2^126 (z below -87.3).
+// An infinite e^(-z) is held to the largest finite value, which s makes 0.  The
+// accurate functions for fp32 rows.
 template <typename T>
 __device__ __forceinline__ F2 logistic2(F2 z, F2& one_minus) {
   F2 e, s;
@@ -126,7 +130,7 @@ __device__ __forceinline__ F2 logistic2(F2 z, F2& one_minus) {
     const F2 d = add2(e, f2(1.f));
     s = f2(rcp_fast(d.x), rcp_fast(d.y));
   }
-  one_minus = mul2(f2(fminf(e.x, 5e34f), fminf(e.y, 5e34f)), s);
+  one_minus = mul2(f2(fminf(e.x, FLT_MAX), fminf(e.y, FLT_MAX)), s);
   return s;
 }
 
