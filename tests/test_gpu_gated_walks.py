@@ -10,6 +10,7 @@ import torch
 import mlp_step_gb300 as M
 import test_gpu_glu as glu
 import test_gpu_resnorm as rn
+import test_gpu_sublayer as sublayer
 from philox import factor, keep_mask
 from test_gpu_ffn import (ACTS, BF16, F16, F32, SLOPE, U24, Guarded, ckpt_values, near, new_ckpt,
                           rnd, rounding, vec)
@@ -237,3 +238,58 @@ def test_every_activation_in_every_form(T, k, n, act, dtype):
                     for got, r, e in ((db[0], rdg, edg), (db[1], rdu, edu)):
                         near(got, r.sum(0), e.sum(0) + (T + 8) * U24 * r.abs().sum(0), "db")
                 assert dg.intact() and du.intact() and a.intact()
+
+
+# ------------------------------------------------------------ a training step
+
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("T,d,hidden", [(1, 64, 96), (77, 128, 232), (3000, 512, 1376)])
+def test_training_step_call_by_call(T, d, hidden, dtype, ckpt):
+    """Every output of a step against the 64-bit formula of what the calls before
+    it left, to the roundings of its own call."""
+    s = sublayer.Sublayer(T, d, hidden, dtype, ckpt)
+    s.forward()
+    s.backward()
+    o, gain = s.out, s.gains
+    norm, both = rn.FORMS[6], dict(rn.FORMS[0], p=sublayer.P)
+    seed, step = s.rng.tolist()
+    k = factor(T, d, sublayer.P, seed, step, sublayer.SITE)
+
+    def check(name, ref, err, got=None):
+        got = o[name] if got is None else got
+        near(got, ref, rounding(got.dtype, ref) + err + 1e-30, name)
+
+    # forward
+    ref = rn.forward_ref(dict(x=s.x, ng=gain[0]), norm, 1.0, None)
+    check("n0", *ref["n"])
+    check("r0", *ref["h_rstd"])
+    rg, eg, ru, eu, ry, ey = glu.forward_ref(o["n0"], *s.halves(s.w), None, None, "silu")
+    check("y", ry, ey)
+    if not ckpt:
+        check("g", rg, eg, s.kept[0])
+        check("u", ru, eu, s.kept[1])
+    check("b", *glu.product(o["y"], s.wd))
+    m = dict(x=s.x, b=o["b"], z=s.z, pg=gain[1], ng=gain[2])
+    ref = rn.forward_ref(m, both, sublayer.SCALE, k)
+    for name, key in (("h", "h"), ("n1", "n"), ("rb", "b_rstd"), ("rh", "h_rstd")):
+        check(name, *ref[key])
+    # backward
+    m.update(x=o["h"], dh=s.dh, dn=s.dn)
+    ref = rn.backward_ref(m, both, sublayer.SCALE, k, True, dict(h=o["rh"], b=o["rb"]))
+    for name, key in (("dx1", "dx"), ("db", "db"), ("dz", "dz"), ("dpost", "dpost"),
+                      ("dnext", "dnext")):
+        check(name, *ref[key])
+    g, u = (ckpt_values(*v) if ckpt else v.double() for v in s.kept)
+    rdg, edg, rdu, edu, ra, ea = glu.backward_ref(o["db"], s.wd, g, u, "silu")
+    dg, du = s.halves(o["dgu"])
+    check("dg", rdg, edg, dg)
+    check("du", rdu, edu, du)
+    check("a", ra, ea)
+    check("dwd", *glu.product(o["a"].t(), o["db"]))
+    check("dn0", *glu.product(o["dgu"], s.w.t()))
+    check("dw", *glu.product(o["n0"].t(), o["dgu"]))
+    ref = rn.backward_ref(dict(x=s.x, dh=o["dx1"], dn=o["dn0"], ng=gain[0]), norm, 1.0, None, True,
+                          dict(h=o["r0"]))
+    check("dx", *ref["dx"])
+    check("dgain0", *ref["dnext"])
