@@ -506,8 +506,10 @@ mlp_status mlp_stack_train_step_ckpt8(int n_blocks, int T, int d, int hidden, fl
  * Activations are good to 5e-5 of f and of the two terms of f' where those are
  * tiny (near 1e-36), 1e-5 at 1e-4 and a few 2^-23 near and above 0; magnitudes
  * below 2^-118 may read as 0.
- * The tensor cores' fp32 accumulation truncates: sums are low by about 1e-9 of
- * their size per unit of d_in (1e-5 at d_in = 8,192), below the rounding of
+ * The tensor cores' fp32 accumulation truncates, so sums are low by a share of
+ * their size that grows with d_in: measured per unit of it 0.7e-9 to 2.5e-9 where
+ * terms are of mixed sign or few, up to 6.5e-9 for many terms of one sign (at
+ * d_in = 8,192 1e-5 and 5.3e-5; less where d_in is split), below the rounding of
  * 16-bit outputs.
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
 size_t mlp_linear_workspace_bytes(int T, int d_in, int d_out, int dtype);
@@ -584,8 +586,9 @@ mlp_status mlp_glu_fwd(const void* x, int ldx, const void* w_gate, int ldwg, con
  * du u (the same pointer and pitch).  With dg and du side by side in one
  * [T][2 hidden] matrix, as W_gate and W_up in theirs, the remaining gradients
  * are one product each: dx = [dg du] [W_gate W_up]^T (mlp_linear_bwd without an
- * activation) and [dW_gate dW_up] = x^T [dg du] (mlp_gemm); in 16 bits hidden is
- * then a multiple of 8, so that both halves start on 16 bytes.
+ * activation) and [dW_gate dW_up] = x^T [dg du] (mlp_gemm); hidden is then a
+ * multiple of 8 in 16-bit types, of 4 in F32, so that both halves start on 16
+ * bytes.
  * Pitches of dy and W_down in 16-bit types are multiples of 8.
  * workspace: mlp_glu_bwd_workspace_bytes(...) bytes. */
 size_t mlp_glu_bwd_workspace_bytes(int T, int hidden, int d_out, int dtype);
@@ -631,7 +634,9 @@ mlp_status mlp_dropout(const void* x, int ldx, const void* residual, int ldr, in
  * NULL, and nothing that belongs to b.  b_rstd_out and h_rstd_out: fp32 [T]
  * (nullable), rb and rh for the backward pass.  n is computed from the unrounded
  * h.  All matrices have the type dtype (F32, BF16 or F16); statistics and
- * arithmetic are fp32.  h may be x or b (the same pointer and pitch).
+ * arithmetic are fp32.  The logistic function s of a gate z and its derivative
+ * s (1 - s) are good to (8 |z| + 40) 2^-24 of themselves, and may read as 0 where s
+ * is below 2^-126.  h may be x or b (the same pointer and pitch).
  * 1 <= d <= 65536.
  * Errors: INVALID_ARG, MISALIGNED, UNSUPPORTED_SHAPE. */
 mlp_status mlp_resnorm_fwd(const void* x, int ldx, const void* b, int ldb, int dtype,

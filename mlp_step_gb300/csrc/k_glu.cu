@@ -18,7 +18,8 @@
 // tile overlaps the MMAs of the next.  The body is in glu_tc.cuh.
 //
 // Bound: the MMAs for long K (4,096 x 8,192 -> 8,192 fp16 610 us = 1.80 PFLOP/s, 94 %
-// of the library's rate, with both pre-activations kept 614).  For K of a few
+// of the library's rate, with both pre-activations kept 614, in short runs; called
+// again and again, under the power cap, 714).  For K of a few
 // hundred the epilogue (65,536 x 512 -> 1,408 bf16 SiLU: 122 us = 1.55 PFLOP/s, of
 // which loads and MMAs alone take 104 and the accumulators' way to registers 5; with
 // g and u kept 149, in 8 bits 151).
@@ -67,8 +68,8 @@ GluPlan plan(long long T, int K, int N, bool bwd) {
   return best;
 }
 
-// Epilogue warps of a pair: twelve, whose 128 registers hold a unit without
-// spills (65,536 x 512 -> 1,408 bf16 SiLU with 8-bit g and u: sixteen 167 us,
+// Epilogue warps of a pair: twelve, whose 128 registers hold a unit of the forward
+// without spills (65,536 x 512 -> 1,408 bf16 SiLU with 8-bit g and u: sixteen 167 us,
 // twelve 151, eight 153; without kept values 127, 122, 120; GELU and 8-bit values
 // 174, 164, 167); eight where both are kept in 16 bits, whose boxes would take an
 // operand stage beside twelve (171, 163, 149).
@@ -78,6 +79,9 @@ mlp_status launch(const GluMaps& maps, const GluParams& p, GluTile tile, cudaStr
   if (tile == kGluPair)
     return glu_whole(p, false) ? launch_glu_pair<5, EW, H16, MODE, true>(maps, p, st)
                                : launch_glu_pair<5, EW, H16, MODE, false>(maps, p, st);
+  // Up to 32 rows a stage holds just those, and five stages fit instead of four (us
+  // with this and with whole tiles, 16 to 32 rows, cold weights: 4,096 -> 11,008 42.5
+  // and 45.4; 4,096 -> 1,361, 512 -> 1,408 and 8,192 -> 8,192 the same within 0.2).
   if (tile == kGluTall)
     return p.a_bytes <= 32 * GBK * 2 ? launch_glu_single<256, 5, 4, 32, H16, MODE>(maps, p, st)
                                      : launch_glu_single<256, 4, 4, 128, H16, MODE>(maps, p, st);

@@ -22,7 +22,9 @@ namespace {
 // 16-bit saved values take boxes twice as large as 8-bit ones: beside twelve
 // epilogue warps a ring of three operand stages, which long K feels, beside
 // eight one of four (us with twelve and eight, K = 512 194 and 210, 1,024 134
-// and 118, 1,536 224 and 198, 8,192 425 and 374).
+// and 118, 1,536 224 and 198, 8,192 425 and 374).  Registers spill a little, in
+// bytes a thread: twelve warps from 16 bits 16 (ragged pieces 20), from 8 bits none
+// (12), eight warps 4 (20), the 128-column single tile 36.
 constexpr int kShortK = 12;  // k-blocks
 
 template <int H16, int MODE>

@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kThreads) glu_finish_bwd_kernel(const GluArgs 
 // registers, sets the bytes in flight; the rows of x are in shared memory as
 // fp32.  A thread keeps 16 bytes of columns and walks down K (runs of 128 bytes
 // of either weight per 128 accumulators in 16 bits).  All CTAs of a launch are
-// resident at once.  8,192 -> 8,192 bf16, one row, back to back: 42.5 us, 6.3 TB/s;
+// resident at once up to 152 kPerSm tiles; more run on in further waves (clusters
+// do not wait for one another).  8,192 -> 8,192 bf16, one row, back to back: 42.5 us, 6.3 TB/s;
 // 512 -> 1,408 5 us from L2, 12 with cold caches.
 
 constexpr int kFewX = 4096;  // values of x staged at a time (all rows)
@@ -343,8 +344,9 @@ mlp_status few_launch(const GluArgs& a, cudaStream_t st) {
   using Shape = FewShape<MT, COLS>;
   static PerDevice configured;
   if (!allow_smem(configured, glu_few_kernel<T, MT, COLS>, Shape::kSmem)) return MLP_ERR_CUDA;
-  // the widest cluster with which all CTAs are resident (on 152 SMs) and each
-  // still has 64 of K
+  // The widest cluster with which all CTAs are resident (on 152 SMs) and each still
+  // has 64 of K; 1 where there are more tiles than places.  From the shape alone, as
+  // the order of the sums follows from it.
   const long long tiles = (a.N + COLS / 2 - 1) / (COLS / 2);
   int cluster = 8;
   while (cluster > 1 && (tiles * cluster > 152 * Shape::kPerSm || a.K < 64 * cluster)) --cluster;
@@ -398,7 +400,10 @@ mlp_status finish_launch(const GluArgs& a, bool bwd, cudaStream_t st) {
 
 }  // namespace
 
-// Up to 8 rows for fp32, whose tiled product computes 128 rows whatever T is.
+// Up to 8 rows for fp32, whose tiled product computes 128 rows whatever T is (us
+// here and there with cold weights: 784 -> 1,001, rows that start anywhere, T = 1 14.5
+// and 15.5, 4 15.6 and 16.7, 8 10.6 and 15.9; 512 -> 1,408 T = 1 6.0 and 16.6, 8 7.4
+// and 17.9; 4,096 -> 11,008 T = 1 71 and 397, 4 74 and 398, 8 148 and 399).
 // In 16 bits the tensor cores take over once the FMAs, not the reading of the
 // weights, bound this kernel: above 2 rows, 8 of small weights (us here and there
 // with cold weights, bf16: 512 -> 1,408 T = 1 9 and 13, 4 11 and 13, 8 13 and 13; 1,024

@@ -681,6 +681,14 @@ mlp_status bwd_of(const ResNorm& p, int* rows, cudaStream_t st) {
                      R::bytes(2 * !!p.n + !!p.x + !!p.b + !!p.z), cluster, p, st);
 }
 
+// kExact where it applies (us with it and with kFull, 2^25 values, 2^26 from 2,048 and
+// 2^27 from 8,192 columns on: forward bf16 512 columns 50 and 53, 1,024 51 and 55, 4,096 89
+// and 98, 8,192 169 and 185, with gate and dropout 61 and 64, 62 and 69, 119 and 136, 226
+// and 255; backward 73 and 77, 76 and 83, 170 and 178, 327 and 331).  With gate and
+// dropout its 16-bit backward spills 24 to 48 bytes a thread at two to eight warps a
+// row and is the slower one there (bf16 1,024 columns 117 and 112, 2,048 236 and 216, 4,096
+// 267 and 238, 8,192 549 and 525; fp16 113 and 110, 225 and 216, 253 and 240, but 8,192 499
+// and 538, and 512 98 and 101, 96 and 100).
 template <typename T, int WPR, bool WIDE, bool BWD>
 mlp_status of_form(const ResNorm& p, bool full, int* rows, cudaStream_t st) {
   const bool exact = full && p.d % (vpt<T>() * 32 * WPR) == 0;
